@@ -34,6 +34,7 @@
 #ifndef DEX_H_
 #define DEX_H_
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -263,6 +264,102 @@ typedef struct dex_copy_job {
  * job.  Stream-ordered, no sync.  DEX_EINVAL for a bad geometry or pointer. */
 int dex_kv_collapse(void* committed, const void* pool, const dex_kv_geom* geom,
                     const dex_copy_job* jobs, int32_t n_jobs, int32_t* rejected, void* stream);
+
+/* ---- paged K/V cache: append and shared-prefix attention --------------------------- */
+
+typedef enum dex_dtype { DEX_DT_BF16 = 0, DEX_DT_FP16 = 1, DEX_DT_FP32 = 2 } dex_dtype;
+
+/* One layer of a paged K/V cache.  A page holds page_size consecutive positions of one
+ * sequence, head-major like the committed cache: [2 (K, V)][n_kv_heads][page_size][head_dim].
+ * Position p of sequence b is row p % page_size of page table[b * table_stride + p / page_size].
+ * Pages lie page_stride elements apart, so the layers of a model can share one allocation
+ * (page_stride = n_layers * 2 * n_kv_heads * page_size * head_dim, pages offset to the layer).
+ * Several sequences may name the same page (a shared prefix).
+ * Constraints (DEX_EINVAL otherwise): head_dim 64 or 128; page_size 16, 32, 64, 128 or 256;
+ * dtype DEX_DT_BF16 or DEX_DT_FP16; pages 16-byte aligned; page_stride a multiple of 8 and at
+ * least one page; batch <= 1024; table_width * page_size < 2^31; table_stride >= table_width. */
+typedef struct dex_paged_kv {
+  void* pages;            /* device, bf16 or fp16 */
+  const int32_t* table;   /* device, int32 [batch][table_stride] page ids */
+  int64_t page_stride;    /* elements between pages */
+  int32_t n_pages, page_size, n_kv_heads, head_dim;
+  int32_t batch, table_width, table_stride, dtype;
+} dex_paged_kv;
+
+/* The tokens of one dex_paged_append call.  q (may be NULL, with q_out), k and v: device,
+ * [n_tokens][heads][head_dim] in in_dtype (the cache's type or DEX_DT_FP32), rows of one token
+ * contiguous, tokens *_stride elements apart (slices of a fused projection are fine).  q_out:
+ * device, in the cache's type; it may be q itself when in_dtype is the cache's type and the
+ * strides agree.  Every pointer 16-byte aligned, every stride a multiple of 16 bytes. */
+typedef struct dex_append_args {
+  const void *q, *k, *v;
+  void* q_out;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  const int32_t* seq;       /* device [n_tokens]: sequence, -1 for a padding token */
+  const int32_t* pos;       /* device [n_tokens]: cache position */
+  const int32_t* rope_pos;  /* device [n_tokens]: rotation position, or NULL for pos */
+  int32_t n_tokens, n_heads, in_dtype;
+  float rope_theta;         /* >= 1, or 0 to store k and q unrotated */
+} dex_append_args;
+
+/* Append n_tokens keys and values to a paged cache, rotating k (and q into q_out) on the way:
+ * the pair (x_j, x_{j + head_dim/2}) turns by rope_pos * theta^(-2j / head_dim), in fp32 with the
+ * angle reduced exactly, rounded once to the cache's type.  A token with seq -1 is skipped; one
+ * whose sequence, position or page id is out of range is skipped without any access to the cache
+ * and counted in rejected.  A skipped token's row of q_out is left as it was.  Two tokens of
+ * one call must not name the same cache row.  rejected: device int32 or NULL; when given, the
+ * call zeroes it (stream-ordered) and adds one per rejected token.  Runs on the current
+ * device; stream-ordered, no allocation, no sync, capturable.  n_tokens 0 is a no-op. */
+int dex_paged_append(const dex_paged_kv* kv, const dex_append_args* a, int32_t* rejected, void* stream);
+
+/* One dex_prefix_attention call.  The queries of sequence b are tokens q_start[b] ..
+ * q_start[b+1]-1 and stand at its last positions: query i of n at p = seq_len[b] - n + i
+ * (seq_len counts the prefix and the queries' own positions, already appended).  It sees the
+ * positions 0..p, or with tree_mask every position before seq_len[b] - n and, of the last n,
+ * position seq_len[b] - n + j where bit j of its word is set (n <= 64).  A query that sees
+ * nothing gets zeros and lse -inf.  Query head h reads K/V head h / (n_heads / n_kv_heads).
+ * prefix_len: every sequence's positions below it hold the same keys and values; they are
+ * read through prefix_table (NULL: row 0 of the cache's table), once for the whole batch. */
+typedef struct dex_attention_args {
+  const void* q;               /* device, cache's type, [n_tokens][n_heads][head_dim] */
+  void* out;                   /* device, cache's type, [n_tokens][n_heads][head_dim] */
+  float* lse;                  /* device [n_tokens][n_heads] or NULL: log of the softmax denominator */
+  int64_t q_stride, out_stride;/* elements between tokens (a multiple of 8) */
+  const int32_t* q_start;      /* device [batch + 1], non-decreasing, within 0..n_tokens */
+  const int32_t* seq_len;      /* device [batch] */
+  const int32_t* prefix_table; /* device [ceil(prefix_len / page_size)] page ids or NULL */
+  const uint64_t* tree_mask;   /* device [n_tokens] or NULL */
+  int32_t n_tokens, n_heads;
+  int32_t max_q;               /* no sequence has more queries than this (<= 64 with tree_mask) */
+  int32_t prefix_len;          /* >= 0 */
+  float scale;                 /* of the scores, usually 1 / sqrt(head_dim) */
+} dex_attention_args;
+
+/* Bits a call ORs into *status (device int32, cleared by the caller). */
+#define DEX_ATTN_BAD_PAGE 1    /* a page id in use is outside [0, n_pages) */
+#define DEX_ATTN_BAD_RANGE 2   /* a sequence's q_start or seq_len is out of range */
+#define DEX_ATTN_TIMEOUT 4     /* a bounded device wait gave up */
+
+/* Device scratch that dex_prefix_attention needs for these sizes (host call, no GPU work; reads the
+ * integer fields only).  Depends on n_tokens, n_heads, max_q, prefix_len and the cache's
+ * geometry, not on the lengths. */
+int dex_prefix_attention_workspace(const dex_paged_kv* kv, const dex_attention_args* a, size_t* bytes);
+
+/* Attention of a ragged batch of queries over a paged cache whose sequences share their first
+ * prefix_len positions.  Scores, softmax statistics and sums are fp32; the probabilities enter the
+ * second product in the cache's type.  Rows of out and lse that belong to no sequence are
+ * left as they were.  Keys and values at positions below seq_len must be finite; what pages hold
+ * beyond is never used.  A page id that is out of range is never followed: the rows that need
+ * it become NaN and status gets DEX_ATTN_BAD_PAGE.  A sequence whose seq_len is negative or beyond the
+ * table gets NaN rows, one whose queries exceed max_q or n_tokens is skipped, both with DEX_ATTN_BAD_RANGE.
+ * workspace: device, 256-byte aligned, at least the bytes dex_prefix_attention_workspace gives
+ * (DEX_ECAPACITY otherwise); calls that may overlap on the GPU need workspaces of their own.
+ * Constraints: the cache's, n_heads a multiple of n_kv_heads with at most 128 query heads per
+ * K/V head, q and out 16-byte aligned, prefix_len within the table.  Runs on the current device;
+ * stream-ordered, no allocation, no sync, capturable: lengths, tables and masks are read
+ * on the device, so a captured call can be replayed on new ones. */
+int dex_prefix_attention(const dex_paged_kv* kv, const dex_attention_args* a, void* workspace, size_t workspace_bytes,
+                         int32_t* status, void* stream);
 
 /* ---- host-only lattice scheduler (no GPU needed) ---------------------------------- */
 

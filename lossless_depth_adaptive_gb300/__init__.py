@@ -86,6 +86,29 @@ class dex_plan_node(C.Structure):
                 ("tail", C.c_int32 * 16)]
 
 
+class dex_paged_kv(C.Structure):
+    _fields_ = [("pages", C.c_void_p), ("table", C.c_void_p), ("page_stride", C.c_int64), ("n_pages", C.c_int32),
+                ("page_size", C.c_int32), ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32), ("batch", C.c_int32),
+                ("table_width", C.c_int32), ("table_stride", C.c_int32), ("dtype", C.c_int32)]
+
+
+class dex_append_args(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p), ("q_out", C.c_void_p),
+                ("q_stride", C.c_int64), ("k_stride", C.c_int64), ("v_stride", C.c_int64),
+                ("q_out_stride", C.c_int64), ("seq", C.c_void_p), ("pos", C.c_void_p), ("rope_pos", C.c_void_p),
+                ("n_tokens", C.c_int32), ("n_heads", C.c_int32), ("in_dtype", C.c_int32), ("rope_theta", C.c_float)]
+
+
+class dex_attention_args(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("out", C.c_void_p), ("lse", C.c_void_p), ("q_stride", C.c_int64),
+                ("out_stride", C.c_int64), ("q_start", C.c_void_p), ("seq_len", C.c_void_p),
+                ("prefix_table", C.c_void_p), ("tree_mask", C.c_void_p), ("n_tokens", C.c_int32),
+                ("n_heads", C.c_int32), ("max_q", C.c_int32), ("prefix_len", C.c_int32), ("scale", C.c_float)]
+
+
+DEX_DT_BF16, DEX_DT_FP16, DEX_DT_FP32 = 0, 1, 2
+DEX_ATTN_BAD_PAGE, DEX_ATTN_BAD_RANGE, DEX_ATTN_TIMEOUT = 1, 2, 4
+
 P = C.c_void_p
 I32P = C.POINTER(C.c_int32)
 # name -> (restype, argtypes): every symbol of include/dex.h
@@ -109,6 +132,11 @@ SIGNATURES = {
     "dex_exit_head_decs_noalloc": (C.c_int, [P, C.c_int32, C.c_int32, P, C.c_float, P, C.c_int32, P, P,
                                              C.c_int32, C.c_float, C.c_uint64, P, P, P]),
     "dex_kv_collapse": (C.c_int, [P, P, C.POINTER(dex_kv_geom), P, C.c_int32, P, P]),
+    "dex_paged_append": (C.c_int, [C.POINTER(dex_paged_kv), C.POINTER(dex_append_args), P, P]),
+    "dex_prefix_attention_workspace": (C.c_int, [C.POINTER(dex_paged_kv), C.POINTER(dex_attention_args),
+                                                 C.POINTER(C.c_size_t)]),
+    "dex_prefix_attention": (C.c_int, [C.POINTER(dex_paged_kv), C.POINTER(dex_attention_args), P, C.c_size_t, P,
+                                       P]),
     "dex_lattice_new": (C.c_int, [I32P, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.POINTER(P)]),
     "dex_lattice_start": (C.c_int, [P, C.c_int32, C.c_int32, C.c_int32]),
     "dex_lattice_plan": (C.c_int, [P, C.POINTER(dex_plan_node), C.c_int32, I32P]),
@@ -146,6 +174,11 @@ def check(code: int, where: str) -> int:
     if code != DEX_OK:
         raise DexError(code, where)
     return code
+
+
+def _need(ok: bool, message: str) -> None:
+    if not ok:
+        raise DexError(DEX_EINVAL, message)
 
 
 def i32(values: Sequence[int]):
@@ -251,6 +284,26 @@ def dex_kv_collapse(committed_ptr: int, pool_ptr: int, geom: dex_kv_geom, jobs_p
                                 P(rejected_ptr or None), P(stream)), "dex_kv_collapse")
 
 
+def dex_paged_append(kv: dex_paged_kv, args: dex_append_args, rejected_ptr: int = 0, stream: int = 0) -> None:
+    """rejected_ptr: device int32 that receives the number of out-of-range tokens skipped (or 0)."""
+    check(lib().dex_paged_append(C.byref(kv), C.byref(args), P(rejected_ptr or None), P(stream)), "dex_paged_append")
+
+
+def dex_prefix_attention_workspace(kv: dex_paged_kv, args: dex_attention_args) -> int:
+    """Bytes of device scratch dex_prefix_attention needs (reads the integer fields only)."""
+    n = C.c_size_t()
+    check(lib().dex_prefix_attention_workspace(C.byref(kv), C.byref(args), C.byref(n)),
+          "dex_prefix_attention_workspace")
+    return n.value
+
+
+def dex_prefix_attention(kv: dex_paged_kv, args: dex_attention_args, workspace_ptr: int, workspace_bytes: int,
+                         status_ptr: int = 0, stream: int = 0) -> None:
+    """status_ptr: device int32 into which the call ORs DEX_ATTN_* bits (or 0)."""
+    check(lib().dex_prefix_attention(C.byref(kv), C.byref(args), P(workspace_ptr or None), workspace_bytes,
+                                     P(status_ptr or None), P(stream)), "dex_prefix_attention")
+
+
 # ---- model marshalling (PyTorch tensors -> dex_model) -------------------------------------------
 
 class ModelRef:
@@ -337,6 +390,148 @@ class Decoder:
             self.close()
         except Exception:
             pass
+
+
+class PagedCache:
+    """One layer of a paged K/V cache: append with rotary positions, shared-prefix attention.
+
+    ``pages``: [n_pages, 2 (K, V), kv_heads, page_size, head_dim] bf16 or fp16, contiguous within a
+    page (a slice of a larger allocation is fine, so the layers of a model can share one).
+    ``table``: int32 [batch, width] page ids; position p of sequence b is row ``p % page_size`` of page
+    ``table[b, p // page_size]``.  Both stay the caller's and may be changed in place between calls.
+
+    Calls run on the pages' device and its current stream, never synchronise and can be captured into
+    a CUDA graph.  A bad argument raises DexError before anything is launched; the device-side checks
+    of ``dex_paged_append`` and ``dex_prefix_attention`` (include/dex.h) report through ``rejected`` and
+    ``status``.
+    """
+
+    def __init__(self, pages, table):
+        import torch
+        self._torch = torch
+        self._code = {torch.bfloat16: DEX_DT_BF16, torch.float16: DEX_DT_FP16}
+        _need(pages.dim() == 5 and pages.shape[1] == 2, "pages must be [n_pages, 2, kv_heads, page_size, head_dim]")
+        n, _, kvh, ps, hd = pages.shape
+        _need(pages.dtype in self._code, "pages must be bf16 or fp16")
+        _need(n > 0 and pages.stride()[1:] == (kvh * ps * hd, ps * hd, hd, 1), "each page must be contiguous")
+        _need(table.dim() == 2 and table.dtype == torch.int32 and table.stride(1) == 1 and table.shape[0] > 0,
+              "table must be int32 [batch, width], contiguous rows")
+        self.pages, self.table, self.device = pages, table, pages.device
+        page_stride = pages.stride(0) if n > 1 else 2 * kvh * ps * hd
+        table_stride = table.stride(0) if table.shape[0] > 1 else table.shape[1]
+        self.kv = dex_paged_kv(pages.data_ptr(), table.data_ptr(), page_stride, n, ps, kvh, hd, table.shape[0],
+                               table.shape[1], table_stride, self._code[pages.dtype])
+        self.kv_heads, self.head_dim = kvh, hd
+        # the geometry checks of the library, which look at the sizes alone
+        dex_prefix_attention_workspace(self.kv, dex_attention_args(n_heads=kvh, max_q=1, scale=1.0))
+        self._on_device(table=table)
+
+    def _on_device(self, **tensors):
+        for name, t in tensors.items():
+            _need(t is None or (t.is_cuda and t.device == self.device), f"{name} must be on the pages' CUDA device")
+
+    def _rows(self, name, t, heads, n=None):
+        """[n, heads, head_dim] with the rows of a token contiguous; the stride between tokens."""
+        hd = self.head_dim
+        _need(t.dim() == 3 and t.shape[2] == hd and (heads is None or t.shape[1] == heads) and
+              (n is None or t.shape[0] == n) and t.stride(2) == 1 and (t.stride(1) == hd or t.shape[1] == 1),
+              f"{name} must be [tokens{'' if n is None else f' = {n}'}, {heads or 'heads'}, {hd}] with contiguous heads")
+        return t.stride(0) if t.shape[0] > 1 else t.shape[1] * hd
+
+    def _index(self, name, t, n, dtype=None):
+        _need(t.dim() == 1 and t.shape[0] == n and t.is_contiguous() and t.dtype == (dtype or self._torch.int32),
+              f"{name} must be a contiguous {dtype or self._torch.int32} vector of {n}")
+        return t.data_ptr()
+
+    def _run(self, fn, *args):
+        with self._torch.cuda.device(self.device):
+            fn(*args, self._torch.cuda.current_stream().cuda_stream)
+
+    def append(self, k, v, seq, pos, q=None, q_out=None, theta: float = 10000.0, rope_pos=None, rejected=None):
+        """Store k (rotated) and v of token t at position pos[t] of sequence seq[t]; return q rotated.
+
+        k, v: [tokens, kv_heads, head_dim], q: [tokens, heads, head_dim] or None, in the cache's type or
+        fp32 (slices of a fused projection are fine).  seq, pos, rope_pos: int32 [tokens]; seq -1 skips a
+        token, rope_pos (default: pos) is the rotation position.  theta 0 stores k unrotated.  q_out:
+        [tokens, heads, head_dim] in the cache's type, allocated when not given; it may be q itself.
+        rejected: int32 [1], receives the number of tokens out of range, which are skipped.
+        """
+        torch = self._torch
+        n = k.shape[0]
+        _need(k.dtype == v.dtype and (k.dtype == self.pages.dtype or k.dtype == torch.float32),
+              "k and v must have the cache's type or fp32")
+        a = dex_append_args(k=k.data_ptr(), v=v.data_ptr(), k_stride=self._rows("k", k, self.kv_heads),
+                            v_stride=self._rows("v", v, self.kv_heads, n), seq=self._index("seq", seq, n),
+                            pos=self._index("pos", pos, n), n_tokens=n, rope_theta=theta,
+                            in_dtype=DEX_DT_FP32 if k.dtype == torch.float32 else self.kv.dtype)
+        if rope_pos is not None:
+            a.rope_pos = self._index("rope_pos", rope_pos, n)
+        _need(q is not None or q_out is None, "q_out needs q")
+        if q is not None:
+            a.q_stride = self._rows("q", q, None, n)
+            _need(q.dtype == k.dtype, "q must have the type of k")
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=self.pages.dtype, device=q.device)
+            a.q_out_stride = self._rows("q_out", q_out, q.shape[1], n)
+            _need(q_out.dtype == self.pages.dtype, "q_out must have the cache's type")
+            a.q, a.q_out, a.n_heads = q.data_ptr(), q_out.data_ptr(), q.shape[1]
+        if rejected is not None:
+            self._index("rejected", rejected, 1)
+        self._on_device(k=k, v=v, q=q, q_out=q_out, seq=seq, pos=pos, rope_pos=rope_pos, rejected=rejected)
+        self._run(dex_paged_append, self.kv, a, 0 if rejected is None else rejected.data_ptr())
+        return q_out
+
+    def attention_workspace(self, q, max_q: int, prefix_len: int = 0):
+        """A scratch tensor for attention() calls of these sizes (any lengths); calls that may overlap
+        on the GPU need one each."""
+        a = dex_attention_args(n_tokens=q.shape[0], n_heads=q.shape[1], max_q=max_q, prefix_len=prefix_len, scale=1.0)
+        return self._torch.empty(max(1, dex_prefix_attention_workspace(self.kv, a)), dtype=self._torch.uint8,
+                                 device=self.device)
+
+    def attention(self, q, q_start, seq_len, max_q: int, prefix_len: int = 0, prefix_table=None, tree_mask=None,
+                  scale: Optional[float] = None, out=None, lse=None, workspace=None, status=None):
+        """Attention of q over the cache; returns out ([tokens, heads, head_dim], the cache's type).
+
+        The queries of sequence b are tokens q_start[b] .. q_start[b+1]-1 (int32 [batch + 1], at most max_q
+        each) and stand at its last positions; seq_len (int32 [batch]) counts them.  Query i of n sees
+        positions 0 .. seq_len - n + i, or with tree_mask (int64 [tokens]) everything before the last n and
+        of those the ones whose bit is set.  Positions below prefix_len are read through prefix_table (int32;
+        default: row 0 of the table), once for the batch.  scale defaults to head_dim**-0.5.  lse: fp32
+        [tokens, heads], receives the log of the softmax denominator.  workspace: from
+        attention_workspace(), allocated when not given.  status: int32 [1], receives DEX_ATTN_* bits.
+        Rows of out and lse that belong to no sequence are left as they were.
+        """
+        torch = self._torch
+        n, batch = q.shape[0], self.kv.batch
+        _need(0 <= prefix_len < 2 ** 31 and 0 < max_q < 2 ** 31, "prefix_len or max_q out of range")
+        a = dex_attention_args(q=q.data_ptr(), q_stride=self._rows("q", q, None), n_tokens=n, n_heads=q.shape[1],
+                               q_start=self._index("q_start", q_start, batch + 1),
+                               seq_len=self._index("seq_len", seq_len, batch), max_q=max_q, prefix_len=prefix_len,
+                               scale=self.head_dim ** -0.5 if scale is None else scale)
+        _need(q.dtype == self.pages.dtype, "q must have the cache's type")
+        if out is None:
+            out = torch.empty((n, q.shape[1], self.head_dim), dtype=q.dtype, device=q.device)
+        _need(out.dtype == q.dtype, "out must have the cache's type")
+        a.out, a.out_stride = out.data_ptr(), self._rows("out", out, q.shape[1], n)
+        if prefix_table is not None:
+            a.prefix_table = self._index("prefix_table", prefix_table, prefix_table.numel())
+            _need(prefix_table.numel() * self.kv.page_size >= prefix_len, "prefix_table is shorter than prefix_len")
+        if tree_mask is not None:
+            a.tree_mask = self._index("tree_mask", tree_mask, n, torch.int64)
+        if lse is not None:
+            _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == q.shape[:2],
+                  "lse must be contiguous fp32 [tokens, heads]")
+            a.lse = lse.data_ptr()
+        if status is not None:
+            self._index("status", status, 1)
+        if workspace is None:
+            workspace = self.attention_workspace(q, max_q, prefix_len)
+        _need(workspace.is_contiguous(), "workspace must be contiguous")
+        self._on_device(q=q, out=out, q_start=q_start, seq_len=seq_len, prefix_table=prefix_table,
+                        tree_mask=tree_mask, lse=lse, workspace=workspace, status=status)
+        self._run(dex_prefix_attention, self.kv, a, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                  0 if status is None else status.data_ptr())
+        return out
 
 
 class Lattice:

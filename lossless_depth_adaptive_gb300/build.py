@@ -20,7 +20,7 @@ LIB = os.path.join(OUT, "libdex.so")
 CUDA_HOME = os.environ.get("CUDA_HOME", "/usr/local/cuda")
 NVCC = os.path.join(CUDA_HOME, "bin", "nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-CU_SOURCES = ["gemm.cu", "attention.cu", "misc.cu", "dex_api.cu"]
+CU_SOURCES = ["gemm.cu", "attention.cu", "misc.cu", "dex_api.cu", "paged.cu", "prefix_attention.cu"]
 CXX_SOURCES = ["lattice.cpp"]
 
 

@@ -272,4 +272,45 @@ cudaError_t launch_decode_best(const unsigned long long* best, int n, const int3
 // the kernels' DevNode rows.
 cudaError_t launch_exit_nodes(const void* exit_nodes, int n, DevNode* out, cudaStream_t st);
 
+// ---- paged cache --------------------------------------------------------------------------
+// One layer of a paged K/V cache as the kernels see it: pages of [2][KVH][page][hd] elements,
+// page_stride elements apart; position p of sequence b is row p % page of page
+// table[b * table_stride + p / page] (page = 1 << page_shift).
+struct PagedKv {
+  void* pages;
+  const int32_t* table;
+  int64_t page_stride;
+  int32_t n_pages, page_shift, KVH, hd;
+  int32_t batch, table_width, table_stride, fp16;   // fp16: 1 for fp16, 0 for bf16
+};
+
+struct AppendArgs {
+  PagedKv kv;
+  const void *q, *k, *v;
+  void* q_out;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  const int32_t *seq, *pos, *rope_pos;
+  int32_t n_tokens, H, in_fp32, rotate;
+  int32_t* rejected;
+  // the angle of pair j at position 1, in units of 2^-64 of a turn
+  uint64_t turn[64];
+};
+cudaError_t launch_paged_append(const AppendArgs& a, cudaStream_t st);
+
+struct PrefixAttnArgs {
+  PagedKv kv;
+  const void* q;
+  void* out;
+  float* lse;
+  int64_t q_stride, out_stride;
+  const int32_t *q_start, *seq_len, *prefix_table;
+  const uint64_t* tree;
+  int32_t n_tokens, H, G, max_q, prefix_len;   // G = H / KVH
+  float scale_log2;                            // log2(e) * scale
+  int32_t* status;
+};
+// Bytes of device scratch a call of these sizes needs (host, sizes only).
+size_t prefix_attention_workspace(const PrefixAttnArgs& a);
+cudaError_t launch_prefix_attention(const PrefixAttnArgs& a, void* workspace, cudaStream_t st);
+
 }  // namespace dex

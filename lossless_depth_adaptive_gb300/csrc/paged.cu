@@ -1,0 +1,273 @@
+// Paged K/V cache: the append kernel (rotary positions applied on the way) and the C entry
+// points of the cache (include/dex.h, "paged K/V cache").
+#include <math.h>
+
+#include "../../include/dex.h"
+#include "common.cuh"
+#include "kernels.h"
+
+namespace dex {
+
+namespace {
+
+constexpr int kAppendThreads = 256;
+constexpr int kAppendUnroll = 4;   // items a thread holds in flight
+
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ void from_f32(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void from_f32(__half& y, float x) { y = __float2half_rn(x); }
+
+// Eight consecutive elements as loaded (16 bytes of a 16-bit type, 32 of fp32).
+template <typename T>
+struct alignas(16) Vec8 {
+  T v[8];
+};
+template <typename T>
+__device__ __forceinline__ Vec8<T> load8(const T* p) {
+  Vec8<T> r;
+  const uint4* s = reinterpret_cast<const uint4*>(p);
+  uint4* d = reinterpret_cast<uint4*>(&r);
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i) d[i] = __ldcs(s + i);
+  return r;
+}
+
+}  // namespace
+
+// One block per token.  An item is 16 elements of one head row: of q and k the eight pairs
+// (x_j, x_{j + HD/2}), j = 8c .. 8c+7, of v the elements 16c .. 16c+15, so each item is two
+// 16-byte loads and two 16-byte stores.  The HD/2 angles of the token are the same for all
+// its heads, so they are computed once per block; the rows are loaded before that.
+//
+// Angle: the turn of pair j at position r is r * theta^(-2j/HD) / 2 pi.  With the turn of position
+// 1 as a 64-bit fixed-point fraction, r times it modulo 2^64 is the fraction of a turn left after
+// whole turns, exactly -- an fp32 product r * frequency would be off by 2^-24 r radians (0.06 at
+// r = 10^6).  Its upper 32 bits as a signed number are half-turns in units of 2^-31.
+template <typename CT, typename IT, int HD>
+__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __grid_constant__ AppendArgs a) {
+  __shared__ float2 cs[HD / 2];
+  constexpr int kItems = HD / 16;   // items per head row
+  const int t = blockIdx.x, tid = threadIdx.x;
+  const int n_rows = (a.q ? a.H : 0) + 2 * a.kv.KVH, n_items = n_rows * kItems;
+  const int k_row0 = a.q ? a.H : 0, v_row0 = k_row0 + a.kv.KVH;
+
+  const int seq = __ldg(a.seq + t), pos = __ldg(a.pos + t);
+  const int rpos = a.rope_pos ? __ldg(a.rope_pos + t) : pos;
+  Vec8<IT> lo[kAppendUnroll], hi[kAppendUnroll];
+  auto load_items = [&](int base) {
+#pragma unroll
+    for (int u = 0; u < kAppendUnroll; ++u) {
+      const int it = base + u * kAppendThreads + tid;
+      if (it >= n_items) break;
+      const int row = it / kItems, c = it % kItems;
+      const bool is_v = row >= v_row0;
+      const IT* src = row < k_row0 ? static_cast<const IT*>(a.q) + t * a.q_stride + static_cast<int64_t>(row) * HD
+                      : !is_v ? static_cast<const IT*>(a.k) + t * a.k_stride + static_cast<int64_t>(row - k_row0) * HD
+                              : static_cast<const IT*>(a.v) + t * a.v_stride + static_cast<int64_t>(row - v_row0) * HD;
+      lo[u] = load8(src + (is_v ? 16 * c : 8 * c));
+      hi[u] = load8(src + (is_v ? 16 * c + 8 : 8 * c + HD / 2));
+    }
+  };
+  load_items(0);
+
+  // destination: every thread checks for itself, so all of them agree without a barrier
+  const int page_size = 1 << a.kv.page_shift;
+  const int pidx = pos >> a.kv.page_shift;
+  bool ok = seq >= 0 && seq < a.kv.batch && pos >= 0 && pidx < a.kv.table_width;
+  int page = -1;
+  if (ok) {
+    page = __ldg(a.kv.table + static_cast<int64_t>(seq) * a.kv.table_stride + pidx);
+    ok = page >= 0 && page < a.kv.n_pages;
+  }
+  if (!ok) {
+    if (seq != -1 && tid == 0 && a.rejected) atomicAdd(a.rejected, 1);
+    return;
+  }
+  if (a.rotate && tid < HD / 2) {
+    const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(rpos)) * a.turn[tid];
+    float s, c;
+    sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f, &s, &c);   // 2^-31
+    cs[tid] = make_float2(c, s);
+  }
+  __syncthreads();
+
+  CT* kv_row = static_cast<CT*>(a.kv.pages) + page * a.kv.page_stride +
+               static_cast<int64_t>(pos & (page_size - 1)) * HD;
+  const int64_t head_stride = static_cast<int64_t>(page_size) * HD;
+  for (int base = 0; base < n_items; base += kAppendUnroll * kAppendThreads) {
+    if (base) load_items(base);
+#pragma unroll
+    for (int u = 0; u < kAppendUnroll; ++u) {
+      const int it = base + u * kAppendThreads + tid;
+      if (it >= n_items) break;
+      const int row = it / kItems, c = it % kItems;
+      const bool is_v = row >= v_row0;
+      Vec8<CT> x, y;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float p = to_f32(lo[u].v[i]), r = to_f32(hi[u].v[i]);
+        if (!is_v && a.rotate) {
+          const float2 w = cs[8 * c + i];
+          const float p0 = p;
+          p = p0 * w.x - r * w.y;
+          r = r * w.x + p0 * w.y;
+        }
+        from_f32(x.v[i], p);
+        from_f32(y.v[i], r);
+      }
+      CT* dst = row < k_row0 ? static_cast<CT*>(a.q_out) + t * a.q_out_stride + static_cast<int64_t>(row) * HD
+                             : kv_row + (row - k_row0) * head_stride;   // V heads follow the K heads in a page
+      *reinterpret_cast<uint4*>(dst + (is_v ? 16 * c : 8 * c)) = *reinterpret_cast<const uint4*>(&x);
+      *reinterpret_cast<uint4*>(dst + (is_v ? 16 * c + 8 : 8 * c + HD / 2)) = *reinterpret_cast<const uint4*>(&y);
+    }
+  }
+}
+
+template <typename CT, typename IT>
+static cudaError_t launch_append_hd(const AppendArgs& a, cudaStream_t st) {
+  if (a.kv.hd == 128) paged_append_kernel<CT, IT, 128><<<a.n_tokens, kAppendThreads, 0, st>>>(a);
+  else paged_append_kernel<CT, IT, 64><<<a.n_tokens, kAppendThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_paged_append(const AppendArgs& a, cudaStream_t st) {
+  if (a.kv.fp16) return a.in_fp32 ? launch_append_hd<__half, float>(a, st) : launch_append_hd<__half, __half>(a, st);
+  return a.in_fp32 ? launch_append_hd<__nv_bfloat16, float>(a, st)
+                   : launch_append_hd<__nv_bfloat16, __nv_bfloat16>(a, st);
+}
+
+}  // namespace dex
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// Checks a cache description and fills the kernels' form of it.
+int paged_kv(const dex_paged_kv* kv, dex::PagedKv* out) {
+  if (!kv || (kv->head_dim != 64 && kv->head_dim != 128) || kv->n_pages < 1 || kv->n_kv_heads < 1 ||
+      kv->n_kv_heads > 1024 || kv->batch < 1 || kv->batch > 1024 || kv->table_width < 1 ||
+      kv->table_stride < kv->table_width || (kv->dtype != DEX_DT_BF16 && kv->dtype != DEX_DT_FP16))
+    return DEX_EINVAL;
+  int shift = 4;
+  while (shift < 8 && (1 << shift) != kv->page_size) ++shift;
+  if ((1 << shift) != kv->page_size) return DEX_EINVAL;
+  if (static_cast<int64_t>(kv->table_width) * kv->page_size >= (int64_t(1) << 31)) return DEX_EINVAL;
+  const int64_t page_elems = int64_t(2) * kv->n_kv_heads * kv->page_size * kv->head_dim;
+  if (kv->page_stride < page_elems || kv->page_stride % 8 || kv->page_stride >= (int64_t(1) << 39)) return DEX_EINVAL;
+  out->pages = kv->pages;
+  out->table = kv->table;
+  out->page_stride = kv->page_stride;
+  out->n_pages = kv->n_pages;
+  out->page_shift = shift;
+  out->KVH = kv->n_kv_heads;
+  out->hd = kv->head_dim;
+  out->batch = kv->batch;
+  out->table_width = kv->table_width;
+  out->table_stride = kv->table_stride;
+  out->fp16 = kv->dtype == DEX_DT_FP16;
+  return DEX_OK;
+}
+
+}  // namespace
+
+extern "C" int dex_paged_append(const dex_paged_kv* kv, const dex_append_args* a, int32_t* rejected, void* stream) {
+  dex::AppendArgs d = {};
+  const int rc = paged_kv(kv, &d.kv);
+  if (rc) return rc;
+  if (!a || a->n_tokens < 0 || !kv->pages || !kv->table || !aligned16(kv->pages)) return DEX_EINVAL;
+  if (a->in_dtype != kv->dtype && a->in_dtype != DEX_DT_FP32) return DEX_EINVAL;
+  if (!(a->rope_theta == 0.0f || (a->rope_theta >= 1.0f && a->rope_theta < INFINITY))) return DEX_EINVAL;
+  const int64_t vec = a->in_dtype == DEX_DT_FP32 ? 4 : 8;   // elements in 16 bytes
+  if (a->n_tokens > 0) {
+    if (!a->k || !a->v || !a->seq || !a->pos || !aligned16(a->k) || !aligned16(a->v) || a->k_stride % vec ||
+        a->v_stride % vec || (a->q == nullptr) != (a->q_out == nullptr))
+      return DEX_EINVAL;
+    if (a->q && (a->n_heads < 1 || a->n_heads > 131072 || !aligned16(a->q) || !aligned16(a->q_out) || a->q_stride % vec ||
+                 a->q_out_stride % 8 ||
+                 (a->n_tokens > 1 && a->q_out_stride < static_cast<int64_t>(a->n_heads) * kv->head_dim)))
+      return DEX_EINVAL;
+    if (a->q && a->q == a->q_out && (a->in_dtype != kv->dtype || a->q_stride != a->q_out_stride)) return DEX_EINVAL;
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rejected && cudaMemsetAsync(rejected, 0, sizeof(int32_t), st) != cudaSuccess) return DEX_ECUDA;
+  if (a->n_tokens == 0) return DEX_OK;
+  d.q = a->q;
+  d.k = a->k;
+  d.v = a->v;
+  d.q_out = a->q_out;
+  d.q_stride = a->q_stride;
+  d.k_stride = a->k_stride;
+  d.v_stride = a->v_stride;
+  d.q_out_stride = a->q_out_stride;
+  d.seq = a->seq;
+  d.pos = a->pos;
+  d.rope_pos = a->rope_pos;
+  d.n_tokens = a->n_tokens;
+  d.H = a->q ? a->n_heads : 0;
+  d.in_fp32 = a->in_dtype == DEX_DT_FP32;
+  d.rotate = a->rope_theta != 0.0f;
+  d.rejected = rejected;
+  if (d.rotate) {
+    // 53-bit turns: at position 2^31 the angle is off by at most 2^-24 of a turn
+    const double step = pow(static_cast<double>(a->rope_theta), -2.0 / kv->head_dim);
+    double f = 0.15915494309189535;   // 1 / 2 pi
+    for (int j = 0; j < kv->head_dim / 2; ++j, f *= step) d.turn[j] = static_cast<uint64_t>(f * 18446744073709551616.0);
+  }
+  return dex::launch_paged_append(d, st) == cudaSuccess ? DEX_OK : DEX_ECUDA;
+}
+
+// Checks an attention call's sizes (host fields only) and fills the kernels' form of it.
+static int attention_args(const dex_paged_kv* kv, const dex_attention_args* a, dex::PrefixAttnArgs* d) {
+  const int rc = paged_kv(kv, &d->kv);
+  if (rc) return rc;
+  if (!a || a->n_tokens < 0 || a->n_tokens >= (1 << 24) || a->n_heads < 1 || a->n_heads % kv->n_kv_heads ||
+      a->n_heads / kv->n_kv_heads > 128 || a->max_q < 1 || a->prefix_len < 0 ||
+      a->prefix_len > static_cast<int64_t>(kv->table_width) * kv->page_size)
+    return DEX_EINVAL;
+  d->n_tokens = a->n_tokens;
+  d->H = a->n_heads;
+  d->G = a->n_heads / kv->n_kv_heads;
+  d->max_q = a->max_q;
+  d->prefix_len = a->prefix_len;
+  return DEX_OK;
+}
+
+extern "C" int dex_prefix_attention_workspace(const dex_paged_kv* kv, const dex_attention_args* a, size_t* bytes) {
+  dex::PrefixAttnArgs d = {};
+  const int rc = attention_args(kv, a, &d);
+  if (rc || !bytes) return DEX_EINVAL;
+  *bytes = dex::prefix_attention_workspace(d);
+  return DEX_OK;
+}
+
+extern "C" int dex_prefix_attention(const dex_paged_kv* kv, const dex_attention_args* a, void* workspace,
+                                    size_t workspace_bytes, int32_t* status, void* stream) {
+  dex::PrefixAttnArgs d = {};
+  const int rc = attention_args(kv, a, &d);
+  if (rc) return rc;
+  if (!kv->pages || !kv->table || !aligned16(kv->pages) || !a->q_start || !a->seq_len || (a->tree_mask && a->max_q > 64) ||
+      !(a->scale > -INFINITY && a->scale < INFINITY))
+    return DEX_EINVAL;
+  if (a->n_tokens == 0) return DEX_OK;
+  const int64_t row = static_cast<int64_t>(a->n_heads) * kv->head_dim;
+  if (!a->q || !a->out || !aligned16(a->q) || !aligned16(a->out) || a->q_stride % 8 || a->out_stride % 8 ||
+      (a->n_tokens > 1 && a->out_stride < row))
+    return DEX_EINVAL;
+  const size_t need = dex::prefix_attention_workspace(d);
+  if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255))) return DEX_EINVAL;
+  if (workspace_bytes < need) return DEX_ECAPACITY;
+  d.q = a->q;
+  d.out = a->out;
+  d.lse = a->lse;
+  d.q_stride = a->q_stride;
+  d.out_stride = a->out_stride;
+  d.q_start = a->q_start;
+  d.seq_len = a->seq_len;
+  d.prefix_table = a->prefix_table ? a->prefix_table : kv->table;
+  d.tree = a->tree_mask;
+  d.scale_log2 = a->scale * 1.4426950408889634f;
+  d.status = status;
+  return dex::launch_prefix_attention(d, workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DEX_OK : DEX_ECUDA;
+}

@@ -1,0 +1,385 @@
+"""GPU parity of the paged-cache operators (append with rotation, shared-prefix attention) against
+plain 64-bit forms, element by element within bounds derived from the arithmetic."""
+import math
+
+import pytest
+import torch
+
+from gpu_util import require_gpu
+from paged_ref import HALF, attention, rotate, rotate_bound
+
+pytestmark = pytest.mark.gpu
+BF, FP = torch.bfloat16, torch.float16
+
+
+def paged(dexlib, kvh, hd, ps, lens, dtype, prefix=0, width=0, spare=2, seed=0, layers=1, fill=math.nan):
+    """A cache of the given lengths on shuffled pages; every row no sequence uses holds `fill`.
+
+    Returns the PagedCache and CPU copies of its pages and table."""
+    gen = torch.Generator().manual_seed(seed)
+    shared = prefix // ps
+    need = [max(0, -(-n // ps) - shared) for n in lens]
+    n_pages = shared + sum(need) + spare
+    ids = torch.randperm(n_pages, generator=gen).int()
+    width = width or max(1, max(-(-n // ps) for n in lens))
+    table = torch.full((len(lens), width), -1, dtype=torch.int32)
+    table[:, :shared] = ids[:shared]
+    at = shared
+    big = torch.full((n_pages, layers, 2, kvh, ps, hd), fill, dtype=dtype)
+    pages = big[:, layers - 1]
+    pages[ids[:shared].long()] = torch.randn((shared, 2, kvh, ps, hd), generator=gen).to(dtype)
+    tail = torch.randn((2, kvh, prefix % ps, hd), generator=gen).to(dtype)
+    for b, n in enumerate(lens):
+        table[b, shared:shared + need[b]] = ids[at:at + need[b]]
+        at += need[b]
+        rows = torch.randn((2, kvh, max(0, n - shared * ps), hd), generator=gen).to(dtype)
+        rows[:, :, :prefix % ps] = tail[:, :, :rows.shape[2]]
+        for i in range(need[b]):
+            part = rows[:, :, i * ps:(i + 1) * ps]
+            pages[int(table[b, shared + i]), :, :, :part.shape[2]] = part
+    cache = dexlib.PagedCache(big.cuda()[:, layers - 1], table.cuda())
+    return cache, pages, table
+
+
+def queries(H, hd, new, dtype, seed=1, pad=0, strided=False):
+    gen = torch.Generator().manual_seed(seed)
+    n = sum(new) + pad
+    q = torch.randn((n, H + (2 if strided else 0), hd), generator=gen).to(dtype).cuda()[:, :H]
+    start = torch.tensor([0] + new).cumsum(0).int()
+    return q, start
+
+
+def compare(out, lse, ref, owned):
+    o, L, bo, bl = ref
+    out, lse = out.cpu().double(), lse.cpu().double()
+    err = (out - o).abs()[owned]
+    assert not torch.isnan(out[owned]).any()
+    worst = (err / bo[owned].clamp_min(1e-30)).max().item() if err.numel() else 0.0
+    assert bool((err <= bo[owned]).all()), f"out is {worst} of its bound"
+    inf = torch.isinf(L[owned])
+    assert torch.equal(inf, torch.isinf(lse[owned]))
+    d = (lse - L).abs()[owned][~inf]
+    assert bool((d <= bl[owned][~inf]).all()), f"lse off by {d.max().item()}"
+    return worst
+
+
+def run_case(H, kvh, hd, ps, dtype, lens, new, prefix=0, tree=None, pad=0, strided=False, layers=1, seed=0, scale=None,
+             prefix_table=False):
+    dexlib = require_gpu()
+    cache, pages, table = paged(dexlib, kvh, hd, ps, lens, dtype, prefix, seed=seed, layers=layers)
+    q, start = queries(H, hd, new, dtype, seed + 1, pad, strided)
+    seq_len = torch.tensor(lens, dtype=torch.int32)
+    out = torch.full(q.shape, 7.0, dtype=dtype, device="cuda")
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ptab = table[0, :-(-prefix // ps)].clone() if prefix_table else None
+    kw = dict(max_q=max(1, max(new)), prefix_len=prefix, scale=scale,
+              tree_mask=None if tree is None else tree.cuda(), prefix_table=None if ptab is None else ptab.cuda())
+    got = cache.attention(q, start.cuda(), seq_len.cuda(), out=out, lse=lse, status=status, **kw)
+    assert got is out
+    again, lse2 = torch.full_like(out, 7.0), torch.full_like(lse, 7.0)
+    cache.attention(q, start.cuda(), seq_len.cuda(), out=again, lse=lse2, **kw)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    assert torch.equal(out, again) and torch.equal(lse, lse2)   # the same bits every time
+    ref = attention(pages, table, q.cpu(), start, lens, prefix, ptab, tree, scale)
+    owned = torch.zeros(len(q), dtype=torch.bool)
+    owned[:int(start[-1])] = True
+    compare(out, lse, ref, owned)
+    assert bool((out[int(start[-1]):] == 7.0).all()) and bool((lse[int(start[-1]):] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("H,kvh,hd", [(32, 8, 128), (4, 4, 64), (6, 2, 64), (5, 1, 128)])
+@pytest.mark.parametrize("ps", [16, 64, 256])
+def test_attention_decode(H, kvh, hd, ps, dtype):
+    """Single tokens, no sharing: lengths of one, around tile and page borders, an inactive slot."""
+    run_case(H, kvh, hd, ps, dtype, [1, 2, 63, 64, 65, 127, 128, 129, 300, 40], [1, 1, 1, 1, 1, 1, 1, 1, 1, 0])
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("H,kvh,hd,ps", [(32, 8, 128, 16), (8, 8, 128, 32), (16, 4, 64, 64), (6, 2, 128, 128)])
+@pytest.mark.parametrize("prefix", [1, 128, 200, 511])
+def test_attention_decode_prefix(H, kvh, hd, ps, prefix, dtype):
+    """Single tokens behind a shared prefix that ends anywhere in a page or tile."""
+    own = [1, 2, 17, 64, 130, 5, 1, 90, 33, 128, 1, 77, 3, 1, 1, 40, 22]
+    run_case(H, kvh, hd, ps, dtype, [prefix + n for n in own], [1] * len(own), prefix, prefix_table=prefix == 200)
+
+
+@pytest.mark.parametrize("G", [1, 3, 5, 8, 12, 16, 17, 32, 71, 128])
+def test_attention_group_sizes(G):
+    """Any number of query heads per K/V head, with and without sharing."""
+    run_case(2 * G, 2, 64, 32, FP, [300 + 13 * i for i in range(5)], [1, 2, 0, 1, 3], 260)
+    run_case(G, 1, 128, 16, BF, [1, 140, 77], [1, 1, 1])
+
+
+@pytest.mark.parametrize("H,kvh,hd,dtype", [(32, 8, 128, BF), (4, 4, 64, FP), (3, 1, 128, FP)])
+@pytest.mark.parametrize("prefix", [0, 130, 384])
+def test_attention_prompts(H, kvh, hd, dtype, prefix):
+    """Query runs of every length, causal among themselves, padding rows behind the last one."""
+    new = [1, 16, 17, 33, 64, 65, 130, 257, 0, 300]
+    past = [0, 5, 0, 100, 63, 1, 0, 7, 3, 129]
+    run_case(H, kvh, hd, 64, dtype, [prefix + p + n for p, n in zip(past, new)], new, prefix, pad=3, strided=True)
+
+
+@pytest.mark.parametrize("H,kvh,hd", [(32, 8, 128), (4, 4, 64), (8, 1, 128)])
+@pytest.mark.parametrize("prefix", [0, 150])
+@pytest.mark.parametrize("most", [4, 15, 64])
+def test_attention_tree(H, kvh, hd, prefix, most):
+    """Lattice nodes: ancestry masks over the last positions, some words empty."""
+    g = torch.Generator().manual_seed(most)
+    new = [1, most, most // 2 + 1, 0, 2, most]
+    past = [0, 3, 64, 9, 140, 0]
+    words = []
+    for n in new:
+        for i in range(n):
+            w = 1 << i
+            for k in range(i):
+                w |= int(torch.randint(0, 2, (1,), generator=g)) << k
+            words.append(0 if i % 7 == 3 else w - (1 << 64) if w >= 1 << 63 else w)
+    tree = torch.tensor(words, dtype=torch.int64)
+    run_case(H, kvh, hd, 32, FP, [prefix + p + n for p, n in zip(past, new)], new, prefix, tree)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_attention_nothing_visible(dtype):
+    """Empty sequences, queries ahead of a sequence's start, sequences inside the prefix."""
+    run_case(8, 2, 64, 16, dtype, [0, 3, 0, 1, 200], [1, 5, 2, 4, 1])                    # p < 0 rows: zeros, -inf
+    run_case(8, 2, 64, 16, dtype, [100, 260, 300, 30], [40, 1, 40, 30], prefix=100)      # a query run across the border
+    tree = torch.zeros(4, dtype=torch.int64)
+    run_case(8, 2, 128, 16, dtype, [2, 2], [2, 2], tree=tree)                            # all words empty, nothing cached
+
+
+def test_attention_long_and_layers():
+    """A long context split over the whole GPU, pages strided over the layers of a model."""
+    run_case(8, 2, 128, 16, BF, [20011], [1], layers=3)
+    run_case(8, 2, 128, 128, FP, [9000, 9001, 9002, 8999], [1, 2, 1, 1], prefix=8990)
+
+
+def test_attention_scale_and_extremes():
+    """Large scores (one key dominates), a negative and a zero scale."""
+    for scale in (3.0, -0.5, 0.0):
+        run_case(4, 2, 64, 32, FP, [150, 400, 90], [1, 3, 20], prefix=64, scale=scale)
+
+
+def test_attention_bad_pages_and_ranges():
+    """Bad page ids and lengths poison the rows that need them and nothing else."""
+    dexlib = require_gpu()
+    H, kvh, hd, ps = 8, 2, 64, 16
+    lens, new = [50, 60, 70, 80], [1, 1, 1, 1]
+    cache, pages, table = paged(dexlib, kvh, hd, ps, lens, BF)
+    q, start = queries(H, hd, new, BF)
+    ref = attention(pages, table, q.cpu(), start, lens)
+    for victim, value in ((1, 10 ** 9), (1, -1), (1, -2 ** 31)):
+        bad = table.clone()
+        bad[victim, 2] = value
+        cache.table.copy_(bad)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        lse = torch.zeros((4, H), device="cuda")
+        out = cache.attention(q, start.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), max_q=1, lse=lse,
+                              status=status)
+        assert int(status.item()) == dexlib.DEX_ATTN_BAD_PAGE
+        assert bool(torch.isnan(out[victim]).all()) and bool(torch.isnan(lse[victim]).all())
+        compare(out, lse, ref, torch.tensor([b != victim for b in range(4)]))
+    cache.table.copy_(table)
+    for value in (-1, cache.table.shape[1] * ps + 1, 2 ** 31 - 1):
+        L = torch.tensor(lens, dtype=torch.int32)
+        L[2] = value
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        lse = torch.zeros((4, H), device="cuda")
+        out = cache.attention(q, start.cuda(), L.cuda(), max_q=1, lse=lse, status=status)
+        assert int(status.item()) == dexlib.DEX_ATTN_BAD_RANGE
+        assert bool(torch.isnan(out[2]).all())
+        compare(out, lse, ref, torch.tensor([True, True, False, True]))
+    # more queries than max_q: that sequence is left out, its rows stay
+    q, start = queries(H, hd, [1, 3, 1, 1], BF)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full(q.shape, 7.0, dtype=BF, device="cuda")
+    cache.attention(q, start.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), max_q=2, out=out,
+                    status=status)
+    assert int(status.item()) == dexlib.DEX_ATTN_BAD_RANGE
+    assert bool((out[1:4] == 7.0).all()) and not bool((out[[0, 4, 5]] == 7.0).any())
+
+
+def test_attention_graph_and_streams():
+    """A captured call replayed on other lengths and tables; a call on a side stream."""
+    dexlib = require_gpu()
+    H, kvh, hd, ps, prefix = 8, 2, 128, 32, 96
+    lens, new = [prefix + 900, prefix + 5, prefix + 40], [1, 1, 1]
+    cache, pages, table = paged(dexlib, kvh, hd, ps, lens, FP, prefix)
+    q, start = queries(H, hd, new, FP)
+    seq = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    st = start.cuda()
+    ws = cache.attention_workspace(q, 1, prefix)
+    out = torch.zeros(q.shape, dtype=FP, device="cuda")
+    lse = torch.zeros(q.shape[:2], device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        cache.attention(q, st, seq, 1, prefix, out=out, lse=lse, workspace=ws)
+    side.synchronize()
+    own = torch.ones(3, dtype=torch.bool)
+    compare(out, lse, attention(pages, table, q.cpu(), start, lens, prefix), own)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.attention(q, st, seq, 1, prefix, out=out, lse=lse, workspace=ws)
+    for now in (lens, [prefix + 1, prefix + 2, prefix + 3], [prefix + 300, prefix, prefix + 40]):
+        seq.copy_(torch.tensor(now, dtype=torch.int32))
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        compare(out, lse, attention(pages, table, q.cpu(), start, now, prefix), own)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("in32", [False, True])
+@pytest.mark.parametrize("H,kvh,hd,ps", [(32, 8, 128, 16), (4, 4, 64, 64), (70, 70, 64, 32), (3, 1, 128, 256)])
+def test_append(H, kvh, hd, ps, in32, dtype):
+    """Rotation, destination rows, strided inputs, far positions, padding and rejected tokens."""
+    dexlib = require_gpu()
+    lens, width = [3 * ps, 2 * ps + 5, ps], 4
+    cache, pages, table = paged(dexlib, kvh, hd, ps, lens, dtype, width=width, fill=0.5)
+    gen = torch.Generator().manual_seed(3)
+    it = torch.float32 if in32 else dtype
+    toks = [(0, 0), (0, 1), (0, 3 * ps - 1), (1, 2 * ps), (1, ps - 1), (2, 5), (-1, 3), (2, -1), (3, 0), (0, 4 * ps),
+            (2, 2 * ps), (-5, 0), (0, 2 ** 31 - 1)]   # the last six out of range, (2, 2 ps) on a page id of -1
+    n = len(toks)
+    rope = torch.tensor([0, 1, 131071, 2 ** 31 - 1, 77, 1000003, 5, 5, 5, 5, 5, 5, 5], dtype=torch.int32)
+    qkv = torch.randn((n, (H + 2 * kvh) * hd + 8), generator=gen).to(it)
+    dev = qkv.cuda()
+    parts = [x.unflatten(1, (-1, hd)) for x in dev[:, :(H + 2 * kvh) * hd].split((H * hd, kvh * hd, kvh * hd), dim=1)]
+    host = [x.unflatten(1, (-1, hd)) for x in qkv[:, :(H + 2 * kvh) * hd].split((H * hd, kvh * hd, kvh * hd), dim=1)]
+    seq = torch.tensor([t[0] for t in toks], dtype=torch.int32)
+    pos = torch.tensor([t[1] for t in toks], dtype=torch.int32)
+    q_out = torch.full((n, H, hd), 7.0, dtype=dtype, device="cuda")
+    rejected = torch.full((1,), 99, dtype=torch.int32, device="cuda")
+    for theta, use_rope in ((10000.0, True), (1e6, False), (0.0, True)):
+        q_out.fill_(7.0)
+        cache.pages.copy_(pages)
+        r = rope if use_rope else pos
+        got = cache.append(parts[1], parts[2], seq.cuda(), pos.cuda(), q=parts[0], q_out=q_out, theta=theta,
+                           rope_pos=rope.cuda() if use_rope else None, rejected=rejected)
+        assert got is q_out and int(rejected.item()) == 6
+        want = pages.double()
+        tol = torch.zeros_like(want)
+        k, kb = rotate(host[1], r, theta), rotate_bound(host[1], dtype)
+        for t in range(6):
+            pg, row = int(table[toks[t][0], toks[t][1] // ps]), toks[t][1] % ps
+            want[pg, 0, :, row], tol[pg, 0, :, row] = k[t], kb[t]
+            want[pg, 1, :, row] = host[2][t].to(dtype).double()
+        assert bool(((cache.pages.cpu().double() - want).abs() <= tol).all())
+        qq = q_out.cpu().double()
+        assert bool(((qq[:6] - rotate(host[0], r, theta)[:6]).abs() <= rotate_bound(host[0], dtype)[:6]).all())
+        assert bool((qq[6:] == 7.0).all())
+    # q rotated in place equals q rotated aside; without q the cache gets the same rows
+    if not in32:
+        before = cache.pages.clone()
+        cache.append(parts[1], parts[2], seq.cuda(), pos.cuda(), q=parts[0], q_out=parts[0], theta=0.0, rope_pos=rope.cuda())
+        assert torch.equal(dev, qkv.cuda())
+        a = cache.append(parts[1], parts[2], seq.cuda(), pos.cuda(), q=parts[0], rope_pos=rope.cuda())
+        first = cache.pages.clone()
+        cache.pages.copy_(before)
+        cache.append(parts[1], parts[2], seq.cuda(), pos.cuda(), q=parts[0], q_out=parts[0], rope_pos=rope.cuda())
+        assert torch.equal(parts[0][:6], a[:6]) and torch.equal(first, cache.pages)
+        cache.pages.copy_(before)
+        assert cache.append(parts[1], parts[2], seq.cuda(), pos.cuda(), rope_pos=rope.cuda()) is None
+        assert torch.equal(first, cache.pages)
+
+
+def test_append_empty_and_graph():
+    dexlib = require_gpu()
+    cache, _, table = paged(dexlib, 2, 64, 16, [32, 32], FP, fill=0.0)
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    rejected = torch.full((1,), 5, dtype=torch.int32, device="cuda")
+    cache.append(torch.zeros((0, 2, 64), dtype=FP, device="cuda"), torch.zeros((0, 2, 64), dtype=FP, device="cuda"), none,
+                 none, rejected=rejected)
+    assert int(rejected.item()) == 0
+    k = torch.randn((2, 2, 64), dtype=FP, device="cuda")
+    seq = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    pos = torch.tensor([3, 4], dtype=torch.int32, device="cuda")
+    cache.append(k, k, seq, pos)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.append(k, k, seq, pos, theta=0.0)
+    for p in ([5, 6], [31, 0]):
+        pos.copy_(torch.tensor(p, dtype=torch.int32))
+        cache.pages.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for b in range(2):
+            pg = int(table[b, p[b] // 16])
+            assert torch.equal(cache.pages[pg, 0, :, p[b] % 16], k[b]) and torch.equal(cache.pages[pg, 1, :, p[b] % 16], k[b])
+        assert int((cache.pages != 0).any(-1).sum()) == 2 * 2 * 2
+
+
+@pytest.mark.parametrize("H,kvh,hd,dtype", [(32, 8, 128, BF), (4, 4, 64, FP)])
+def test_append_then_attend_as_a_server_would(H, kvh, hd, dtype):
+    """A common prompt appended once, private continuations, then decode steps and a round of lattice
+    nodes: every step's output against attention over the tokens' own q, k, v in 64 bits."""
+    dexlib = require_gpu()
+    ps, theta, B, common = 32, 1e4, 5, 130
+    gen = torch.Generator().manual_seed(9)
+    private = [1, 60, 17, 128, 33]
+    width = 12
+    shared = common // ps
+    n_pages = shared + B * (width - shared)
+    ids = torch.randperm(n_pages, generator=gen).int()
+    table = torch.empty((B, width), dtype=torch.int32)
+    table[:, :shared] = ids[:shared]
+    table[:, shared:] = ids[shared:].view(B, -1)
+    cache = dexlib.PagedCache(torch.full((n_pages, 2, kvh, ps, hd), math.nan, dtype=dtype, device="cuda"), table.cuda())
+    hist_k = [torch.zeros((0, kvh, hd), dtype=torch.float64) for _ in range(B)]
+    hist_v = [torch.zeros((0, kvh, hd), dtype=torch.float64) for _ in range(B)]
+
+    def step(new, rope=None, tree=None, prefix=common, shared_rows=False):
+        """Append new[b] tokens to every sequence and attend; returns the worst share of the bound."""
+        n = sum(new)
+        qkv = torch.randn((n, H + 2 * kvh, hd), generator=gen).to(dtype)
+        seq = torch.tensor([b for b in range(B) for _ in range(new[b])], dtype=torch.int32)
+        pos = torch.tensor([len(hist_k[b]) + i for b in range(B) for i in range(new[b])], dtype=torch.int32)
+        r = pos if rope is None else rope
+        dev = qkv.cuda()
+        q = cache.append(dev[:, H:H + kvh], dev[:, H + kvh:], seq.cuda(), pos.cuda(), q=dev[:, :H], theta=theta,
+                         rope_pos=None if rope is None else rope.cuda())
+        start = torch.tensor([0] + list(new)).cumsum(0).int()
+        k, v = rotate(qkv[:, H:H + kvh], r, theta), qkv[:, H + kvh:].double()
+        qr = rotate(qkv[:, :H], r, theta)
+        for b in range(B):
+            s = slice(int(start[b]), int(start[b + 1]))
+            hist_k[b], hist_v[b] = torch.cat((hist_k[b], k[s])), torch.cat((hist_v[b], v[s]))
+        lens = [len(x) for x in hist_k]
+        out = cache.attention(q, start.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), max_q=max(new),
+                              prefix_len=prefix, tree_mask=None if tree is None else tree.cuda()).cpu().double()
+        u = HALF[dtype]
+        for b in range(B):
+            for i in range(new[b]):
+                t, L = int(start[b]) + i, lens[b]
+                seen = torch.arange(L) <= L - new[b] + i
+                if tree is not None:
+                    seen = torch.tensor([j < L - new[b] or bool(int(tree[t]) >> (j - L + new[b]) & 1) for j in range(L)])
+                kk = hist_k[b][seen].repeat_interleave(H // kvh, 1)
+                vv = hist_v[b][seen].repeat_interleave(H // kvh, 1)
+                sc = torch.einsum("hd,jhd->hj", qr[t], kk) * hd ** -0.5
+                w = torch.softmax(sc, -1)
+                want = torch.einsum("hj,jhd->hd", w, vv)
+                # q and k rounded to the cache's type move a score by up to 2u sum|q k| / sqrt(hd), a weight
+                # by twice that relatively, and the weights' sum again
+                ds = (torch.einsum("hd,jhd->hj", qr[t].abs(), kk.abs()) * hd ** -0.5).amax(-1) * 2.1 * u
+                bound = u * want.abs() + (2.0 * torch.expm1(2 * ds) + 2 * u)[:, None] * torch.einsum("hj,jhd->hd", w, vv.abs())
+                assert bool(((out[t] - want).abs() <= bound + 1e-6).all())
+
+    # the prompt goes in through sequence 0; the others share its whole pages and copy the last one
+    hist = [common, 0, 0, 0, 0]
+    step(hist, prefix=0)
+    for b in range(1, B):
+        hist_k[b], hist_v[b] = hist_k[0].clone(), hist_v[0].clone()
+        cache.pages[int(table[b, shared]), :, :, :common % ps] = cache.pages[int(table[0, shared]), :, :, :common % ps]
+    step(private)
+    for _ in range(3):
+        step([1] * B)
+    # lattice nodes: a chain of three and two siblings, cache rows apart from rotation positions
+    words, rope = [], []
+    for b in range(B):
+        words += [0b00001, 0b00011, 0b00111, 0b01001, 0b10001]
+        rope += [len(hist_k[b]) + d for d in (0, 1, 2, 1, 1)]
+    step([5] * B, torch.tensor(rope, dtype=torch.int32), torch.tensor(words, dtype=torch.int64))
