@@ -67,6 +67,8 @@ int pow2_at_least(int x) {
 
 }  // namespace
 
+PFN_cuTensorMapEncodeTiled_v12000 dex::tensor_map_encoder() { return get_encoder() == DEX_OK ? g_encode : nullptr; }
+
 constexpr int kPrefillRowsMax = 512;   // most prompt positions per prefill pass (rows of the scratch planes)
 
 struct dex_handle {

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -271,6 +272,9 @@ cudaError_t launch_decode_best(const unsigned long long* best, int n, const int3
 // Node table of an isolated exit-head call (host struct dex_exit_node, device array) ->
 // the kernels' DevNode rows.
 cudaError_t launch_exit_nodes(const void* exit_nodes, int n, DevNode* out, cudaStream_t st);
+
+// The driver's tensor-map encoder, or null when it cannot be had.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // ---- paged cache --------------------------------------------------------------------------
 // One layer of a paged K/V cache as the kernels see it: pages of [2][KVH][page][hd] elements,

@@ -1,4 +1,34 @@
 // Attention of a ragged batch of queries over a paged K/V cache whose sequences share a prefix.
+//
+//   o_i = sum_j softmax_j(scale q_i . k_j) v_j        over the keys j that query i sees
+//
+// The softmax over a set of keys is carried as (m, l, O): the largest score, the sum of
+// exp2(s - m) and the sum of exp2(s - m) v.  Two disjoint key sets join as m = max(m1, m2),
+// x = x1 2^(m1-m) + x2 2^(m2-m), so any split of a query's keys over CTAs gives the same result.
+//
+// A *segment* is a set of query rows of one K/V head that reads the same keys:
+//  * prefix segment: rows of all sequences (token-major, the G query heads of the K/V head
+//    next to each other) against the shared positions [0, prefix_len) -- each key is read once
+//    for up to 256 rows;
+//  * own segment: rows of one sequence against its positions from prefix_len on (from 0 when
+//    nothing is shared).
+// Key tiles of all segments are laid end to end and cut into equal contiguous ranges, one per
+// CTA of a persistent grid, so lengths need no plan on the host and any mix of lengths balances.
+// A segment that lies in one CTA is finished there; one that is cut leaves a partial (m, l, O) per
+// CTA, and combine_kernel joins the parts of each row in a fixed order (no atomics: the same
+// lengths give the same bits).
+//
+// Two kernels compute segments:
+//  * rows_kernel (at most 16 rows: single tokens, few heads): the keys are the work, so it is a
+//    stream of K and V through a TMA ring into m16n8k16 MMAs on register fragments;
+//  * tile_kernel (up to 256 rows): 5th-generation tensor cores, two 128-row tiles per CTA that
+//    share every K and V tile.
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include <atomic>
+#include <type_traits>
+
 #include "../../include/dex.h"
 #include "common.cuh"
 #include "kernels.h"
@@ -7,15 +37,195 @@ namespace dex {
 
 namespace {
 
-__device__ __forceinline__ float2 pair_f32(__nv_bfloat162 x) { return __bfloat1622float2(x); }
-__device__ __forceinline__ float2 pair_f32(__half2 x) { return __half22float2(x); }
-template <typename T> struct PairOf;
-template <> struct PairOf<__nv_bfloat16> { using type = __nv_bfloat162; };
-template <> struct PairOf<__half> { using type = __half2; };
-__device__ __forceinline__ __nv_bfloat162 pair_of(float x, float y, __nv_bfloat162) { return __floats2bfloat162_rn(x, y); }
-__device__ __forceinline__ __half2 pair_of(float x, float y, __half2) { return __floats2half2_rn(x, y); }
+constexpr int kRowsTile = 64;     // keys of a tile of rows_kernel
+constexpr int kRowsMax = 16;      // its query rows
+constexpr int kRowsWarps = 4;     // compute warps: each takes 16 keys of a tile
+constexpr int kRowsThreads = 32 * (kRowsWarps + 1);
+constexpr int kRowsPerSm = 2;     // resident CTAs
+constexpr int kTileKeys = 128;    // keys of a tile of tile_kernel
+constexpr int kTileRows = 256;    // its query rows (two tiles of 128)
+constexpr int kMaxBatch = 1024;
 
-// The sequence whose queries hold token t, or -1: the last b with q_start[b] <= t.
+// What one of the two kernels has to do in a call.
+struct SegWork {
+  PrefixAttnArgs a;
+  int32_t share;        // 1: positions below prefix_len belong to prefix segments
+  int32_t do_prefix;    // this kernel computes the prefix segments
+  int32_t do_own;       // this kernel computes the own segments
+  int32_t joined;       // 1: rows have prefix and own parts, so a finished segment is not yet the output
+  float* part_o;        // [2 * CTAs][rows][hd] parts of cut segments
+  float2* part_ml;      // [2 * CTAs][rows] (m, l)
+  float* pre_o;         // [n_tokens * H][hd] finished prefix segments (joined)
+  float2* pre_ml;
+  float* own_o;         // the same of own segments
+  float2* own_ml;
+  int2* pre_info;       // [prefix segments] first and last CTA
+  int2* own_info;       // [own segments]
+};
+
+template <typename T> struct Half2Of;
+template <> struct Half2Of<__nv_bfloat16> { using type = __nv_bfloat162; };
+template <> struct Half2Of<__half> { using type = __half2; };
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {   // x in the low half
+  typename Half2Of<T>::type v;
+  if constexpr (std::is_same<T, __half>::value) v = __floats2half2_rn(x, y);
+  else v = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fffffff); }
+
+// ---- segments ------------------------------------------------------------------------------
+struct SeqRef {
+  int q0, n, len;
+  bool valid;   // has queries, and they are in range
+  bool bad;     // length out of range: rows are poisoned
+};
+__device__ __forceinline__ SeqRef seq_ref(const PrefixAttnArgs& a, int b, bool* report = nullptr) {
+  SeqRef s;
+  s.q0 = __ldg(a.q_start + b);
+  const int q1 = __ldg(a.q_start + b + 1);
+  s.len = __ldg(a.seq_len + b);
+  const bool range = s.q0 >= 0 && q1 >= s.q0 && q1 <= a.n_tokens && q1 - s.q0 <= a.max_q;
+  s.n = range ? q1 - s.q0 : 0;
+  s.valid = s.n > 0;
+  s.bad = s.len < 0 || s.len > (a.kv.table_width << a.kv.page_shift);
+  if (report) *report = !range || s.bad;
+  if (s.bad) s.len = 0;
+  return s;
+}
+
+// Keys [lo, hi) of a sequence's own segment of rows [r0, r1) and its tiles.
+struct KeyRange {
+  int lo, hi, t0, nt;
+};
+template <int TILE>
+__device__ __forceinline__ KeyRange own_range(const SegWork& w, const SeqRef& s, int r1) {
+  KeyRange k;
+  k.lo = w.share ? w.a.prefix_len : 0;
+  const int last = s.len - s.n + (r1 - 1) / w.a.G;   // position of the last query
+  k.hi = s.bad ? 0 : w.a.tree ? s.len : max(0, last + 1);
+  k.t0 = k.lo / TILE;
+  k.nt = k.hi > k.lo ? (k.hi + TILE - 1) / TILE - k.t0 : 0;
+  if (k.nt == 0) {
+    k.hi = k.lo;
+    // someone has to write the row: an empty tile, unless the prefix part covers it
+    if (!w.share || s.bad) k.nt = 1;
+  }
+  return k;
+}
+
+// The segment that holds a key tile, and the walk to the next one.
+template <int RT, int TILE>
+struct Walker {
+  const SegWork& w;
+  int n_pre, pre_nt;       // prefix segments of this kernel and their tiles
+  // current segment
+  bool prefix;
+  int seg, b, rt, kvh, rows, r0;   // seg: prefix segment index; r0: first row within the sequence / batch
+  SeqRef s;
+  KeyRange k;
+
+  __device__ __forceinline__ explicit Walker(const SegWork& work) : w(work) {
+    const int pre_rows = w.a.n_tokens * w.a.G;
+    n_pre = w.do_prefix ? (pre_rows + RT - 1) / RT * w.a.kv.KVH : 0;
+    pre_nt = (w.a.prefix_len + TILE - 1) / TILE;
+  }
+  __device__ __forceinline__ uint32_t pre_tiles() const {
+    return static_cast<uint32_t>(n_pre) * static_cast<uint32_t>(pre_nt);
+  }
+  // tiles of one K/V head over the row tiles of sequence b
+  __device__ __forceinline__ uint32_t seq_tiles(const SeqRef& q) const {
+    if (!q.valid) return 0;
+    uint32_t n = 0;
+    for (int r = 0; r < q.n * w.a.G; r += RT) n += own_range<TILE>(w, q, min(r + RT, q.n * w.a.G)).nt;
+    return n;
+  }
+  __device__ __forceinline__ void set_prefix(int index) {
+    prefix = true;
+    seg = index;
+    kvh = index % w.a.kv.KVH;
+    rt = index / w.a.kv.KVH;
+    r0 = rt * RT;
+    rows = min(RT, w.a.n_tokens * w.a.G - r0);
+    k = KeyRange{0, w.a.prefix_len, 0, pre_nt};
+  }
+  __device__ __forceinline__ void set_own() {
+    prefix = false;
+    r0 = rt * RT;
+    rows = min(RT, s.n * w.a.G - r0);
+    k = own_range<TILE>(w, s, r0 + rows);
+  }
+  // Segment of tile g (cum[b]: own tiles of all K/V heads before sequence b); returns the tile within it.
+  __device__ __forceinline__ int find(uint32_t g, const uint32_t* cum) {
+    if (g < pre_tiles()) {
+      set_prefix(static_cast<int>(g / static_cast<uint32_t>(pre_nt)));
+      return static_cast<int>(g % static_cast<uint32_t>(pre_nt));
+    }
+    g -= pre_tiles();
+    int lo = 0, hi = w.a.kv.batch - 1;
+    while (lo < hi) {   // last b with cum[b] <= g: a sequence with tiles, since the total is beyond g
+      const int mid = (lo + hi + 1) >> 1;
+      if (cum[mid] <= g) lo = mid;
+      else hi = mid - 1;
+    }
+    b = lo;
+    g -= cum[lo];
+    s = seq_ref(w.a, b);
+    for (rt = 0;; ++rt) {
+      set_own();
+      const uint32_t cnt = static_cast<uint32_t>(k.nt) * static_cast<uint32_t>(w.a.kv.KVH);
+      if (g < cnt) break;
+      g -= cnt;
+    }
+    kvh = static_cast<int>(g / static_cast<uint32_t>(k.nt));
+    return static_cast<int>(g % static_cast<uint32_t>(k.nt));
+  }
+  // The next segment that has tiles (the caller knows that there is one).
+  __device__ __forceinline__ void next() {
+    if (prefix) {
+      if (seg + 1 < n_pre) {
+        set_prefix(seg + 1);
+        return;
+      }
+      b = -1;
+    } else {
+      if (++kvh < w.a.kv.KVH) return;
+      kvh = 0;
+      while ((rt + 1) * RT < s.n * w.a.G) {
+        ++rt;
+        set_own();
+        if (k.nt > 0) return;
+      }
+    }
+    kvh = 0;
+    while (++b < w.a.kv.batch) {
+      s = seq_ref(w.a, b);
+      if (!s.valid) continue;
+      for (rt = 0; rt * RT < s.n * w.a.G; ++rt) {
+        set_own();
+        if (k.nt > 0) return;
+      }
+    }
+  }
+  // Token, query head and position of row r of the segment.
+  __device__ __forceinline__ int token(int r) const { return (prefix ? 0 : s.q0) + (r0 + r) / w.a.G; }
+  __device__ __forceinline__ int head(int r) const { return kvh * w.a.G + (r0 + r) % w.a.G; }
+  __device__ __forceinline__ int own_info_index() const {
+    return own_info_of(w.a, s.q0, b, rt, kvh);
+  }
+  __device__ static __forceinline__ int own_info_of(const PrefixAttnArgs& a, int q0, int b, int rt, int kvh) {
+    return (static_cast<int>(static_cast<int64_t>(q0) * a.G / RT) + b + rt) * a.kv.KVH + kvh;
+  }
+};
+
+// The sequence whose queries can hold token t: the last b with q_start[b] <= t.
 __device__ __forceinline__ int seq_of_token(const PrefixAttnArgs& a, int t) {
   int lo = 0, hi = a.kv.batch - 1;
   while (lo < hi) {
@@ -23,91 +233,1280 @@ __device__ __forceinline__ int seq_of_token(const PrefixAttnArgs& a, int t) {
     if (__ldg(a.q_start + mid) <= t) lo = mid;
     else hi = mid - 1;
   }
-  return (__ldg(a.q_start + lo) <= t && t < __ldg(a.q_start + lo + 1)) ? lo : -1;
+  return lo;
+}
+
+// Which keys a row sees: j in [lo, hi), and j <= last or (tree) bit j - first of the word.
+struct RowView {
+  int last;        // causal: the row's position; tree: the last key before the queries' own
+  int first;       // tree: position of the first query
+  uint64_t word;
+  bool owned;      // the row belongs to a sequence (its result is written)
+  __device__ __forceinline__ bool sees(int j) const {
+    return j <= last || (word != 0 && j >= first && j - first < 64 && ((word >> (j - first)) & 1));
+  }
+};
+__device__ __forceinline__ RowView row_view(const PrefixAttnArgs& a, const SeqRef& s, int t) {
+  RowView v;
+  v.owned = s.valid && t >= s.q0 && t < s.q0 + s.n;
+  v.first = s.len - s.n;
+  v.word = a.tree && v.owned ? __ldg(reinterpret_cast<const unsigned long long*>(a.tree) + t) : 0ull;
+  v.last = a.tree ? v.first - 1 : v.first + (t - s.q0);
+  if (s.bad) v.last = -1, v.word = 0;
+  if (!v.owned) v.last = 0x7fffffff;   // its result is not used: no reason to mask
+  return v;
+}
+
+// Own tiles of every sequence, as running totals in cum[0 .. batch]; the block's threads together.
+// scratch: 32 words.  Returns the total number of tiles of the kernel.
+template <int RT, int TILE, int THREADS>
+__device__ __forceinline__ uint32_t count_tiles(const Walker<RT, TILE>& wk, uint32_t* cum, uint32_t* scratch) {
+  const SegWork& w = wk.w;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = w.do_own ? w.a.kv.batch : 0;
+  uint32_t base = 0;
+  for (int b0 = 0; b0 < B; b0 += THREADS) {
+    const int b = b0 + tid;
+    uint32_t n = 0;
+    if (b < B) {
+      bool report;
+      const SeqRef s = seq_ref(w.a, b, &report);
+      n = wk.seq_tiles(s) * static_cast<uint32_t>(w.a.kv.KVH);
+      if (report && blockIdx.x == 0 && w.a.status) atomicOr(w.a.status, DEX_ATTN_BAD_RANGE);
+    }
+    uint32_t x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) scratch[warp] = x;
+    __syncthreads();
+    uint32_t before = base;
+    for (int i = 0; i < THREADS / 32; ++i) {
+      if (i < warp) before += scratch[i];
+      base += scratch[i];
+    }
+    if (b < B) cum[b] = before + x - n;
+    __syncthreads();
+  }
+  return wk.pre_tiles() + base;
+}
+
+// This CTA's share [g0, g1) of `total` tiles over at most `ctas` CTAs (none is left without a tile
+// between two that have one), and the CTA that holds tile g.
+struct Share {
+  uint32_t total, ctas;
+  __device__ __forceinline__ Share(uint32_t n, uint32_t c) : total(n), ctas(min(n, c)) {}
+  __device__ __forceinline__ uint32_t begin(uint32_t c) const {
+    return static_cast<uint32_t>(static_cast<uint64_t>(c) * total / ctas);
+  }
+  __device__ __forceinline__ int owner(uint32_t g) const {
+    return static_cast<int>((static_cast<uint64_t>(g + 1) * ctas - 1) / total);
+  }
+};
+
+// ---- device primitives beyond common.cuh ------------------------------------------------------
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Loads key tiles (TILE positions) of a segment: K and V boxes of the pages that hold a key of [lo, hi),
+// one page per lane; the whole warp takes part.  ids holds the page ids of table entries id0 + lane.
+template <int HD, int TILE>
+struct PageLoader {
+  const CUtensorMap* map;
+  const PagedKv* kv;
+  const int32_t* tab;
+  int id0, ids, lane;
+  int id_end;   // entries below this one are in use
+  __device__ __forceinline__ void start(const int32_t* table, int key_end) {
+    tab = table;
+    id0 = -(1 << 30);
+    id_end = (key_end + (1 << kv->page_shift) - 1) >> kv->page_shift;
+  }
+  __device__ __forceinline__ int boxes(int key0, int lo, int hi, int& first) const {   // pages of the tile in use
+    const int a = max(key0, lo), b = min(key0 + TILE, hi);
+    if (b <= a) return 0;
+    first = a >> kv->page_shift;
+    return ((b - 1) >> kv->page_shift) - first + 1;
+  }
+  // rows of one box: a page, or the whole tile when pages are larger
+  __device__ __forceinline__ int box_rows() const { return min(1 << kv->page_shift, TILE); }
+  __device__ __forceinline__ void prefetch(int first, int n) {
+    if (n > 0 && (first < id0 || first + n > id0 + 32)) {
+      id0 = first;
+      ids = first + lane < id_end ? __ldg(tab + first + lane) : -1;
+    }
+  }
+  // This lane's page of the tile, n_pages (beyond the tensor: the copy fills zeros) for an id out of
+  // range; returns whether any lane's was.
+  __device__ __forceinline__ bool page_of_lane(int first, int n, int& page) const {
+    page = __shfl_sync(0xffffffffu, ids, (first - id0 + lane) & 31);
+    const bool bad = lane < n && (page < 0 || page >= kv->n_pages);
+    if (bad) page = kv->n_pages;
+    return __any_sync(0xffffffffu, bad);
+  }
+  // dst: [HD/64][TILE rows][128 B]; which: 0 K, 1 V
+  __device__ __forceinline__ void load(uint8_t* dst, uint64_t* bar, int which, int kvh, int key0, int first, int n,
+                                       int page) const {
+    if (lane >= n) return;
+    const int row = first + lane - (key0 >> kv->page_shift);   // page within the tile
+    const int y = key0 & ((1 << kv->page_shift) - 1);          // tile within the page (pages larger than a tile)
+#pragma unroll
+    for (int h = 0; h < HD / 64; ++h)
+      tma_load_4d(dst + h * TILE * 128 + (row << kv->page_shift) * 128, map, bar, h * 64, y, which * kv->KVH + kvh, page);
+  }
+};
+
+}  // namespace
+
+// ============================================================================================
+// At most 16 rows per segment.  Four compute warps take 16 keys each of a 64-key tile: S (16 x 16)
+// and O (16 x HD) are register fragments, every warp keeps its own running (m, l), and the four join
+// once per segment through shared memory.  A fifth warp streams the pages by TMA (128-byte swizzle,
+// so the ldmatrix reads are free of bank conflicts).
+// ============================================================================================
+template <int HD>
+struct RowsSmem {
+  static constexpr int kStages = HD == 128 ? 3 : 6;
+  static constexpr uint32_t kHalf = kRowsTile * HD * 2;          // a K or V tile
+  static constexpr uint32_t kStage = 2 * kHalf;
+  static constexpr uint32_t oJoin = kStages * kStage;            // float [16][HD + 4]
+  static constexpr uint32_t oMl = oJoin + kRowsMax * (HD + 4) * 4;   // float2 [4][16]
+  static constexpr uint32_t oCum = oMl + kRowsWarps * kRowsMax * 8;
+  static constexpr uint32_t oScr = oCum + kMaxBatch * 4;
+  static constexpr uint32_t oBar = oScr + 32 * 4;                // full, empty, bad flags
+  static constexpr uint32_t kTotal = oBar + 2 * kStages * 8 + kStages * 4 + 1024;
+};
+static_assert(2 * (RowsSmem<128>::kTotal + 1024) <= 228 * 1024, "two CTAs per SM");
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
+    rows_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ SegWork w) {
+  using SM = RowsSmem<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::oBar);
+  uint64_t* empty = full + SM::kStages;
+  volatile int* bad_stage = reinterpret_cast<volatile int*>(empty + SM::kStages);
+  uint32_t* cum = reinterpret_cast<uint32_t*>(smem + SM::oCum);
+  const PrefixAttnArgs& a = w.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < SM::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kRowsWarps);
+    }
+    fence_mbar_init();
+    tma_prefetch(&tm);
+  }
+  Walker<kRowsMax, kRowsTile> wk(w);
+  const uint32_t total = count_tiles<kRowsMax, kRowsTile, kRowsThreads>(wk, cum, reinterpret_cast<uint32_t*>(smem + SM::oScr));
+  __syncthreads();
+  griddep_launch_dependents();
+  const Share sh(total, gridDim.x);
+  if (blockIdx.x < sh.ctas) {
+    const uint32_t g0 = sh.begin(blockIdx.x), g1 = sh.begin(blockIdx.x + 1);
+    int tile = wk.find(g0, cum);
+    if (warp == kRowsWarps) {
+      // ---------------- producer ----------------
+      PageLoader<HD, kRowsTile> ld;
+      ld.map = &tm;
+      ld.kv = &a.kv;
+      ld.lane = lane;
+      int it = 0;
+      bool ok = true;
+      for (uint32_t g = g0; g < g1 && ok; wk.next(), tile = 0) {
+        const int cnt = min(wk.k.nt - tile, static_cast<int>(g1 - g));
+        ld.start(wk.prefix ? a.prefix_table : a.kv.table + static_cast<int64_t>(wk.b) * a.kv.table_stride, wk.k.hi);
+        for (int i = 0; i < cnt; ++i, ++it) {
+          const int st = it % SM::kStages, key0 = (wk.k.t0 + tile + i) * kRowsTile;
+          int first = 0;
+          const int n = ld.boxes(key0, wk.k.lo, wk.k.hi, first);
+          ld.prefetch(first, n);
+          if (it >= SM::kStages && !mbar_wait(&empty[st], static_cast<uint32_t>(it / SM::kStages - 1) & 1u, nullptr, 0)) {
+            if (a.status && lane == 0) atomicOr(a.status, DEX_ATTN_TIMEOUT);
+            ok = false;
+            break;
+          }
+          uint8_t* dst = smem + st * SM::kStage;
+          int page;
+          const bool bad = ld.page_of_lane(first, n, page);
+          if (lane == 0) {
+            bad_stage[st] = bad;
+            if (bad && a.status) atomicOr(a.status, DEX_ATTN_BAD_PAGE);
+            if (n > 0) mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(n * ld.box_rows() * HD * 2 * 2));
+            else mbar_arrive(&full[st]);
+          }
+          __syncwarp();
+          ld.load(dst, &full[st], 0, wk.kvh, key0, first, n, page);
+          ld.load(dst + SM::kHalf, &full[st], 1, wk.kvh, key0, first, n, page);
+        }
+        g += static_cast<uint32_t>(cnt);
+        if (g >= g1) break;
+      }
+      if (!ok) {   // let the copies in flight land before the CTA goes
+        for (int j = max(0, it - SM::kStages); j < it; ++j)
+          mbar_wait(&full[j % SM::kStages], static_cast<uint32_t>(j / SM::kStages) & 1u, nullptr, 0);
+      }
+    } else {
+      // ---------------- compute ----------------
+      const int gr = lane >> 2, tq = lane & 3;   // fragment row and column pair
+      float* join = reinterpret_cast<float*>(smem + SM::oJoin);
+      float2* join_ml = reinterpret_cast<float2*>(smem + SM::oMl);
+      const float c = a.scale_log2 == 0.0f ? 1.0f : fabsf(a.scale_log2);
+      int it = 0;
+      bool ok = true;
+      for (uint32_t g = g0; g < g1;) {
+        const int cnt = min(wk.k.nt - tile, static_cast<int>(g1 - g));
+        // query fragments: rows gr and gr + 8 (zero beyond the segment), signed as the scale
+        uint32_t qf[HD / 16][4];
+        RowView rv[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = gr + 8 * h;
+          const bool on = r < wk.rows && a.scale_log2 != 0.0f;
+          const uint32_t* src = reinterpret_cast<const uint32_t*>(
+              static_cast<const T*>(a.q) + (r < wk.rows ? wk.token(r) * a.q_stride + static_cast<int64_t>(wk.head(r)) * HD : 0));
+          const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+          for (int ks = 0; ks < HD / 16; ++ks) {
+            qf[ks][h] = on ? __ldg(src + ks * 8 + tq) ^ flip : 0u;
+            qf[ks][2 + h] = on ? __ldg(src + ks * 8 + 4 + tq) ^ flip : 0u;
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = gr + 8 * h;
+          if (r >= wk.rows) rv[h] = RowView{0x7fffffff, 0, 0, false};
+          else if (wk.prefix) rv[h] = row_view(a, seq_ref(a, seq_of_token(a, wk.token(r))), wk.token(r));
+          else rv[h] = row_view(a, wk.s, wk.token(r));
+        }
+        // keys below this one are seen by both rows
+        const int seen_by_all = min(rv[0].last, rv[1].last);
+        float o[HD / 8][4];
+#pragma unroll
+        for (int n = 0; n < HD / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+        bool bad = !wk.prefix && wk.s.bad;
+        for (int i = 0; i < cnt; ++i, ++it) {
+          const int st = it % SM::kStages;
+          if (ok && !mbar_wait(&full[st], static_cast<uint32_t>(it / SM::kStages) & 1u, nullptr, 0)) {
+            if (a.status && lane == 0) atomicOr(a.status, DEX_ATTN_TIMEOUT);
+            ok = false;
+          }
+          if (!ok) continue;
+          bad |= bad_stage[st] != 0;
+          const int key0 = (wk.k.t0 + tile + i) * kRowsTile + warp * 16;   // this warp's 16 keys
+          uint8_t* kt = smem + st * SM::kStage;
+          uint8_t* vt = kt + SM::kHalf;
+          const int in0 = max(wk.k.lo - key0, 0), in1 = min(wk.k.hi - key0, 16);
+          if (in1 > in0) {
+            if (in0 > 0 || in1 < 16) {   // rows outside the segment hold anything: p = 0 must meet a finite v
+              for (int x = lane; x < 16 * HD / 8; x += 32) {
+                const int row = x / (HD / 8), ch = x % (HD / 8);
+                if (row < in0 || row >= in1)
+                  *reinterpret_cast<uint4*>(vt + (ch >> 3) * (kRowsTile * 128) + (warp * 16 + row) * 128 + (ch & 7) * 16) =
+                      make_uint4(0u, 0u, 0u, 0u);
+              }
+              fence_proxy_async_smem();   // before the stage's next copy
+              __syncwarp();
+            }
+            float s[2][4] = {};
+            const int kr = warp * 16 + (lane & 7) + ((lane >> 4) << 3);   // ldmatrix row: key
+#pragma unroll
+            for (int ks = 0; ks < HD / 16; ++ks) {
+              uint32_t kf[4];
+              const int ch = (ks & 3) * 2 + ((lane >> 3) & 1);
+              ldmatrix_x4(smem_u32(kt) + (ks >> 2) * (kRowsTile * 128) + kr * 128 + ((ch ^ (kr & 7)) << 4), kf);
+              mma_16816<T>(s[0], qf[ks], kf[0], kf[1]);
+              mma_16816<T>(s[1], qf[ks], kf[2], kf[3]);
+            }
+            float x[2][4];   // [row half][key: 2 tq, 2 tq + 1, + 8, + 9]
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              x[h][0] = s[0][2 * h] * c;
+              x[h][1] = s[0][2 * h + 1] * c;
+              x[h][2] = s[1][2 * h] * c;
+              x[h][3] = s[1][2 * h + 1] * c;
+            }
+            if (in0 > 0 || in1 < 16 || __any_sync(0xffffffffu, key0 + 15 > seen_by_all)) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int kk = 2 * tq + (e & 1) + (e >> 1) * 8;
+                  if (kk < in0 || kk >= in1 || !rv[h].sees(key0 + kk)) x[h][e] = -INFINITY;
+                }
+            }
+            float mx[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              mx[h] = fmaxf(fmaxf(x[h][0], x[h][1]), fmaxf(x[h][2], x[h][3]));
+              mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+              mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+              mx[h] = fmaxf(mx[h], m[h]);
+            }
+            if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float f = mx[h] > m[h] ? ex2(m[h] - mx[h]) : 1.0f;
+                m[h] = mx[h];
+                l[h] *= f;
+#pragma unroll
+                for (int n = 0; n < HD / 8; ++n) {
+                  o[n][2 * h] *= f;
+                  o[n][2 * h + 1] *= f;
+                }
+              }
+            }
+            uint32_t pf[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float base = m[h] > -INFINITY ? m[h] : 0.0f;
+              const float p0 = ex2(x[h][0] - base), p1 = ex2(x[h][1] - base), p2 = ex2(x[h][2] - base), p3 = ex2(x[h][3] - base);
+              l[h] += (p0 + p1) + (p2 + p3);
+              pf[h] = pack2<T>(p0, p1);
+              pf[2 + h] = pack2<T>(p2, p3);
+            }
+            const int vr = warp * 16 + (lane & 15);   // ldmatrix row: key
+#pragma unroll
+            for (int n = 0; n < HD / 16; ++n) {
+              uint32_t vf[4];
+              const int ch = (n & 3) * 2 + (lane >> 4);
+              ldmatrix_x4_trans(smem_u32(vt) + (n >> 2) * (kRowsTile * 128) + vr * 128 + ((ch ^ (vr & 7)) << 4), vf);
+              mma_16816<T>(o[2 * n], pf, vf[0], vf[1]);
+              mma_16816<T>(o[2 * n + 1], pf, vf[2], vf[3]);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty[st]);
+        }
+        // join the four warps: quarters of the columns in turn, so the order of addition is fixed
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+          l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+          if (bad || !ok) l[h] = quiet_nan();
+          if (tq == 0) join_ml[warp * kRowsMax + gr + 8 * h] = make_float2(m[h], l[h]);
+        }
+        named_bar_sync(1, kRowsWarps * 32);
+        float f[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float M = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < kRowsWarps; ++i) M = fmaxf(M, join_ml[i * kRowsMax + gr + 8 * h].x);
+          f[h] = M > -INFINITY ? ex2(m[h] - M) : 0.0f;
+        }
+#pragma unroll
+        for (int step = 0; step < kRowsWarps; ++step) {
+          // columns in units of 16: warp w takes those with index = (w + step) mod 4
+#pragma unroll
+          for (int n = 0; n < HD / 8; ++n) {
+            if (((n >> 1) & 3) == ((warp + step) & 3)) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float2* dst = reinterpret_cast<float2*>(join + (gr + 8 * h) * (HD + 4) + n * 8 + 2 * tq);
+                float2 v = make_float2(o[n][2 * h] * f[h], o[n][2 * h + 1] * f[h]);
+                if (step > 0) {
+                  const float2 prev = *dst;
+                  v.x += prev.x;
+                  v.y += prev.y;
+                }
+                *dst = v;
+              }
+            }
+          }
+          named_bar_sync(1, kRowsWarps * 32);
+        }
+        // results: thread takes HD/8 columns of row tid/8
+        {
+          const int r = tid >> 3, c0 = (tid & 7) * (HD / 8);
+          const bool starts = tile == 0, ends = tile + cnt == wk.k.nt;
+          // (M, L) of row r, from the lane that holds it
+          float2 mlr = make_float2(-INFINITY, 0.0f);
+          {
+            float2 mm[kRowsWarps];
+#pragma unroll
+            for (int i = 0; i < kRowsWarps; ++i) {
+              mm[i] = join_ml[i * kRowsMax + r];
+              mlr.x = fmaxf(mlr.x, mm[i].x);
+            }
+            const float base = mlr.x > -INFINITY ? mlr.x : 0.0f;
+#pragma unroll
+            for (int i = 0; i < kRowsWarps; ++i) mlr.y += mm[i].y * ex2(mm[i].x - base);
+          }
+          const float* src = join + r * (HD + 4) + c0;
+          if (r < wk.rows) {
+            const int t = wk.token(r), h = wk.head(r);
+            const int64_t row = static_cast<int64_t>(t) * a.H + h;
+            if (starts && ends && !w.joined) {
+              const float inv = isnan(mlr.y) ? mlr.y : mlr.y > 0.0f ? 1.0f / mlr.y : 0.0f;
+              T* dst = static_cast<T*>(a.out) + t * a.out_stride + static_cast<int64_t>(h) * HD + c0;
+#pragma unroll
+              for (int e = 0; e < HD / 8; e += 8) {
+                uint4 v;
+                v.x = pack2<T>(src[e] * inv, src[e + 1] * inv);
+                v.y = pack2<T>(src[e + 2] * inv, src[e + 3] * inv);
+                v.z = pack2<T>(src[e + 4] * inv, src[e + 5] * inv);
+                v.w = pack2<T>(src[e + 6] * inv, src[e + 7] * inv);
+                *reinterpret_cast<uint4*>(dst + e) = v;
+              }
+              if (a.lse && (tid & 7) == 0)
+                a.lse[row] = isnan(mlr.y) ? mlr.y : mlr.y > 0.0f ? (mlr.x + log2f(mlr.y)) * 0.6931471805599453f : -INFINITY;
+            } else {
+              const int64_t at = starts && ends ? row
+                                                : static_cast<int64_t>(2 * blockIdx.x + (starts ? 1 : 0)) * kRowsMax + r;
+              float* po = (starts && ends ? (wk.prefix ? w.pre_o : w.own_o) : w.part_o) + at * HD + c0;
+              float2* pm = (starts && ends ? (wk.prefix ? w.pre_ml : w.own_ml) : w.part_ml) + at;
+#pragma unroll
+              for (int e = 0; e < HD / 8; e += 4)
+                *reinterpret_cast<float4*>(po + e) = make_float4(src[e], src[e + 1], src[e + 2], src[e + 3]);
+              if ((tid & 7) == 0) *pm = mlr;
+            }
+          }
+          if (starts && tid == 0) {
+            int2* info = wk.prefix ? w.pre_info + wk.seg : w.own_info + wk.own_info_index();
+            *info = make_int2(blockIdx.x, sh.owner(g + static_cast<uint32_t>(wk.k.nt) - 1));
+          }
+        }
+        named_bar_sync(1, kRowsWarps * 32);   // join and join_ml are free again
+        g += static_cast<uint32_t>(cnt);
+        if (g < g1) wk.next();
+        tile = 0;
+      }
+    }
+  }
+  griddep_wait();   // a launch that follows must not overtake the one before this
+}
+
+// ============================================================================================
+// Joins the parts of each (token, query head): one warp per row.
+// ============================================================================================
+struct CombineWork {
+  SegWork own, pre;        // the kernels that computed own and prefix segments
+  int32_t own_rt, pre_rt;  // their rows per segment (16 or 256)
+  int32_t share;
+};
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ CombineWork w) {
+  __shared__ int found;
+  const PrefixAttnArgs& a = w.own.a;
+  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  if (tid == 0) found = a.kv.batch;
+  __syncthreads();
+  for (int b = tid; b < a.kv.batch; b += 128) {
+    const SeqRef s = seq_ref(a, b);
+    if (s.valid && t >= s.q0 && t < s.q0 + s.n) atomicMin(&found, b);
+  }
+  __syncthreads();
+  const int b = found, h = blockIdx.y * 4 + (tid >> 5);
+  griddep_wait();
+  if (b >= a.kv.batch || h >= a.H) return;
+  const SeqRef s = seq_ref(a, b);
+  const int kvh = h / a.G, hg = h % a.G;
+  const int64_t row = static_cast<int64_t>(t) * a.H + h;
+
+  // parts: [0, n_pre) of the prefix segment, then those of the own segment
+  const float *pre_o = nullptr, *own_o = nullptr;
+  const float2 *pre_ml = nullptr, *own_ml = nullptr;
+  int n_pre = 0, n_own = 0, pre_c0 = 0, own_c0 = 0, pre_r = 0, own_r = 0;
+  if (w.share) {
+    const int r = t * a.G + hg, rt = r / w.pre_rt;
+    const int2 info = w.pre.pre_info[rt * a.kv.KVH + kvh];
+    n_pre = info.y - info.x + 1;
+    pre_c0 = info.x;
+    pre_r = r - rt * w.pre_rt;
+    pre_o = n_pre == 1 ? w.pre.pre_o + row * HD : w.pre.part_o;
+    pre_ml = n_pre == 1 ? w.pre.pre_ml + row : w.pre.part_ml;
+  }
+  {
+    const int r = (t - s.q0) * a.G + hg, rt = r / w.own_rt;
+    const int r1 = min((rt + 1) * w.own_rt, s.n * a.G);
+    const int nt = w.own_rt == kRowsMax ? own_range<kRowsTile>(w.own, s, r1).nt : own_range<kTileKeys>(w.own, s, r1).nt;
+    if (nt > 0) {
+      const int idx = w.own_rt == kRowsMax ? Walker<kRowsMax, kRowsTile>::own_info_of(a, s.q0, b, rt, kvh)
+                                           : Walker<kTileRows, kTileKeys>::own_info_of(a, s.q0, b, rt, kvh);
+      const int2 info = w.own.own_info[idx];
+      n_own = info.y - info.x + 1;
+      own_c0 = info.x;
+      own_r = r - rt * w.own_rt;
+      if (n_own == 1 && !w.share) return;   // written where it was computed
+      own_o = n_own == 1 ? w.own.own_o + row * HD : w.own.part_o;
+      own_ml = n_own == 1 ? w.own.own_ml + row : w.own.part_ml;
+    }
+  }
+  auto part = [&](int i, const float*& po, const float2*& pm) {
+    const bool pre = i < n_pre;
+    const int k = pre ? i : i - n_pre, n = pre ? n_pre : n_own, c0 = pre ? pre_c0 : own_c0, rt = pre ? w.pre_rt : w.own_rt;
+    const int64_t at = n == 1 ? 0 : static_cast<int64_t>(2 * (c0 + k) + (k == 0 ? 1 : 0)) * rt + (pre ? pre_r : own_r);
+    po = (pre ? pre_o : own_o) + at * HD;
+    pm = (pre ? pre_ml : own_ml) + at;
+  };
+  const int n = n_pre + n_own;
+  constexpr int V = HD / 32;   // values per lane
+  float M = -INFINITY, L = 0.0f, o[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) o[e] = 0.0f;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    const float* po = nullptr;
+    if (i0 + lane < n) {
+      const float2* pm;
+      part(i0 + lane, po, pm);
+      ml = __ldcg(pm);
+    }
+    const float M1 = fmaxf(M, warp_max(ml.x));
+    const float base = M1 > -INFINITY ? M1 : 0.0f;
+    const float f = ex2(M - base), wgt = ex2(ml.x - base);
+    M = M1;
+    L = L * f + warp_sum(ml.y * wgt);   // a poisoned part is NaN whatever its weight
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] *= f;
+    const int cnt = min(32, n - i0);
+    for (int k = 0; k < cnt; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, wgt, k);
+      const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(po), k)) + lane * V;
+      if constexpr (V == 4) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+        o[0] = fmaf(x.x, wk, o[0]);
+        o[1] = fmaf(x.y, wk, o[1]);
+        o[2] = fmaf(x.z, wk, o[2]);
+        o[3] = fmaf(x.w, wk, o[3]);
+      } else {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+        o[0] = fmaf(x.x, wk, o[0]);
+        o[1] = fmaf(x.y, wk, o[1]);
+      }
+    }
+  }
+  const float inv = isnan(L) ? L : L > 0.0f ? 1.0f / L : 0.0f;
+  T* dst = static_cast<T*>(a.out) + t * a.out_stride + static_cast<int64_t>(h) * HD + lane * V;
+  if constexpr (V == 4) {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv));
+  } else {
+    *reinterpret_cast<uint32_t*>(dst) = pack2<T>(o[0] * inv, o[1] * inv);
+  }
+  if (a.lse && lane == 0) a.lse[row] = isnan(L) ? L : L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+}
+
+// ============================================================================================
+// Up to 256 rows per segment, on the 5th-generation tensor cores.  Two teams of four softmax warps
+// own one 128-row S / P tile and one O accumulator in TMEM each:
+//   S = Q K^T   (M = 128 rows, N = 128 keys, both operands in shared memory)
+//   O += P V    (P from TMEM, where it replaces S; V an MN-major operand as loaded)
+// One thread holds one row of S, so the softmax needs no exchange between threads.  With more than 128
+// rows the teams take one row tile each and share every K and V tile; with fewer they share the rows
+// and take alternate key tiles, and join at the segment's end.  Either way one team's softmax runs
+// while the tensor cores work for the other.
+// The running maximum of a row moves only when a score exceeds it by more than 2^8 (P then stays
+// within 2^8, which both 16-bit types hold), so O is rescaled rarely: a rescale reads and writes
+// all of it through registers between two MMAs.
+// ============================================================================================
+constexpr int kTileThreads = 384;   // two softmax teams; producer, MMA issuer and two idle warps
+constexpr float kRescale = 8.0f;
+
+template <int HD>
+struct TileSmem {
+  static constexpr uint32_t kBuf = kTileKeys * HD * 2;               // a Q, K or V tile
+  static constexpr int kStages = HD == 128 ? 5 : 8;
+  static constexpr uint32_t oQ = 0, oRing = 2 * kBuf;                // Q tiles (at a segment's end: O of team 1)
+  static constexpr uint32_t oMl = oRing + kStages * kBuf;            // float2 [128]
+  static constexpr uint32_t oBar = oMl + 128 * 8;
+  static constexpr uint32_t kBars = 2 * kStages + 9;
+  static constexpr uint32_t oMisc = oBar + kBars * 8;                // bad flags [stages], scratch [12], TMEM address
+  static constexpr uint32_t kTotal = oMisc + (kStages + 13) * 4 + 1024;
+  static_assert(kStages * kBuf >= kMaxBatch * 4, "tile counts use the ring before the first copy");
+};
+static_assert(TileSmem<128>::kTotal <= 227 * 1024, "tile_kernel shared memory");
+
+namespace {
+
+__device__ __forceinline__ uint32_t sw_off(int row, int col) {   // element offset in a [128 rows][HD] tile, 64-column halves
+  return static_cast<uint32_t>((col >> 6) * (128 * 128) + row * 128 + ((((col >> 3) & 7) ^ (row & 7)) << 4));
+}
+// K-major A or B descriptor: sw128_kmajor_desc of common.cuh; V as an MN-major B operand: 64 dims per
+// 128-byte row, keys 128 bytes apart in 1024-byte atoms, lbo between the 64-dim halves.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>((128u * 128u) >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+// kind::f16 with fp32 accumulators: type bits of A and B (0 fp16, 1 bf16), B MN-major or not
+__host__ __device__ constexpr uint32_t idesc(bool fp16, bool b_mn, int N) {
+  return (1u << 4) | (fp16 ? 0u : (1u << 7) | (1u << 10)) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (8u << 24);
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint64_t bdesc, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "l"(bdesc), "r"(id), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Bits i of columns [32 c, 32 c + 32) of a key tile at key0 that the row sees, within [lo, hi).
+__device__ __forceinline__ uint32_t range_bits(int from, int to) {   // bits from .. to - 1 of a word
+  from = max(from, 0);
+  to = min(to, 32);
+  if (to <= from) return 0u;
+  return (0xffffffffu >> (32 - (to - from))) << from;
+}
+__device__ __forceinline__ uint32_t seen_bits(const RowView& v, int lo, int hi, int at) {
+  uint32_t bits = range_bits(0, v.last >= at + 31 ? 32 : v.last - at + 1);
+  if (v.word) {
+    const int sh = v.first - at;   // column of the first query's position
+    if (sh >= 0) bits |= sh < 32 ? static_cast<uint32_t>(v.word << sh) : 0u;
+    else if (sh > -64) bits |= static_cast<uint32_t>(v.word >> -sh);
+  }
+  return bits & range_bits(lo - at, hi - at);
+}
+
+// Loads of a segment's cnt tiles: K of the first `ahead` tiles, then V of tile j and K of tile
+// j + ahead in turn -- the order in which the MMAs take them.
+__device__ __forceinline__ int v_load(int j, int cnt, int ahead) {   // index of V_j among the 2 cnt loads
+  const int a = min(ahead, cnt);
+  return a + j + min(j, cnt - a);
 }
 
 }  // namespace
 
-// One warp per (token, query head): every key in turn, the running maximum and sum of the
-// softmax in fp32, HD/32 dims per lane.
 template <typename T, int HD>
-__global__ void __launch_bounds__(128) prefix_attn_kernel(const __grid_constant__ PrefixAttnArgs a) {
-  using T2 = typename PairOf<T>::type;
-  constexpr int P = HD / 64;   // element pairs per lane
-  const int t = blockIdx.x, lane = threadIdx.x & 31;
-  const int h = blockIdx.y * 4 + (threadIdx.x >> 5);
-  if (h >= a.H) return;
-  const int b = seq_of_token(a, t);
-  if (b < 0) return;
-  const int q0 = __ldg(a.q_start + b), n = __ldg(a.q_start + b + 1) - q0, len = __ldg(a.seq_len + b);
-  if (q0 < 0 || n > a.max_q || q0 + n > a.n_tokens) {
-    if (a.status) atomicOr(a.status, DEX_ATTN_BAD_RANGE);
-    return;
-  }
-  bool bad = len < 0 || len > (a.kv.table_width << a.kv.page_shift);
-  if (bad && a.status) atomicOr(a.status, DEX_ATTN_BAD_RANGE);
-  const int first = len - n, p = first + (t - q0);   // first query position, this one's
-  const uint64_t tree = a.tree ? a.tree[t] : 0;
-  const int end = bad ? 0 : a.tree ? len : p + 1;
-  const int page_size = 1 << a.kv.page_shift;
-  const int kvh = h / a.G;
-  const T2* qp = reinterpret_cast<const T2*>(static_cast<const T*>(a.q) + t * a.q_stride + static_cast<int64_t>(h) * HD);
-  float2 q[P], o[P];
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    q[i] = pair_f32(qp[i * 32 + lane]);
-    o[i] = make_float2(0.f, 0.f);
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < end; ++j) {
-    if (a.tree && j >= first && !((tree >> (j - first)) & 1)) continue;
-    const int32_t* tab = j < a.prefix_len ? a.prefix_table : a.kv.table + static_cast<int64_t>(b) * a.kv.table_stride;
-    const int page = __ldg(tab + (j >> a.kv.page_shift));
-    if (page < 0 || page >= a.kv.n_pages) {
-      bad = true;
-      if (a.status) atomicOr(a.status, DEX_ATTN_BAD_PAGE);
-      break;
+__global__ void __launch_bounds__(kTileThreads, 1)
+    tile_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ SegWork w) {
+  using SM = TileSmem<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::oBar);
+  uint64_t* empty = full + SM::kStages;
+  uint64_t* q_full = empty + SM::kStages;   // [2] query tile of a team written
+  uint64_t* s_full = q_full + 2;            // [2] scores of a team's tile in TMEM
+  uint64_t* p_full = s_full + 2;            // [2] its probabilities in TMEM
+  uint64_t* pv_done = p_full + 2;           // [2] its PV complete
+  uint64_t* o_full = pv_done + 2;           // every MMA of the segment complete
+  volatile int* bad_stage = reinterpret_cast<volatile int*>(smem + SM::oMisc);
+  uint32_t* scratch = reinterpret_cast<uint32_t*>(smem + SM::oMisc) + SM::kStages;
+  uint32_t* tmem_slot = scratch + 12;
+  uint32_t* cum = reinterpret_cast<uint32_t*>(smem + SM::oRing);
+  const PrefixAttnArgs& a = w.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < SM::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
     }
-    const T* kr = static_cast<const T*>(a.kv.pages) + page * a.kv.page_stride +
-                  (static_cast<int64_t>(kvh) * page_size + (j & (page_size - 1))) * HD;
-    const T* vr = kr + static_cast<int64_t>(a.kv.KVH) * page_size * HD;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const float2 k = pair_f32(reinterpret_cast<const T2*>(kr)[i * 32 + lane]);
-      s = fmaf(q[i].x, k.x, fmaf(q[i].y, k.y, s));
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 128);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&pv_done[i], 1);
     }
-    s = warp_sum(s) * a.scale_log2;
-    const float m1 = fmaxf(m, s), c = exp2f(m - m1), w = exp2f(s - m1);
-    m = m1;
-    l = l * c + w;
+    mbar_init(o_full, 1);
+    fence_mbar_init();
+    tma_prefetch(&tm);
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);   // S / P of the teams: 128 columns each, then their O
+    tmem_relinquish();
+  }
+  Walker<kTileRows, kTileKeys> wk(w);
+  const uint32_t total = count_tiles<kTileRows, kTileKeys, kTileThreads>(wk, cum, scratch);
+  const Share sh(total, gridDim.x);
+  const bool work = blockIdx.x < sh.ctas;
+  const uint32_t g0 = work ? sh.begin(blockIdx.x) : 0, g1 = work ? sh.begin(blockIdx.x + 1) : 0;
+  int tile = work ? wk.find(g0, cum) : 0;
+  fence_proxy_async_smem();   // the counts in the ring are read before its first copy
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  griddep_launch_dependents();
+  const uint32_t tmem = *tmem_slot;
+  auto timed_out = [&] {
+    if (a.status) atomicOr(a.status, DEX_ATTN_TIMEOUT);
+  };
+
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ---------------- softmax teams: one row per thread ----------------
+    const int team = warp >> 2, r128 = tid & 127;
+    const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + static_cast<uint32_t>(team) * 128 + t_lane;
+    const uint32_t t_o = tmem + 256 + static_cast<uint32_t>(team) * 128 + t_lane;
+    const float c = a.scale_log2 == 0.0f ? 1.0f : fabsf(a.scale_log2);
+    float* join = reinterpret_cast<float*>(smem + SM::oQ);   // [HD][128] O of team 1
+    float2* join_ml = reinterpret_cast<float2*>(smem + SM::oMl);
+    uint32_t n_s = 0, n_seg = 0, base = 0;   // score tiles of this team, segments, loads so far
+    bool ok = true;
+    for (uint32_t g = g0; g < g1;) {
+      const int cnt = min(wk.k.nt - tile, static_cast<int>(g1 - g));
+      const bool alt = wk.rows <= 128;   // the teams share the rows and take alternate key tiles
+      const int ahead = alt ? 2 : 1;
+      const int r = alt ? r128 : team * 128 + r128;
+      const bool on = r < wk.rows;
+      if (!alt || team == 0) {
+        // the row's query, signed as the scale (zero for a zero scale and beyond the segment)
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const T*>(a.q) + (on ? wk.token(r) * a.q_stride + static_cast<int64_t>(wk.head(r)) * HD : 0));
+        const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+        const bool nz = on && a.scale_log2 != 0.0f;
+        uint8_t* dst = smem + SM::oQ + (alt ? 0 : team) * SM::kBuf;
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const float2 v = pair_f32(reinterpret_cast<const T2*>(vr)[i * 32 + lane]);
-      o[i].x = o[i].x * c + w * v.x;
-      o[i].y = o[i].y * c + w * v.y;
+        for (int e = 0; e < HD / 8; ++e) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (nz) {
+            v = __ldg(src + e);
+            v.x ^= flip;
+            v.y ^= flip;
+            v.z ^= flip;
+            v.w ^= flip;
+          }
+          *reinterpret_cast<uint4*>(dst + sw_off(r128, e * 8)) = v;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&q_full[team]);
+      }
+      RowView rv{0x7fffffff, 0, 0, false};
+      if (on) {
+        const int t = wk.token(r);
+        rv = wk.prefix ? row_view(a, seq_ref(a, seq_of_token(a, t)), t) : row_view(a, wk.s, t);
+      }
+      float m = -INFINITY, l = 0.0f;
+      bool bad = !wk.prefix && wk.s.bad, any = false;   // any: this team had a tile
+      for (int j = alt ? team : 0; j < cnt; j += ahead == 2 ? 2 : 1) {
+        if (ok && !mbar_wait(&s_full[team], n_s & 1u, nullptr, 0)) {
+          timed_out();
+          ok = false;
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32_nowait(t_s + q * 32, s[q]);
+        tmem_wait_ld();
+        const int key0 = (wk.k.t0 + tile + j) * kTileKeys;
+        const bool whole = wk.k.lo <= key0 && wk.k.hi >= key0 + kTileKeys;
+        if (!__all_sync(0xffffffffu, whole && rv.last >= key0 + kTileKeys - 1)) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t bits = seen_bits(rv, wk.k.lo, wk.k.hi, key0 + q * 32);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!(bits >> i & 1u)) s[q][i] = 0xff800000u;   // -inf
+          }
+        }
+        float mx4[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          mx4[q] = __uint_as_float(s[q][0]);
+#pragma unroll
+          for (int i = 1; i < 32; ++i) mx4[q] = fmaxf(mx4[q], __uint_as_float(s[q][i]));
+        }
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
+        const bool move = mx > m + kRescale || (m == -INFINITY && mx > -INFINITY);
+        if (__any_sync(0xffffffffu, move)) {
+          const float f = move ? ex2(m - mx) : 1.0f;
+          if (any) {
+            if (!mbar_wait(&pv_done[team], (n_s - 1) & 1u, nullptr, 0)) {
+              timed_out();
+              ok = false;
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < HD / 32; ++q) {
+              uint32_t o[32];
+              tmem_ld32_nowait(t_o + q * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st32(t_o + q * 32, o);
+            }
+          }
+          if (move) m = mx;
+          l *= f;
+        }
+        any = true;
+        const float sub = m > -INFINITY ? m : 0.0f;
+        float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {
+          uint32_t p[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int qq = q + (i >> 4), e = (2 * i) & 31;
+            const float p0 = ex2(fmaf(__uint_as_float(s[qq][e]), c, -sub));
+            const float p1 = ex2(fmaf(__uint_as_float(s[qq][e + 1]), c, -sub));
+            l4[i & 3] += p0 + p1;
+            p[i] = pack2<T>(p0, p1);
+          }
+          tmem_st32(t_s + q * 16, p);
+        }
+        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        // V of this tile: rows outside the segment hold anything, and P = 0 must meet a finite v
+        const uint32_t vl = base + static_cast<uint32_t>(v_load(j, cnt, ahead));
+        const int st = static_cast<int>(vl % SM::kStages);
+        if (!mbar_wait(&full[st], (vl / SM::kStages) & 1u, nullptr, 0)) {
+          timed_out();
+          ok = false;
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        bad |= bad_stage[st] != 0;
+        if (!whole) {
+          uint8_t* vt = smem + SM::oRing + st * SM::kBuf;
+          for (int x = r128; x < kTileKeys * HD / 8; x += 128) {
+            const int row = x / (HD / 8), ch = x % (HD / 8);
+            if (key0 + row < wk.k.lo || key0 + row >= wk.k.hi)
+              *reinterpret_cast<uint4*>(vt + (ch >> 3) * (128 * 128) + row * 128 + (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        mbar_arrive(&p_full[team]);
+        ++n_s;
+      }
+      // ---------------- the segment's result ----------------
+      if (ok && !mbar_wait(o_full, n_seg & 1u, nullptr, 0)) {
+        timed_out();
+        ok = false;
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+      if (bad || !ok) l = quiet_nan();
+      const bool read = ok && any;   // warp-uniform
+      if (alt && team == 1) {
+        join_ml[r128] = make_float2(m, l);
+        if (read) {
+#pragma unroll
+          for (int q = 0; q < HD / 32; ++q) {
+            uint32_t o[32];
+            tmem_ld32_nowait(t_o + q * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) join[(q * 32 + i) * 128 + r128] = __uint_as_float(o[i]);
+          }
+        }
+      }
+      if (alt) named_bar_sync(1, 256);
+      if (!alt || team == 0) {
+        float f0 = 1.0f, f1 = 0.0f;
+        const bool both = alt && cnt > 1;
+        if (both) {
+          const float2 other = join_ml[r128];
+          const float M = fmaxf(m, other.x), sub = M > -INFINITY ? M : 0.0f;
+          f0 = ex2(m - sub);
+          f1 = ex2(other.x - sub);
+          l = l * f0 + other.y * f1;
+          m = M;
+        }
+        const bool starts = tile == 0, ends = tile + cnt == wk.k.nt;
+        const bool direct = starts && ends && !w.joined;
+        const int t = on ? wk.token(r) : 0, h = on ? wk.head(r) : 0;
+        const int64_t row = static_cast<int64_t>(t) * a.H + h;
+        const int64_t at = starts && ends ? row : static_cast<int64_t>(2 * blockIdx.x + (starts ? 1 : 0)) * kTileRows + r;
+        float* po = (starts && ends ? (wk.prefix ? w.pre_o : w.own_o) : w.part_o) + at * HD;
+        const float inv = isnan(l) ? l : l > 0.0f ? 1.0f / l : 0.0f;
+        T* dst = static_cast<T*>(a.out) + t * a.out_stride + static_cast<int64_t>(h) * HD;
+#pragma unroll
+        for (int q = 0; q < HD / 32; ++q) {
+          uint32_t o[32];
+          if (read) {
+            tmem_ld32_nowait(t_o + q * 32, o);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0u;
+          }
+          float x[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]);
+          if (both) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = x[i] * f0 + join[(q * 32 + i) * 128 + r128] * f1;
+          }
+          if (on && direct) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+              *reinterpret_cast<uint4*>(dst + q * 32 + i) =
+                  make_uint4(pack2<T>(x[i] * inv, x[i + 1] * inv), pack2<T>(x[i + 2] * inv, x[i + 3] * inv),
+                             pack2<T>(x[i + 4] * inv, x[i + 5] * inv), pack2<T>(x[i + 6] * inv, x[i + 7] * inv));
+          } else if (on) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<float4*>(po + q * 32 + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+          }
+        }
+        if (on && direct) {
+          if (a.lse) a.lse[row] = isnan(l) ? l : l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        } else if (on) {
+          ((starts && ends ? (wk.prefix ? w.pre_ml : w.own_ml) : w.part_ml) + at)[0] = make_float2(m, l);
+        }
+        if (starts && tid == 0) {
+          int2* info = wk.prefix ? w.pre_info + wk.seg : w.own_info + wk.own_info_index();
+          *info = make_int2(blockIdx.x, sh.owner(g + static_cast<uint32_t>(wk.k.nt) - 1));
+        }
+      }
+      if (alt) named_bar_sync(2, 256);   // the query tiles may be written again
+      tc_fence_before();                 // O is read before the next segment's p_full
+      ++n_seg;
+      base += 2u * static_cast<uint32_t>(cnt);
+      g += static_cast<uint32_t>(cnt);
+      if (g < g1) wk.next();
+      tile = 0;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 8) {
+      // ---------------- producer ----------------
+      PageLoader<HD, kTileKeys> lk, lv;
+      lk.map = lv.map = &tm;
+      lk.kv = lv.kv = &a.kv;
+      lk.lane = lv.lane = lane;
+      uint32_t n_ld = 0;
+      bool ok = true;
+      auto load = [&](PageLoader<HD, kTileKeys>& ld, int which, int j) {
+        const int st = static_cast<int>(n_ld % SM::kStages), key0 = (wk.k.t0 + tile + j) * kTileKeys;
+        int first = 0, page;
+        const int n = ld.boxes(key0, wk.k.lo, wk.k.hi, first);
+        ld.prefetch(first, n);
+        if (n_ld >= SM::kStages && !mbar_wait(&empty[st], (n_ld / SM::kStages - 1) & 1u, nullptr, 0)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          if (lane == 0) timed_out();
+          return;
+        }
+        const bool bad = ld.page_of_lane(first, n, page);
+        if (lane == 0) {
+          bad_stage[st] = bad;
+          if (bad && a.status) atomicOr(a.status, DEX_ATTN_BAD_PAGE);
+          if (n > 0) mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(n * ld.box_rows() * HD * 2));
+          else mbar_arrive(&full[st]);
+        }
+        __syncwarp();
+        ld.load(smem + SM::oRing + st * SM::kBuf, &full[st], which, wk.kvh, key0, first, n, page);
+        ++n_ld;
+      };
+      for (uint32_t g = g0; g < g1 && ok;) {
+        const int cnt = min(wk.k.nt - tile, static_cast<int>(g1 - g));
+        const int ahead = wk.rows <= 128 ? 2 : 1;
+        const int32_t* tab = wk.prefix ? a.prefix_table : a.kv.table + static_cast<int64_t>(wk.b) * a.kv.table_stride;
+        lk.start(tab, wk.k.hi);
+        lv.start(tab, wk.k.hi);
+        for (int j = 0; j < min(ahead, cnt) && ok; ++j) load(lk, 0, j);
+        for (int j = 0; j < cnt && ok; ++j) {
+          load(lv, 1, j);
+          if (ok && j + ahead < cnt) load(lk, 0, j + ahead);
+        }
+        g += static_cast<uint32_t>(cnt);
+        if (g < g1) wk.next();
+        tile = 0;
+      }
+      if (!ok) {   // let the copies in flight land before the CTA goes
+        for (uint32_t i = n_ld > SM::kStages ? n_ld - SM::kStages : 0; i < n_ld; ++i)
+          mbar_wait(&full[i % SM::kStages], (i / SM::kStages) & 1u, nullptr, 0);
+      }
+    } else if (warp == 9 && lane == 0) {
+      // ---------------- MMA issuer ----------------
+      constexpr bool kFp16 = std::is_same<T, __half>::value;
+      constexpr uint32_t id_qk = idesc(kFp16, false, kTileKeys), id_pv = idesc(kFp16, true, HD);
+      const uint32_t q0 = smem_u32(smem + SM::oQ), ring = smem_u32(smem + SM::oRing);
+      uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_ld = 0;
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t n) {
+        if (ok && !mbar_wait(bar, n & 1u, nullptr, 0)) {
+          timed_out();
+          ok = false;
+        }
+        tc_fence_after();
+        return ok;
+      };
+      auto wait_load = [&] { return wait(&full[n_ld % SM::kStages], n_ld / SM::kStages); };
+      auto qk = [&](int team, int q, uint32_t kt) {
+#pragma unroll
+        for (int ks = 0; ks < HD / 16; ++ks) {
+          const uint32_t off = static_cast<uint32_t>((ks >> 2) * 128 * 128 + (ks & 3) * 32);
+          umma_bf16(tmem + static_cast<uint32_t>(team) * 128, sw128_kmajor_desc(q0 + static_cast<uint32_t>(q) * SM::kBuf + off),
+                    sw128_kmajor_desc(kt + off), id_qk, ks > 0 ? 1u : 0u);
+        }
+        umma_commit(&s_full[team]);
+      };
+      auto pv = [&](int team, uint32_t vt, bool first) {
+#pragma unroll
+        for (int ks = 0; ks < kTileKeys / 16; ++ks)
+          umma_ts(tmem + 256 + static_cast<uint32_t>(team) * 128, tmem + static_cast<uint32_t>(team) * 128 + ks * 8,
+                  mn_desc(vt + ks * 16 * 128), id_pv, first && ks == 0 ? 0u : 1u);
+        umma_commit(&pv_done[team]);
+      };
+      for (uint32_t g = g0; g < g1 && ok;) {
+        const int cnt = min(wk.k.nt - tile, static_cast<int>(g1 - g));
+        const bool alt = wk.rows <= 128;
+        if (!wait(&q_full[0], n_q[0]++)) break;
+        if (!alt && !wait(&q_full[1], n_q[1]++)) break;
+        const int ahead = alt ? 2 : 1;
+        for (int j = 0; j < min(ahead, cnt) && wait_load(); ++j) {
+          const uint32_t st = n_ld++ % SM::kStages, kt = ring + st * SM::kBuf;
+          if (alt) {
+            qk(j, 0, kt);
+          } else {
+            qk(0, 0, kt);
+            qk(1, 1, kt);
+          }
+          umma_commit(&empty[st]);
+        }
+        for (int j = 0; j < cnt && ok; ++j) {
+          if (!wait_load()) break;
+          const uint32_t vst = n_ld++ % SM::kStages, vt = ring + vst * SM::kBuf;
+          const bool more = j + ahead < cnt;
+          if (alt) {
+            const int team = j & 1;
+            if (!wait(&p_full[team], n_p[team]++)) break;
+            pv(team, vt, j < 2);
+            umma_commit(&empty[vst]);
+            if (more) {
+              if (!wait_load()) break;
+              const uint32_t st = n_ld++ % SM::kStages;
+              qk(team, 0, ring + st * SM::kBuf);
+              umma_commit(&empty[st]);
+            }
+          } else {
+            uint32_t st = 0;
+            for (int team = 0; team < 2 && ok; ++team) {
+              if (!wait(&p_full[team], n_p[team]++)) break;
+              pv(team, vt, j == 0);
+              if (team == 1) umma_commit(&empty[vst]);
+              if (more) {
+                if (team == 0) {
+                  if (!wait_load()) break;
+                  st = n_ld++ % SM::kStages;
+                }
+                qk(team, team, ring + st * SM::kBuf);
+                if (team == 1) umma_commit(&empty[st]);
+              }
+            }
+          }
+        }
+        umma_commit(o_full);
+        g += static_cast<uint32_t>(cnt);
+        if (g < g1) wk.next();
+        tile = 0;
+      }
+      if (!ok) {   // every MMA issued is complete before TMEM goes
+        umma_commit(o_full);
+        // the phase is not known after a break; the teams' bounded waits give the MMAs their time
+      }
     }
   }
-  const float inv = bad ? NAN : l > 0.f ? 1.0f / l : 0.f;
-  T2* op = reinterpret_cast<T2*>(static_cast<T*>(a.out) + t * a.out_stride + static_cast<int64_t>(h) * HD);
-#pragma unroll
-  for (int i = 0; i < P; ++i) op[i * 32 + lane] = pair_of(o[i].x * inv, o[i].y * inv, T2());
-  if (a.lse && lane == 0)
-    a.lse[static_cast<int64_t>(t) * a.H + h] = bad ? NAN : l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  griddep_wait();
 }
 
-size_t prefix_attention_workspace(const PrefixAttnArgs&) { return 0; }
+// ---- host ------------------------------------------------------------------------------------
+namespace {
 
-cudaError_t launch_prefix_attention(const PrefixAttnArgs& a, void*, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(a.n_tokens), static_cast<unsigned>((a.H + 3) / 4));
-  if (a.kv.fp16) {
-    if (a.kv.hd == 128) prefix_attn_kernel<__half, 128><<<grid, 128, 0, st>>>(a);
-    else prefix_attn_kernel<__half, 64><<<grid, 128, 0, st>>>(a);
-  } else {
-    if (a.kv.hd == 128) prefix_attn_kernel<__nv_bfloat16, 128><<<grid, 128, 0, st>>>(a);
-    else prefix_attn_kernel<__nv_bfloat16, 64><<<grid, 128, 0, st>>>(a);
+struct Plan {
+  bool share, prefix_tile, own_tile;   // prefix / own segments on tile_kernel
+  size_t o_rows_part, o_rows_ml, o_tile_part, o_tile_ml, o_pre, o_pre_ml, o_own, o_own_ml, o_pre_info, o_own_info, total;
+};
+
+constexpr int kSms = 152;   // of the sm_103 part: workspace sizes and grids, whatever device is current
+
+// Which kernel computes what.  Own segments of at most 16 rows go to rows_kernel.  The prefix is
+// shared when more than one sequence can have queries (n_tokens > max_q) and it fills a key tile; a
+// sequence whose own rows fill a 128-row tile gains nothing from sharing.
+Plan make_plan(const PrefixAttnArgs& a) {
+  Plan p = {};
+  const int64_t own_rows = static_cast<int64_t>(a.max_q) * a.G, all_rows = static_cast<int64_t>(a.n_tokens) * a.G;
+  p.own_tile = own_rows > kRowsMax;
+  p.share = a.prefix_len >= kRowsTile && a.n_tokens > a.max_q && own_rows < 128;
+  p.prefix_tile = p.share && all_rows > kRowsMax;
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at = up(at + bytes);
+    return o;
+  };
+  const size_t hd4 = static_cast<size_t>(a.kv.hd) * 4;
+  if (!p.own_tile || (p.share && !p.prefix_tile)) {
+    p.o_rows_part = take(size_t(2) * kRowsPerSm * kSms * kRowsMax * hd4);
+    p.o_rows_ml = take(size_t(2) * kRowsPerSm * kSms * kRowsMax * 8);
   }
-  return cudaGetLastError();
+  if (p.own_tile || p.prefix_tile) {
+    p.o_tile_part = take(size_t(2) * kSms * kTileRows * hd4);
+    p.o_tile_ml = take(size_t(2) * kSms * kTileRows * 8);
+  }
+  const size_t all = static_cast<size_t>(a.n_tokens) * a.H;
+  if (p.share) {
+    p.o_pre = take(all * hd4);
+    p.o_pre_ml = take(all * 8);
+    p.o_own = take(all * hd4);
+    p.o_own_ml = take(all * 8);
+    p.o_pre_info = take((all_rows / (p.prefix_tile ? kTileRows : kRowsMax) + 1) * a.kv.KVH * 8);
+  }
+  p.o_own_info = take((all_rows / (p.own_tile ? kTileRows : kRowsMax) + a.kv.batch + 2 +
+                       own_rows / (p.own_tile ? kTileRows : kRowsMax)) * a.kv.KVH * 8);
+  p.total = at;
+  return p;
+}
+
+// One function attribute per device, set before its first launch there.
+template <typename F>
+cudaError_t set_smem(F* func, uint32_t bytes, std::atomic<uint64_t>& done, int dev) {
+  if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess && dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  return e;
+}
+
+// 4-D map of the pages: head_dim, position in the page, (K|V) x K/V head, page; boxes of 64 dims x
+// `rows` positions, 128-byte swizzle.
+bool page_map(CUtensorMap* map, const PagedKv& kv, int rows) {
+  auto encode = tensor_map_encoder();
+  if (!encode) return false;
+  const uint64_t page = uint64_t(1) << kv.page_shift;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(kv.hd), page, static_cast<cuuint64_t>(2) * kv.KVH, static_cast<cuuint64_t>(kv.n_pages)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(kv.hd) * 2, page * kv.hd * 2, static_cast<cuuint64_t>(kv.page_stride) * 2};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1}, estr[4] = {1, 1, 1, 1};
+  return encode(map, kv.fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, kv.pages, dims, strides,
+                box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename K, typename... A>
+cudaError_t launch(K* kernel, dim3 grid, int threads, uint32_t smem, cudaStream_t st, bool pdl, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename T, int HD>
+cudaError_t launch_hd(const PrefixAttnArgs& a, const Plan& p, uint8_t* ws, cudaStream_t st, int dev, int n_sm) {
+  static std::atomic<uint64_t> rows_set{0}, tile_set{0};
+  SegWork base = {};
+  base.a = a;
+  base.share = p.share;
+  base.joined = p.share;
+  base.pre_o = reinterpret_cast<float*>(ws + p.o_pre);
+  base.pre_ml = reinterpret_cast<float2*>(ws + p.o_pre_ml);
+  base.own_o = reinterpret_cast<float*>(ws + p.o_own);
+  base.own_ml = reinterpret_cast<float2*>(ws + p.o_own_ml);
+  base.pre_info = reinterpret_cast<int2*>(ws + p.o_pre_info);
+  base.own_info = reinterpret_cast<int2*>(ws + p.o_own_info);
+  SegWork rows = base, tile = base;
+  rows.part_o = reinterpret_cast<float*>(ws + p.o_rows_part);
+  rows.part_ml = reinterpret_cast<float2*>(ws + p.o_rows_ml);
+  rows.do_own = !p.own_tile;
+  rows.do_prefix = p.share && !p.prefix_tile;
+  tile.part_o = reinterpret_cast<float*>(ws + p.o_tile_part);
+  tile.part_ml = reinterpret_cast<float2*>(ws + p.o_tile_ml);
+  tile.do_own = p.own_tile;
+  tile.do_prefix = p.prefix_tile;
+  const int page = 1 << a.kv.page_shift;
+  const int sms = n_sm < kSms ? n_sm : kSms;
+  bool pdl = false;
+  cudaError_t e = cudaSuccess;
+  if (tile.do_own || tile.do_prefix) {
+    CUtensorMap tm;
+    if (!page_map(&tm, a.kv, page < kTileKeys ? page : kTileKeys)) return cudaErrorInvalidValue;
+    e = set_smem(tile_kernel<T, HD>, TileSmem<HD>::kTotal, tile_set, dev);
+    if (e == cudaSuccess)
+      e = launch(tile_kernel<T, HD>, dim3(static_cast<unsigned>(sms)), kTileThreads, TileSmem<HD>::kTotal, st, pdl, tm, tile);
+    pdl = true;
+  }
+  if (e == cudaSuccess && (rows.do_own || rows.do_prefix)) {
+    CUtensorMap tm;
+    if (!page_map(&tm, a.kv, page < kRowsTile ? page : kRowsTile)) return cudaErrorInvalidValue;
+    e = set_smem(rows_kernel<T, HD>, RowsSmem<HD>::kTotal, rows_set, dev);
+    if (e == cudaSuccess)
+      e = launch(rows_kernel<T, HD>, dim3(static_cast<unsigned>(kRowsPerSm * sms)), kRowsThreads, RowsSmem<HD>::kTotal, st, pdl, tm, rows);
+    pdl = true;
+  }
+  if (e == cudaSuccess) {
+    CombineWork c = {};
+    c.own = p.own_tile ? tile : rows;
+    c.pre = p.prefix_tile ? tile : rows;
+    c.own_rt = p.own_tile ? kTileRows : kRowsMax;
+    c.pre_rt = p.prefix_tile ? kTileRows : kRowsMax;
+    c.share = p.share;
+    e = launch(combine_kernel<T, HD>, dim3(static_cast<unsigned>(a.n_tokens), static_cast<unsigned>((a.H + 3) / 4)), 128, 0, st, pdl, c);
+  }
+  return e;
+}
+
+}  // namespace
+
+size_t prefix_attention_workspace(const PrefixAttnArgs& a) { return make_plan(a).total; }
+
+cudaError_t launch_prefix_attention(const PrefixAttnArgs& a, void* workspace, cudaStream_t st) {
+  int dev = 0, n_sm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const Plan p = make_plan(a);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (a.kv.fp16)
+    return a.kv.hd == 128 ? launch_hd<__half, 128>(a, p, ws, st, dev, n_sm) : launch_hd<__half, 64>(a, p, ws, st, dev, n_sm);
+  return a.kv.hd == 128 ? launch_hd<__nv_bfloat16, 128>(a, p, ws, st, dev, n_sm)
+                        : launch_hd<__nv_bfloat16, 64>(a, p, ws, st, dev, n_sm);
 }
 
 }  // namespace dex
