@@ -12,6 +12,7 @@ namespace {
 
 constexpr int kAppendThreads = 256;
 constexpr int kAppendUnroll = 4;   // items a thread holds in flight
+constexpr int kAppendTokens = 8;   // tokens of a block, at most
 
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
@@ -36,89 +37,97 @@ __device__ __forceinline__ Vec8<T> load8(const T* p) {
 
 }  // namespace
 
-// One block per token.  An item is 16 elements of one head row: of q and k the eight pairs
-// (x_j, x_{j + HD/2}), j = 8c .. 8c+7, of v the elements 16c .. 16c+15, so each item is two
-// 16-byte loads and two 16-byte stores.  The HD/2 angles of the token are the same for all
-// its heads, so they are computed once per block; the rows are loaded before that.
+// A block takes up to kAppendTokens tokens.  An item is 16 elements of one head row: of q and k the
+// eight pairs (x_j, x_{j + HD/2}), j = 8c .. 8c+7, of v the elements 16c .. 16c+15, so each item is two
+// 16-byte loads and two 16-byte stores.  A thread keeps its c and walks the rows of the block's tokens,
+// four items in flight.  The HD/2 angles of a token are the same for all its heads and computed
+// once; the first rows are loaded before that, under the latency of the tokens' table entries.
 //
 // Angle: the turn of pair j at position r is r * theta^(-2j/HD) / 2 pi.  With the turn of position
 // 1 as a 64-bit fixed-point fraction, r times it modulo 2^64 is the fraction of a turn left after
 // whole turns, exactly -- an fp32 product r * frequency would be off by 2^-24 r radians (0.06 at
-// r = 10^6).  Its upper 32 bits as a signed number are half-turns in units of 2^-31.
+// r = 10^6).  Its upper 32 bits as a signed number are half-turns in units of 2^-31.  theta^(-2j/HD)
+// is the product of the powers theta^(-2 2^b / HD) over the bits b of j, each a 64-bit fraction.
 template <typename CT, typename IT, int HD>
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __grid_constant__ AppendArgs a) {
-  __shared__ float2 cs[HD / 2];
-  constexpr int kItems = HD / 16;   // items per head row
-  const int t = blockIdx.x, tid = threadIdx.x;
-  const int n_rows = (a.q ? a.H : 0) + 2 * a.kv.KVH, n_items = n_rows * kItems;
-  const int k_row0 = a.q ? a.H : 0, v_row0 = k_row0 + a.kv.KVH;
+  constexpr int kItems = HD / 16;                     // items per head row
+  constexpr int kStep = kAppendThreads / kItems;      // rows of one pass over the block
+  __shared__ __align__(16) float2 cs[kAppendTokens][HD / 2];
+  __shared__ int64_t dst_row[kAppendTokens];          // element offset of the token's K row, -1: skipped
+  const int tid = threadIdx.x, t0 = blockIdx.x * a.per_block, nt = min(a.per_block, a.n_tokens - t0);
+  const int n_rows = a.H + 2 * a.kv.KVH, v_row0 = a.H + a.kv.KVH;
+  const int c = tid % kItems, first = tid / kItems, n_all = nt * n_rows;
 
-  const int seq = __ldg(a.seq + t), pos = __ldg(a.pos + t);
-  const int rpos = a.rope_pos ? __ldg(a.rope_pos + t) : pos;
   Vec8<IT> lo[kAppendUnroll], hi[kAppendUnroll];
   auto load_items = [&](int base) {
 #pragma unroll
     for (int u = 0; u < kAppendUnroll; ++u) {
-      const int it = base + u * kAppendThreads + tid;
-      if (it >= n_items) break;
-      const int row = it / kItems, c = it % kItems;
-      const bool is_v = row >= v_row0;
-      const IT* src = row < k_row0 ? static_cast<const IT*>(a.q) + t * a.q_stride + static_cast<int64_t>(row) * HD
-                      : !is_v ? static_cast<const IT*>(a.k) + t * a.k_stride + static_cast<int64_t>(row - k_row0) * HD
-                              : static_cast<const IT*>(a.v) + t * a.v_stride + static_cast<int64_t>(row - v_row0) * HD;
-      lo[u] = load8(src + (is_v ? 16 * c : 8 * c));
-      hi[u] = load8(src + (is_v ? 16 * c + 8 : 8 * c + HD / 2));
+      const int p = base + u * kStep;
+      if (p < n_all) {
+        const int tk = p / n_rows, row = p - tk * n_rows;
+        const int64_t t = t0 + tk;
+        const IT* src = row < a.H      ? static_cast<const IT*>(a.q) + t * a.q_stride + static_cast<int64_t>(row) * HD
+                        : row < v_row0 ? static_cast<const IT*>(a.k) + t * a.k_stride + static_cast<int64_t>(row - a.H) * HD
+                                       : static_cast<const IT*>(a.v) + t * a.v_stride + static_cast<int64_t>(row - v_row0) * HD;
+        lo[u] = load8(src + (row < v_row0 ? 8 * c : 16 * c));
+        hi[u] = load8(src + (row < v_row0 ? 8 * c + HD / 2 : 16 * c + 8));
+      }
     }
   };
-  load_items(0);
+  load_items(first);
 
-  // destination: every thread checks for itself, so all of them agree without a barrier
   const int page_size = 1 << a.kv.page_shift;
-  const int pidx = pos >> a.kv.page_shift;
-  bool ok = seq >= 0 && seq < a.kv.batch && pos >= 0 && pidx < a.kv.table_width;
-  int page = -1;
-  if (ok) {
-    page = __ldg(a.kv.table + static_cast<int64_t>(seq) * a.kv.table_stride + pidx);
-    ok = page >= 0 && page < a.kv.n_pages;
+  if (tid < nt) {
+    const int seq = __ldg(a.seq + t0 + tid), pos = __ldg(a.pos + t0 + tid), pidx = pos >> a.kv.page_shift;
+    bool ok = seq >= 0 && seq < a.kv.batch && pos >= 0 && pidx < a.kv.table_width;
+    int page = -1;
+    if (ok) {
+      page = __ldg(a.kv.table + static_cast<int64_t>(seq) * a.kv.table_stride + pidx);
+      ok = page >= 0 && page < a.kv.n_pages;
+    }
+    dst_row[tid] = ok ? page * a.kv.page_stride + static_cast<int64_t>(pos & (page_size - 1)) * HD : -1;
+    if (!ok && seq != -1 && a.rejected) atomicAdd(a.rejected, 1);
   }
-  if (!ok) {
-    if (seq != -1 && tid == 0 && a.rejected) atomicAdd(a.rejected, 1);
-    return;
-  }
-  if (a.rotate && tid < HD / 2) {
-    const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(rpos)) * a.turn[tid];
-    float s, c;
-    sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f, &s, &c);   // 2^-31
-    cs[tid] = make_float2(c, s);
+  if (a.rotate) {
+    for (int x = tid; x < nt * (HD / 2); x += kAppendThreads) {
+      const int tk = x / (HD / 2), j = x % (HD / 2);
+      const int rpos = __ldg((a.rope_pos ? a.rope_pos : a.pos) + t0 + tk);
+      uint64_t turn = a.turn;
+#pragma unroll
+      for (int b = 0; b < 6; ++b)
+        if (j >> b & 1) turn = __umul64hi(turn, a.power[b]);
+      turn *= static_cast<uint64_t>(static_cast<int64_t>(rpos));
+      float s, co;
+      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f, &s, &co);   // 2^-31
+      cs[tk][j] = make_float2(co, s);
+    }
   }
   __syncthreads();
 
-  CT* kv_row = static_cast<CT*>(a.kv.pages) + page * a.kv.page_stride +
-               static_cast<int64_t>(pos & (page_size - 1)) * HD;
   const int64_t head_stride = static_cast<int64_t>(page_size) * HD;
-  for (int base = 0; base < n_items; base += kAppendUnroll * kAppendThreads) {
-    if (base) load_items(base);
+  for (int base = first; base < n_all; base += kAppendUnroll * kStep) {
+    if (base != first) load_items(base);
 #pragma unroll
     for (int u = 0; u < kAppendUnroll; ++u) {
-      const int it = base + u * kAppendThreads + tid;
-      if (it >= n_items) break;
-      const int row = it / kItems, c = it % kItems;
-      const bool is_v = row >= v_row0;
+      const int p = base + u * kStep;
+      if (p >= n_all) continue;
+      const int tk = p / n_rows, row = p - tk * n_rows;
+      const int64_t at = dst_row[tk];
+      if (at < 0) continue;
+      const bool is_v = row >= v_row0, turn = a.rotate && !is_v;
       Vec8<CT> x, y;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float p = to_f32(lo[u].v[i]), r = to_f32(hi[u].v[i]);
-        if (!is_v && a.rotate) {
-          const float2 w = cs[8 * c + i];
-          const float p0 = p;
-          p = p0 * w.x - r * w.y;
-          r = r * w.x + p0 * w.y;
-        }
-        from_f32(x.v[i], p);
-        from_f32(y.v[i], r);
+      for (int i = 0; i < 8; i += 2) {
+        // (cos, sin) of two pairs
+        const float4 w = turn ? *reinterpret_cast<const float4*>(&cs[tk][8 * c + i]) : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+        const float p0 = to_f32(lo[u].v[i]), r0 = to_f32(hi[u].v[i]), p1 = to_f32(lo[u].v[i + 1]), r1 = to_f32(hi[u].v[i + 1]);
+        from_f32(x.v[i], turn ? p0 * w.x - r0 * w.y : p0);
+        from_f32(y.v[i], turn ? r0 * w.x + p0 * w.y : r0);
+        from_f32(x.v[i + 1], turn ? p1 * w.z - r1 * w.w : p1);
+        from_f32(y.v[i + 1], turn ? r1 * w.z + p1 * w.w : r1);
       }
-      CT* dst = row < k_row0 ? static_cast<CT*>(a.q_out) + t * a.q_out_stride + static_cast<int64_t>(row) * HD
-                             : kv_row + (row - k_row0) * head_stride;   // V heads follow the K heads in a page
+      CT* dst = row < a.H ? static_cast<CT*>(a.q_out) + (t0 + tk) * a.q_out_stride + static_cast<int64_t>(row) * HD
+                          : static_cast<CT*>(a.kv.pages) + at + (row - a.H) * head_stride;   // V heads follow the K heads
       *reinterpret_cast<uint4*>(dst + (is_v ? 16 * c : 8 * c)) = *reinterpret_cast<const uint4*>(&x);
       *reinterpret_cast<uint4*>(dst + (is_v ? 16 * c + 8 : 8 * c + HD / 2)) = *reinterpret_cast<const uint4*>(&y);
     }
@@ -127,12 +136,15 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
 
 template <typename CT, typename IT>
 static cudaError_t launch_append_hd(const AppendArgs& a, cudaStream_t st) {
-  if (a.kv.hd == 128) paged_append_kernel<CT, IT, 128><<<a.n_tokens, kAppendThreads, 0, st>>>(a);
-  else paged_append_kernel<CT, IT, 64><<<a.n_tokens, kAppendThreads, 0, st>>>(a);
+  const int blocks = (a.n_tokens + a.per_block - 1) / a.per_block;
+  if (a.kv.hd == 128) paged_append_kernel<CT, IT, 128><<<blocks, kAppendThreads, 0, st>>>(a);
+  else paged_append_kernel<CT, IT, 64><<<blocks, kAppendThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
-cudaError_t launch_paged_append(const AppendArgs& a, cudaStream_t st) {
+cudaError_t launch_paged_append(AppendArgs a, cudaStream_t st) {
+  // one token per block until every SM has six blocks
+  a.per_block = a.n_tokens / (6 * 152) < 1 ? 1 : a.n_tokens / (6 * 152) > kAppendTokens ? kAppendTokens : a.n_tokens / (6 * 152);
   if (a.kv.fp16) return a.in_fp32 ? launch_append_hd<__half, float>(a, st) : launch_append_hd<__half, __half>(a, st);
   return a.in_fp32 ? launch_append_hd<__nv_bfloat16, float>(a, st)
                    : launch_append_hd<__nv_bfloat16, __nv_bfloat16>(a, st);
@@ -210,10 +222,10 @@ extern "C" int dex_paged_append(const dex_paged_kv* kv, const dex_append_args* a
   d.rotate = a->rope_theta != 0.0f;
   d.rejected = rejected;
   if (d.rotate) {
-    // 53-bit turns: at position 2^31 the angle is off by at most 2^-24 of a turn
-    const double step = pow(static_cast<double>(a->rope_theta), -2.0 / kv->head_dim);
-    double f = 0.15915494309189535;   // 1 / 2 pi
-    for (int j = 0; j < kv->head_dim / 2; ++j, f *= step) d.turn[j] = static_cast<uint64_t>(f * 18446744073709551616.0);
+    // powers of 53 bits: at position 2^31 the angle is off by at most 2^-23 of a turn
+    d.turn = static_cast<uint64_t>(0.15915494309189535 * 18446744073709551616.0);   // 2^64 / 2 pi
+    double f = pow(static_cast<double>(a->rope_theta), -2.0 / kv->head_dim);
+    for (int b = 0; b < 6; ++b, f *= f) d.power[b] = f < 1.0 ? static_cast<uint64_t>(f * 18446744073709551616.0) : ~uint64_t(0);
   }
   return dex::launch_paged_append(d, st) == cudaSuccess ? DEX_OK : DEX_ECUDA;
 }

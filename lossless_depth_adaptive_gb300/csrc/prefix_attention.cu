@@ -19,7 +19,7 @@
 // lengths give the same bits).
 //
 // Two kernels compute segments:
-//  * rows_kernel (at most 16 rows: single tokens, few heads): the keys are the work, so it is a
+//  * rows_kernel (at most 64 rows: single tokens, lattice nodes): the keys are the work, so it is a
 //    stream of K and V through a TMA ring into m16n8k16 MMAs on register fragments;
 //  * tile_kernel (up to 256 rows): 5th-generation tensor cores, two 128-row tiles per CTA that
 //    share every K and V tile.
@@ -38,10 +38,12 @@ namespace dex {
 namespace {
 
 constexpr int kRowsTile = 64;     // keys of a tile of rows_kernel
-constexpr int kRowsMax = 16;      // its query rows
-constexpr int kRowsWarps = 4;     // compute warps: each takes 16 keys of a tile
+constexpr int kRowsUnit = 16;     // its query rows come in m16 tiles
+constexpr int kRowsMax = 64;      // and at most this many
+constexpr int kRowsWarps = 4;     // compute warps
 constexpr int kRowsThreads = 32 * (kRowsWarps + 1);
 constexpr int kRowsPerSm = 2;     // resident CTAs
+constexpr int kSms = 152;         // of the sm_103 part: workspace sizes and grids, whatever device is current
 constexpr int kTileKeys = 128;    // keys of a tile of tile_kernel
 constexpr int kTileRows = 256;    // its query rows (two tiles of 128)
 constexpr int kMaxBatch = 1024;
@@ -53,10 +55,11 @@ struct SegWork {
   int32_t do_prefix;    // this kernel computes the prefix segments
   int32_t do_own;       // this kernel computes the own segments
   int32_t joined;       // 1: rows have prefix and own parts, so a finished segment is not yet the output
-  float* part_o;        // [2 * CTAs][rows][hd] parts of cut segments
+  int32_t slots;        // rows_kernel: segments posted ahead
+  float* part_o;        // parts of cut segments, two per CTA: [2 * CTAs][hd / 4][rows][4]
   float2* part_ml;      // [2 * CTAs][rows] (m, l)
-  float* pre_o;         // [n_tokens * H][hd] finished prefix segments (joined)
-  float2* pre_ml;
+  float* pre_o;         // finished prefix segments (joined): [KVH][hd / 4][n_tokens * G][4]
+  float2* pre_ml;       // [KVH][n_tokens * G]
   float* own_o;         // the same of own segments
   float2* own_ml;
   int2* pre_info;       // [prefix segments] first and last CTA
@@ -80,6 +83,23 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 __device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fffffff); }
+
+// Where the (m, l, O) of one row of a part lies: four head dims at o, the next four `step` floats on.
+struct PartRef {
+  float* o;
+  int64_t step;
+  float2* ml;
+};
+template <int HD>
+__device__ __forceinline__ PartRef slot_part(float* part_o, float2* part_ml, int slot, int rows, int r) {
+  return PartRef{part_o + (static_cast<int64_t>(slot) * (HD / 4) * rows + r) * 4, static_cast<int64_t>(rows) * 4,
+                 part_ml + static_cast<int64_t>(slot) * rows + r};
+}
+template <int HD>
+__device__ __forceinline__ PartRef joined_part(float* o, float2* ml, int kvh, int rows_all, int rg) {
+  return PartRef{o + (static_cast<int64_t>(kvh) * (HD / 4) * rows_all + rg) * 4, static_cast<int64_t>(rows_all) * 4,
+                 ml + static_cast<int64_t>(kvh) * rows_all + rg};
+}
 
 // ---- segments ------------------------------------------------------------------------------
 struct SeqRef {
@@ -119,6 +139,11 @@ __device__ __forceinline__ KeyRange own_range(const SegWork& w, const SeqRef& s,
     if (!w.share || s.bad) k.nt = 1;
   }
   return k;
+}
+
+// Index of an own segment's entry in own_info: distinct for the row tiles of sequences in order.
+__device__ __forceinline__ int own_info_of(const PrefixAttnArgs& a, int RT, int q0, int b, int rt, int kvh) {
+  return (static_cast<int>(static_cast<int64_t>(q0) * a.G / RT) + b + rt) * a.kv.KVH + kvh;
 }
 
 // The segment that holds a key tile, and the walk to the next one.
@@ -217,12 +242,7 @@ struct Walker {
   // Token, query head and position of row r of the segment.
   __device__ __forceinline__ int token(int r) const { return (prefix ? 0 : s.q0) + (r0 + r) / w.a.G; }
   __device__ __forceinline__ int head(int r) const { return kvh * w.a.G + (r0 + r) % w.a.G; }
-  __device__ __forceinline__ int own_info_index() const {
-    return own_info_of(w.a, s.q0, b, rt, kvh);
-  }
-  __device__ static __forceinline__ int own_info_of(const PrefixAttnArgs& a, int q0, int b, int rt, int kvh) {
-    return (static_cast<int>(static_cast<int64_t>(q0) * a.G / RT) + b + rt) * a.kv.KVH + kvh;
-  }
+  __device__ __forceinline__ int own_info_index() const { return own_info_of(w.a, RT, s.q0, b, rt, kvh); }
 };
 
 // The sequence whose queries can hold token t: the last b with q_start[b] <= t.
@@ -258,9 +278,11 @@ __device__ __forceinline__ RowView row_view(const PrefixAttnArgs& a, const SeqRe
 }
 
 // Own tiles of every sequence, as running totals in cum[0 .. batch]; the block's threads together.
-// scratch: 32 words.  Returns the total number of tiles of the kernel.
+// scratch: a word per warp.  token_seq (at most 64 tokens, or null) receives each token's sequence.
+// Returns the total number of tiles of the kernel.
 template <int RT, int TILE, int THREADS>
-__device__ __forceinline__ uint32_t count_tiles(const Walker<RT, TILE>& wk, uint32_t* cum, uint32_t* scratch) {
+__device__ __forceinline__ uint32_t count_tiles(const Walker<RT, TILE>& wk, uint32_t* cum, uint32_t* scratch,
+                                                int* token_seq = nullptr) {
   const SegWork& w = wk.w;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = w.do_own ? w.a.kv.batch : 0;
   uint32_t base = 0;
@@ -271,6 +293,8 @@ __device__ __forceinline__ uint32_t count_tiles(const Walker<RT, TILE>& wk, uint
       bool report;
       const SeqRef s = seq_ref(w.a, b, &report);
       n = wk.seq_tiles(s) * static_cast<uint32_t>(w.a.kv.KVH);
+      if (token_seq)
+        for (int i = 0; i < s.n; ++i) token_seq[s.q0 + i] = b;
       if (report && blockIdx.x == 0 && w.a.status) atomicOr(w.a.status, DEX_ATTN_BAD_RANGE);
     }
     uint32_t x = n;
@@ -304,6 +328,20 @@ struct Share {
     return static_cast<int>((static_cast<uint64_t>(g + 1) * ctas - 1) / total);
   }
 };
+
+// Barrier `id` of n threads; whether ok holds on all of them.
+__device__ __forceinline__ bool named_bar_and(int id, int n, bool ok) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.s32 p, %3, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
+      "selp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"(static_cast<int>(ok))
+      : "memory");
+  return r != 0;
+}
 
 // ---- device primitives beyond common.cuh ------------------------------------------------------
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, int w) {
@@ -384,35 +422,62 @@ struct PageLoader {
 }  // namespace
 
 // ============================================================================================
-// At most 16 rows per segment.  Four compute warps take 16 keys each of a 64-key tile: S (16 x 16)
-// and O (16 x HD) are register fragments, every warp keeps its own running (m, l), and the four join
-// once per segment through shared memory.  A fifth warp streams the pages by TMA (128-byte swizzle,
-// so the ldmatrix reads are free of bank conflicts).
+// At most 16 MT rows per segment (MT m16 tiles).  Four compute warps share every 64-key tile:
+//   S = Q K^T      warp w takes keys 16 w .. 16 w + 15 of the tile and all row tiles
+//   m, P           the row maxima meet in shared memory, so all warps keep the same running m
+//   O += P V       warp w takes head dims w HD/4 .. and all keys, P read back from shared memory
+// so K and V leave shared memory once, O needs no join and a segment ends with its l alone.  A fifth
+// warp does everything with a memory latency: it walks the segments, streams their pages by TMA
+// (128-byte swizzle: the ldmatrix reads are free of bank conflicts) and posts each segment's
+// description and query rows ahead of its tiles.
 // ============================================================================================
-template <int HD>
-struct RowsSmem {
-  static constexpr int kStages = HD == 128 ? 3 : 6;
-  static constexpr uint32_t kHalf = kRowsTile * HD * 2;          // a K or V tile
-  static constexpr uint32_t kStage = 2 * kHalf;
-  static constexpr uint32_t oJoin = kStages * kStage;            // float [16][HD + 4]
-  static constexpr uint32_t oMl = oJoin + kRowsMax * (HD + 4) * 4;   // float2 [4][16]
-  static constexpr uint32_t oCum = oMl + kRowsWarps * kRowsMax * 8;
-  static constexpr uint32_t oScr = oCum + kMaxBatch * 4;
-  static constexpr uint32_t oBar = oScr + 32 * 4;                // full, empty, bad flags
-  static constexpr uint32_t kTotal = oBar + 2 * kStages * 8 + kStages * 4 + 1024;
+struct SegDesc {
+  int32_t rows, mt, lo, hi, key0, cnt;      // key0: first tile's first position
+  int32_t kvh, flags;                       // kSeg* bits
+  int32_t info;                             // index into pre_info / own_info (first part only)
+  int32_t last_cta;                         // CTA of the segment's last tile
 };
-static_assert(2 * (RowsSmem<128>::kTotal + 1024) <= 228 * 1024, "two CTAs per SM");
+constexpr int kSegPrefix = 1, kSegStarts = 2, kSegEnds = 4, kSegBad = 8;
+struct RowDesc {
+  int32_t last, first, token, pad;
+  uint64_t word;
+};
 
-template <typename T, int HD>
+template <int HD, int MT>
+struct RowsSmem {
+  static constexpr int kRows = kRowsUnit * MT;                   // rows of a segment
+  static constexpr int kStages = HD == 128 ? 5 : 10;             // K or V tiles in the ring
+  static constexpr int kSlots = 4;                               // segments posted ahead, at most
+  static constexpr uint32_t kBuf = kRowsTile * HD * 2;
+  static constexpr uint32_t kQRow = HD * 2 + 16;                 // padded: ldmatrix without bank conflicts
+  static constexpr int kQRows = 64;                              // rows of all slots together
+  static constexpr uint32_t oP = kStages * kBuf;                 // [MT][16][64] probabilities, swizzled
+  static constexpr uint32_t oQ = oP + kRows * kRowsTile * 2;
+  static constexpr uint32_t oRow = oQ + kQRows * kQRow;          // RowDesc [64]
+  static constexpr uint32_t oMax = oRow + kQRows * sizeof(RowDesc);   // float [4][kRows]
+  static constexpr uint32_t oSum = oMax + kRowsWarps * kRows * 4;     // float [4][kRows]
+  static constexpr uint32_t oSeg = oSum + kRowsWarps * kRows * 4;     // SegDesc [kSlots]
+  static constexpr uint32_t oBar = oSeg + kSlots * sizeof(SegDesc);   // full, empty, seg_full, seg_empty
+  static constexpr uint32_t oMisc = oBar + (2 * kStages + 2 * kSlots) * 8;   // bad flags, scratch [32], sequence of a token [64]
+  static constexpr uint32_t kTotal = oMisc + (kStages + 32 + 64) * 4 + 1024;
+  static_assert(kStages * kBuf >= kMaxBatch * 4, "tile counts use the ring before the first copy");
+  static_assert(kRowsPerSm * (kTotal + 1024) <= 228 * 1024, "resident CTAs");
+};
+
+template <typename T, int HD, int MT>
 __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
     rows_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ SegWork w) {
-  using SM = RowsSmem<HD>;
+  using SM = RowsSmem<HD, MT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::oBar);
   uint64_t* empty = full + SM::kStages;
-  volatile int* bad_stage = reinterpret_cast<volatile int*>(empty + SM::kStages);
-  uint32_t* cum = reinterpret_cast<uint32_t*>(smem + SM::oCum);
+  uint64_t* seg_full = empty + SM::kStages;
+  uint64_t* seg_empty = seg_full + SM::kSlots;
+  volatile int* bad_stage = reinterpret_cast<volatile int*>(smem + SM::oMisc);
+  uint32_t* scratch = reinterpret_cast<uint32_t*>(smem + SM::oMisc) + SM::kStages;
+  int* token_seq = reinterpret_cast<int*>(scratch + 32);
+  uint32_t* cum = reinterpret_cast<uint32_t*>(smem);
   const PrefixAttnArgs& a = w.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -421,399 +486,332 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], kRowsWarps);
     }
+    for (int s = 0; s < SM::kSlots; ++s) {
+      mbar_init(&seg_full[s], 1);
+      mbar_init(&seg_empty[s], kRowsWarps);
+    }
     fence_mbar_init();
     tma_prefetch(&tm);
   }
-  Walker<kRowsMax, kRowsTile> wk(w);
-  const uint32_t total = count_tiles<kRowsMax, kRowsTile, kRowsThreads>(wk, cum, reinterpret_cast<uint32_t*>(smem + SM::oScr));
+  if (tid < 64) token_seq[tid] = -1;
+  __syncthreads();
+  Walker<SM::kRows, kRowsTile> wk(w);
+  const uint32_t total = count_tiles<SM::kRows, kRowsTile, kRowsThreads>(wk, cum, scratch, w.do_prefix ? token_seq : nullptr);
+  const Share sh(total, gridDim.x);
+  const bool work = blockIdx.x < sh.ctas;
+  const uint32_t g0 = work ? sh.begin(blockIdx.x) : 0, g1 = work ? sh.begin(blockIdx.x + 1) : 0;
+  const int tile0 = work ? wk.find(g0, cum) : 0;
+  fence_proxy_async_smem();   // the counts in the ring are read before its first copy
   __syncthreads();
   griddep_launch_dependents();
-  const Share sh(total, gridDim.x);
-  if (blockIdx.x < sh.ctas) {
-    const uint32_t g0 = sh.begin(blockIdx.x), g1 = sh.begin(blockIdx.x + 1);
-    int tile = wk.find(g0, cum);
-    if (warp == kRowsWarps) {
-      // ---------------- producer ----------------
-      PageLoader<HD, kRowsTile> ld;
-      ld.map = &tm;
-      ld.kv = &a.kv;
-      ld.lane = lane;
-      int it = 0;
-      bool ok = true;
-      for (uint32_t g = g0; g < g1 && ok; wk.next(), tile = 0) {
-        const int cnt = min(wk.k.nt - tile, static_cast<int>(g1 - g));
-        ld.start(wk.prefix ? a.prefix_table : a.kv.table + static_cast<int64_t>(wk.b) * a.kv.table_stride, wk.k.hi);
-        for (int i = 0; i < cnt; ++i, ++it) {
-          const int st = it % SM::kStages, key0 = (wk.k.t0 + tile + i) * kRowsTile;
-          int first = 0;
-          const int n = ld.boxes(key0, wk.k.lo, wk.k.hi, first);
-          ld.prefetch(first, n);
-          if (it >= SM::kStages && !mbar_wait(&empty[st], static_cast<uint32_t>(it / SM::kStages - 1) & 1u, nullptr, 0)) {
-            if (a.status && lane == 0) atomicOr(a.status, DEX_ATTN_TIMEOUT);
-            ok = false;
-            break;
+  const int n_slots = w.slots;   // 64 / (rows of the call's largest segment), at most kSlots
+
+  if (warp == kRowsWarps) {
+    // ---------------- producer ----------------
+    PageLoader<HD, kRowsTile> ld;
+    ld.map = &tm;
+    ld.kv = &a.kv;
+    ld.lane = lane;
+    uint32_t n_ld = 0, n_seg = 0;
+    int tile = tile0;
+    bool ok = true;
+    for (uint32_t g = g0; g < g1 && ok; ++n_seg) {
+      const int cnt = min(wk.k.nt - tile, static_cast<int>(g1 - g));
+      // the segment's description, row table and query rows
+      const int slot = static_cast<int>(n_seg % n_slots), row0 = slot * (SM::kQRows / n_slots);
+      if (n_seg >= static_cast<uint32_t>(n_slots) &&
+          !mbar_wait(&seg_empty[slot], (n_seg / n_slots - 1) & 1u, nullptr, 0))
+        ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        for (int r = lane; r < wk.rows; r += 32) {
+          const int t = wk.token(r);
+          SeqRef s = wk.s;
+          if (wk.prefix) {
+            const int b = token_seq[t];
+            if (b >= 0) s = seq_ref(a, b);
+            else s = SeqRef{0, 0, 0, false, false};
           }
-          uint8_t* dst = smem + st * SM::kStage;
-          int page;
-          const bool bad = ld.page_of_lane(first, n, page);
+          const RowView v = row_view(a, s, t);
+          RowDesc* d = reinterpret_cast<RowDesc*>(smem + SM::oRow) + row0 + r;
+          d->last = v.last;
+          d->first = v.first;
+          d->token = t;
+          d->word = v.word;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          SegDesc* d = reinterpret_cast<SegDesc*>(smem + SM::oSeg) + slot;
+          const bool starts = tile == 0, ends = tile + cnt == wk.k.nt;
+          d->rows = wk.rows;
+          d->mt = (wk.rows + kRowsUnit - 1) / kRowsUnit;
+          d->lo = wk.k.lo;
+          d->hi = wk.k.hi;
+          d->key0 = (wk.k.t0 + tile) * kRowsTile;
+          d->cnt = cnt;
+          d->kvh = wk.kvh;
+          d->flags = (wk.prefix ? kSegPrefix : 0) | (starts ? kSegStarts : 0) | (ends ? kSegEnds : 0) |
+                     (!wk.prefix && wk.s.bad ? kSegBad : 0);
+          d->info = wk.prefix ? wk.seg : wk.own_info_index();
+          d->last_cta = starts ? sh.owner(g + static_cast<uint32_t>(wk.k.nt) - 1) : 0;
+          mbar_arrive_expect_tx(&seg_full[slot], static_cast<uint32_t>(wk.rows * HD * 2));
+        }
+        __syncwarp();
+        for (int r = lane; r < wk.rows; r += 32)
+          bulk_load_1d(smem + SM::oQ + (row0 + r) * SM::kQRow,
+                       static_cast<const T*>(a.q) + wk.token(r) * a.q_stride + static_cast<int64_t>(wk.head(r)) * HD, HD * 2,
+                       &seg_full[slot]);
+        ld.start(wk.prefix ? a.prefix_table : a.kv.table + static_cast<int64_t>(wk.b) * a.kv.table_stride, wk.k.hi);
+      }
+      for (int i = 0; i < cnt && ok; ++i) {
+        const int key0 = (wk.k.t0 + tile + i) * kRowsTile;
+        int first = 0, page;
+        const int n = ld.boxes(key0, wk.k.lo, wk.k.hi, first);
+        ld.prefetch(first, n);
+        const bool bad = ld.page_of_lane(first, n, page);
+        for (int which = 0; which < 2 && ok; ++which) {
+          const int st = static_cast<int>(n_ld % SM::kStages);
+          if (n_ld >= SM::kStages && !mbar_wait(&empty[st], (n_ld / SM::kStages - 1) & 1u, nullptr, 0)) ok = false;
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           if (lane == 0) {
             bad_stage[st] = bad;
             if (bad && a.status) atomicOr(a.status, DEX_ATTN_BAD_PAGE);
-            if (n > 0) mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(n * ld.box_rows() * HD * 2 * 2));
+            if (n > 0) mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(n * ld.box_rows() * HD * 2));
             else mbar_arrive(&full[st]);
           }
           __syncwarp();
-          ld.load(dst, &full[st], 0, wk.kvh, key0, first, n, page);
-          ld.load(dst + SM::kHalf, &full[st], 1, wk.kvh, key0, first, n, page);
+          ld.load(smem + st * SM::kBuf, &full[st], which, wk.kvh, key0, first, n, page);
+          ++n_ld;
         }
-        g += static_cast<uint32_t>(cnt);
-        if (g >= g1) break;
       }
-      if (!ok) {   // let the copies in flight land before the CTA goes
-        for (int j = max(0, it - SM::kStages); j < it; ++j)
-          mbar_wait(&full[j % SM::kStages], static_cast<uint32_t>(j / SM::kStages) & 1u, nullptr, 0);
+      g += static_cast<uint32_t>(cnt);
+      if (g < g1) wk.next();
+      tile = 0;
+    }
+    if (!ok) {   // let the copies in flight land before the CTA goes
+      if (lane == 0 && a.status) atomicOr(a.status, DEX_ATTN_TIMEOUT);
+      for (uint32_t j = n_ld > SM::kStages ? n_ld - SM::kStages : 0; j < n_ld; ++j)
+        mbar_wait(&full[j % SM::kStages], (j / SM::kStages) & 1u, nullptr, 0);
+      for (uint32_t j = n_seg > static_cast<uint32_t>(n_slots) ? n_seg - n_slots : 0; j < n_seg; ++j)
+        mbar_wait(&seg_full[j % n_slots], (j / n_slots) & 1u, nullptr, 0);
+    }
+  } else {
+    // ---------------- compute ----------------
+    constexpr int NV = HD / 32;                // n8 tiles of this warp's head dims
+    const int gr = lane >> 2, tq = lane & 3;   // fragment row and column pair
+    float* smax = reinterpret_cast<float*>(smem + SM::oMax);
+    float* ssum = reinterpret_cast<float*>(smem + SM::oSum);
+    const uint32_t sp = smem_u32(smem + SM::oP);
+    const float c = a.scale_log2;
+    uint32_t n_ld = 0, n_seg = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t n) {
+      if (ok && !mbar_wait(bar, n & 1u, nullptr, 0)) {
+        if (a.status && lane == 0) atomicOr(a.status, DEX_ATTN_TIMEOUT);
+        ok = false;
       }
-    } else {
-      // ---------------- compute ----------------
-      const int gr = lane >> 2, tq = lane & 3;   // fragment row and column pair
-      float* join = reinterpret_cast<float*>(smem + SM::oJoin);
-      float2* join_ml = reinterpret_cast<float2*>(smem + SM::oMl);
-      const float c = a.scale_log2 == 0.0f ? 1.0f : fabsf(a.scale_log2);
-      int it = 0;
-      bool ok = true;
-      for (uint32_t g = g0; g < g1;) {
-        const int cnt = min(wk.k.nt - tile, static_cast<int>(g1 - g));
-        // query fragments: rows gr and gr + 8 (zero beyond the segment), signed as the scale
-        uint32_t qf[HD / 16][4];
-        RowView rv[2];
+    };
+    for (uint32_t g = g0; g < g1; ++n_seg) {
+      const int slot = static_cast<int>(n_seg % n_slots), row0 = slot * (SM::kQRows / n_slots);
+      wait(&seg_full[slot], n_seg / n_slots);
+      if (!named_bar_and(1, kRowsWarps * 32, ok)) break;   // all four warps or none: they meet at barriers
+      const SegDesc d = reinterpret_cast<const SegDesc*>(smem + SM::oSeg)[slot];
+      const RowDesc* rd = reinterpret_cast<const RowDesc*>(smem + SM::oRow) + row0;
+      const uint32_t sq = smem_u32(smem + SM::oQ) + row0 * SM::kQRow;
+      float o[MT][NV][4];
+      float m[MT][2], l[MT][2];
+      int seen_by_all = 0x7fffffff;   // keys up to this one are seen by every row of this thread
+#pragma unroll
+      for (int u = 0; u < MT; ++u) {
+#pragma unroll
+        for (int n = 0; n < NV; ++n) o[u][n][0] = o[u][n][1] = o[u][n][2] = o[u][n][3] = 0.0f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int r = gr + 8 * h;
-          const bool on = r < wk.rows && a.scale_log2 != 0.0f;
-          const uint32_t* src = reinterpret_cast<const uint32_t*>(
-              static_cast<const T*>(a.q) + (r < wk.rows ? wk.token(r) * a.q_stride + static_cast<int64_t>(wk.head(r)) * HD : 0));
-          const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
-#pragma unroll
-          for (int ks = 0; ks < HD / 16; ++ks) {
-            qf[ks][h] = on ? __ldg(src + ks * 8 + tq) ^ flip : 0u;
-            qf[ks][2 + h] = on ? __ldg(src + ks * 8 + 4 + tq) ^ flip : 0u;
-          }
+          const int r = u * 16 + gr + 8 * h;
+          m[u][h] = -INFINITY;
+          l[u][h] = 0.0f;
+          if (r < d.rows) seen_by_all = min(seen_by_all, rd[r].last);
         }
+      }
+      bool bad = d.flags & kSegBad;
+      for (int i = 0; i < d.cnt; ++i) {
+        // ---- scores of this warp's 16 keys ----
+        const int kst = static_cast<int>(n_ld % SM::kStages);
+        wait(&full[kst], n_ld / SM::kStages);
+        ++n_ld;
+        const int vst = static_cast<int>(n_ld % SM::kStages);
+        bad |= bad_stage[kst] != 0;
+        const int key0 = d.key0 + i * kRowsTile + warp * 16;
+        const int in0 = max(d.lo - key0, 0), in1 = min(d.hi - key0, 16);   // keys of the segment among them
+        const bool edge = in0 > 0 || in1 < 16;
+        const bool masked = __any_sync(0xffffffffu, edge || key0 + 15 > seen_by_all);
+        float x[MT][2][4];   // [row half][key: 2 tq, 2 tq + 1, + 8, + 9]
+        {
+          uint32_t kf[HD / 16][4];
+          const int kr = warp * 16 + (lane & 7) + ((lane >> 4) << 3);   // ldmatrix row: key
+          const uint32_t kt = smem_u32(smem + kst * SM::kBuf) + kr * 128;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = gr + 8 * h;
-          if (r >= wk.rows) rv[h] = RowView{0x7fffffff, 0, 0, false};
-          else if (wk.prefix) rv[h] = row_view(a, seq_ref(a, seq_of_token(a, wk.token(r))), wk.token(r));
-          else rv[h] = row_view(a, wk.s, wk.token(r));
-        }
-        // keys below this one are seen by both rows
-        const int seen_by_all = min(rv[0].last, rv[1].last);
-        float o[HD / 8][4];
+          for (int ks = 0; ks < HD / 16; ++ks)
+            ldmatrix_x4(kt + (ks >> 2) * (kRowsTile * 128) + ((((ks & 3) * 2 + ((lane >> 3) & 1)) ^ (kr & 7)) << 4), kf[ks]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty[kst]);
 #pragma unroll
-        for (int n = 0; n < HD / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-        bool bad = !wk.prefix && wk.s.bad;
-        for (int i = 0; i < cnt; ++i, ++it) {
-          const int st = it % SM::kStages;
-          if (ok && !mbar_wait(&full[st], static_cast<uint32_t>(it / SM::kStages) & 1u, nullptr, 0)) {
-            if (a.status && lane == 0) atomicOr(a.status, DEX_ATTN_TIMEOUT);
-            ok = false;
-          }
-          if (!ok) continue;
-          bad |= bad_stage[st] != 0;
-          const int key0 = (wk.k.t0 + tile + i) * kRowsTile + warp * 16;   // this warp's 16 keys
-          uint8_t* kt = smem + st * SM::kStage;
-          uint8_t* vt = kt + SM::kHalf;
-          const int in0 = max(wk.k.lo - key0, 0), in1 = min(wk.k.hi - key0, 16);
-          if (in1 > in0) {
-            if (in0 > 0 || in1 < 16) {   // rows outside the segment hold anything: p = 0 must meet a finite v
-              for (int x = lane; x < 16 * HD / 8; x += 32) {
-                const int row = x / (HD / 8), ch = x % (HD / 8);
-                if (row < in0 || row >= in1)
-                  *reinterpret_cast<uint4*>(vt + (ch >> 3) * (kRowsTile * 128) + (warp * 16 + row) * 128 + (ch & 7) * 16) =
-                      make_uint4(0u, 0u, 0u, 0u);
-              }
-              fence_proxy_async_smem();   // before the stage's next copy
-              __syncwarp();
-            }
-            float s[2][4] = {};
-            const int kr = warp * 16 + (lane & 7) + ((lane >> 4) << 3);   // ldmatrix row: key
+          for (int u = 0; u < MT; ++u) {
+            if (u >= d.mt) break;
+            float s[2][2][4] = {};   // two chains: even and odd k steps
 #pragma unroll
             for (int ks = 0; ks < HD / 16; ++ks) {
-              uint32_t kf[4];
-              const int ch = (ks & 3) * 2 + ((lane >> 3) & 1);
-              ldmatrix_x4(smem_u32(kt) + (ks >> 2) * (kRowsTile * 128) + kr * 128 + ((ch ^ (kr & 7)) << 4), kf);
-              mma_16816<T>(s[0], qf[ks], kf[0], kf[1]);
-              mma_16816<T>(s[1], qf[ks], kf[2], kf[3]);
+              uint32_t qf[4];
+              ldmatrix_x4(sq + (u * 16 + (lane & 15)) * SM::kQRow + ks * 32 + (lane >> 4) * 16, qf);
+              mma_16816<T>(s[ks & 1][0], qf, kf[ks][0], kf[ks][1]);
+              mma_16816<T>(s[ks & 1][1], qf, kf[ks][2], kf[ks][3]);
             }
-            float x[2][4];   // [row half][key: 2 tq, 2 tq + 1, + 8, + 9]
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              x[h][0] = s[0][2 * h] * c;
-              x[h][1] = s[0][2 * h + 1] * c;
-              x[h][2] = s[1][2 * h] * c;
-              x[h][3] = s[1][2 * h + 1] * c;
-            }
-            if (in0 > 0 || in1 < 16 || __any_sync(0xffffffffu, key0 + 15 > seen_by_all)) {
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
+              for (int e = 0; e < 4; ++e)
+                x[u][h][e] = (s[0][e >> 1][2 * h + (e & 1)] + s[1][e >> 1][2 * h + (e & 1)]) * c;
+              if (masked) {
+                const int r = u * 16 + gr + 8 * h;
+                RowView v{0x7fffffff, 0, 0, false};
+                if (r < d.rows) v.last = rd[r].last, v.first = rd[r].first, v.word = rd[r].word;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   const int kk = 2 * tq + (e & 1) + (e >> 1) * 8;
-                  if (kk < in0 || kk >= in1 || !rv[h].sees(key0 + kk)) x[h][e] = -INFINITY;
-                }
-            }
-            float mx[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              mx[h] = fmaxf(fmaxf(x[h][0], x[h][1]), fmaxf(x[h][2], x[h][3]));
-              mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-              mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-              mx[h] = fmaxf(mx[h], m[h]);
-            }
-            if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float f = mx[h] > m[h] ? ex2(m[h] - mx[h]) : 1.0f;
-                m[h] = mx[h];
-                l[h] *= f;
-#pragma unroll
-                for (int n = 0; n < HD / 8; ++n) {
-                  o[n][2 * h] *= f;
-                  o[n][2 * h + 1] *= f;
+                  if (kk < in0 || kk >= in1 || !v.sees(key0 + kk)) x[u][h][e] = -INFINITY;
                 }
               }
-            }
-            uint32_t pf[4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float base = m[h] > -INFINITY ? m[h] : 0.0f;
-              const float p0 = ex2(x[h][0] - base), p1 = ex2(x[h][1] - base), p2 = ex2(x[h][2] - base), p3 = ex2(x[h][3] - base);
-              l[h] += (p0 + p1) + (p2 + p3);
-              pf[h] = pack2<T>(p0, p1);
-              pf[2 + h] = pack2<T>(p2, p3);
-            }
-            const int vr = warp * 16 + (lane & 15);   // ldmatrix row: key
-#pragma unroll
-            for (int n = 0; n < HD / 16; ++n) {
-              uint32_t vf[4];
-              const int ch = (n & 3) * 2 + (lane >> 4);
-              ldmatrix_x4_trans(smem_u32(vt) + (n >> 2) * (kRowsTile * 128) + vr * 128 + ((ch ^ (vr & 7)) << 4), vf);
-              mma_16816<T>(o[2 * n], pf, vf[0], vf[1]);
-              mma_16816<T>(o[2 * n + 1], pf, vf[2], vf[3]);
+              float mx = fmaxf(fmaxf(x[u][h][0], x[u][h][1]), fmaxf(x[u][h][2], x[u][h][3]));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+              if (tq == 0) smax[warp * SM::kRows + u * 16 + gr + 8 * h] = mx;
             }
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&empty[st]);
         }
-        // join the four warps: quarters of the columns in turn, so the order of addition is fixed
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-          l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-          if (bad || !ok) l[h] = quiet_nan();
-          if (tq == 0) join_ml[warp * kRowsMax + gr + 8 * h] = make_float2(m[h], l[h]);
+        wait(&full[vst], n_ld / SM::kStages);
+        ++n_ld;
+        if (edge && ok) {   // rows outside the segment hold anything: p = 0 must meet a finite v
+          uint8_t* vt = smem + vst * SM::kBuf;
+          for (int z = lane; z < 16 * HD / 8; z += 32) {
+            const int row = z / (HD / 8), ch = z % (HD / 8);
+            if (row < in0 || row >= in1)
+              *reinterpret_cast<uint4*>(vt + (ch >> 3) * (kRowsTile * 128) + (warp * 16 + row) * 128 + (ch & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();   // before the stage's next copy
         }
         named_bar_sync(1, kRowsWarps * 32);
-        float f[2];
+        // ---- the running maximum, P of this warp's keys ----
+#pragma unroll
+        for (int u = 0; u < MT; ++u) {
+          if (u >= d.mt) break;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int r = u * 16 + gr + 8 * h;
+            float mx = m[u][h];
+#pragma unroll
+            for (int k = 0; k < kRowsWarps; ++k) mx = fmaxf(mx, smax[k * SM::kRows + r]);
+            const float base = mx > -INFINITY ? mx : 0.0f;
+            const float f = ex2(m[u][h] - base);
+            m[u][h] = mx;
+            const float p0 = ex2(x[u][h][0] - base), p1 = ex2(x[u][h][1] - base);
+            const float p2 = ex2(x[u][h][2] - base), p3 = ex2(x[u][h][3] - base);
+            l[u][h] = l[u][h] * f + ((p0 + p1) + (p2 + p3));
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+              o[u][n][2 * h] *= f;
+              o[u][n][2 * h + 1] *= f;
+            }
+            const uint32_t row = sp + u * 2048 + (gr + 8 * h) * 128 + tq * 4;
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(row + (((2 * warp) ^ gr) << 4)), "r"(pack2<T>(p0, p1)) : "memory");
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(row + (((2 * warp + 1) ^ gr) << 4)), "r"(pack2<T>(p2, p3)) : "memory");
+          }
+        }
+        named_bar_sync(1, kRowsWarps * 32);
+        // ---- O of this warp's head dims ----
+#pragma unroll
+        for (int ks = 0; ks < kRowsTile / 16; ++ks) {
+          uint32_t vf[NV / 2][4];
+          const int vr = ks * 16 + (lane & 15);   // ldmatrix row: key
+#pragma unroll
+          for (int n = 0; n < NV / 2; ++n) {
+            const int dim = warp * (HD / 4) + n * 16 + (lane >> 4) * 8;
+            ldmatrix_x4_trans(smem_u32(smem + vst * SM::kBuf) + (dim >> 6) * (kRowsTile * 128) + vr * 128 +
+                                  ((((dim >> 3) & 7) ^ (vr & 7)) << 4), vf[n]);
+          }
+#pragma unroll
+          for (int u = 0; u < MT; ++u) {
+            if (u >= d.mt) break;
+            uint32_t pf[4];
+            const int pr = lane & 15;
+            ldmatrix_x4(sp + u * 2048 + pr * 128 + (((2 * ks + (lane >> 4)) ^ (pr & 7)) << 4), pf);
+#pragma unroll
+            for (int n = 0; n < NV / 2; ++n) {
+              mma_16816<T>(o[u][2 * n], pf, vf[n][0], vf[n][1]);
+              mma_16816<T>(o[u][2 * n + 1], pf, vf[n][2], vf[n][3]);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[vst]);
+      }
+      // ---- the segment's result ----
+#pragma unroll
+      for (int u = 0; u < MT; ++u) {
+        if (u >= d.mt) break;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float M = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < kRowsWarps; ++i) M = fmaxf(M, join_ml[i * kRowsMax + gr + 8 * h].x);
-          f[h] = M > -INFINITY ? ex2(m[h] - M) : 0.0f;
+          l[u][h] += __shfl_xor_sync(0xffffffffu, l[u][h], 1);
+          l[u][h] += __shfl_xor_sync(0xffffffffu, l[u][h], 2);
+          if (bad || !ok) l[u][h] = quiet_nan();
+          if (tq == 0) ssum[warp * SM::kRows + u * 16 + gr + 8 * h] = l[u][h];
         }
-#pragma unroll
-        for (int step = 0; step < kRowsWarps; ++step) {
-          // columns in units of 16: warp w takes those with index = (w + step) mod 4
-#pragma unroll
-          for (int n = 0; n < HD / 8; ++n) {
-            if (((n >> 1) & 3) == ((warp + step) & 3)) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float2* dst = reinterpret_cast<float2*>(join + (gr + 8 * h) * (HD + 4) + n * 8 + 2 * tq);
-                float2 v = make_float2(o[n][2 * h] * f[h], o[n][2 * h + 1] * f[h]);
-                if (step > 0) {
-                  const float2 prev = *dst;
-                  v.x += prev.x;
-                  v.y += prev.y;
-                }
-                *dst = v;
-              }
-            }
-          }
-          named_bar_sync(1, kRowsWarps * 32);
-        }
-        // results: thread takes HD/8 columns of row tid/8
-        {
-          const int r = tid >> 3, c0 = (tid & 7) * (HD / 8);
-          const bool starts = tile == 0, ends = tile + cnt == wk.k.nt;
-          // (M, L) of row r, from the lane that holds it
-          float2 mlr = make_float2(-INFINITY, 0.0f);
-          {
-            float2 mm[kRowsWarps];
-#pragma unroll
-            for (int i = 0; i < kRowsWarps; ++i) {
-              mm[i] = join_ml[i * kRowsMax + r];
-              mlr.x = fmaxf(mlr.x, mm[i].x);
-            }
-            const float base = mlr.x > -INFINITY ? mlr.x : 0.0f;
-#pragma unroll
-            for (int i = 0; i < kRowsWarps; ++i) mlr.y += mm[i].y * ex2(mm[i].x - base);
-          }
-          const float* src = join + r * (HD + 4) + c0;
-          if (r < wk.rows) {
-            const int t = wk.token(r), h = wk.head(r);
-            const int64_t row = static_cast<int64_t>(t) * a.H + h;
-            if (starts && ends && !w.joined) {
-              const float inv = isnan(mlr.y) ? mlr.y : mlr.y > 0.0f ? 1.0f / mlr.y : 0.0f;
-              T* dst = static_cast<T*>(a.out) + t * a.out_stride + static_cast<int64_t>(h) * HD + c0;
-#pragma unroll
-              for (int e = 0; e < HD / 8; e += 8) {
-                uint4 v;
-                v.x = pack2<T>(src[e] * inv, src[e + 1] * inv);
-                v.y = pack2<T>(src[e + 2] * inv, src[e + 3] * inv);
-                v.z = pack2<T>(src[e + 4] * inv, src[e + 5] * inv);
-                v.w = pack2<T>(src[e + 6] * inv, src[e + 7] * inv);
-                *reinterpret_cast<uint4*>(dst + e) = v;
-              }
-              if (a.lse && (tid & 7) == 0)
-                a.lse[row] = isnan(mlr.y) ? mlr.y : mlr.y > 0.0f ? (mlr.x + log2f(mlr.y)) * 0.6931471805599453f : -INFINITY;
-            } else {
-              const int64_t at = starts && ends ? row
-                                                : static_cast<int64_t>(2 * blockIdx.x + (starts ? 1 : 0)) * kRowsMax + r;
-              float* po = (starts && ends ? (wk.prefix ? w.pre_o : w.own_o) : w.part_o) + at * HD + c0;
-              float2* pm = (starts && ends ? (wk.prefix ? w.pre_ml : w.own_ml) : w.part_ml) + at;
-#pragma unroll
-              for (int e = 0; e < HD / 8; e += 4)
-                *reinterpret_cast<float4*>(po + e) = make_float4(src[e], src[e + 1], src[e + 2], src[e + 3]);
-              if ((tid & 7) == 0) *pm = mlr;
-            }
-          }
-          if (starts && tid == 0) {
-            int2* info = wk.prefix ? w.pre_info + wk.seg : w.own_info + wk.own_info_index();
-            *info = make_int2(blockIdx.x, sh.owner(g + static_cast<uint32_t>(wk.k.nt) - 1));
-          }
-        }
-        named_bar_sync(1, kRowsWarps * 32);   // join and join_ml are free again
-        g += static_cast<uint32_t>(cnt);
-        if (g < g1) wk.next();
-        tile = 0;
       }
+      named_bar_sync(1, kRowsWarps * 32);
+      const bool starts = d.flags & kSegStarts, whole = starts && (d.flags & kSegEnds), prefix = d.flags & kSegPrefix;
+      const int rows_all = a.n_tokens * a.G;
+#pragma unroll
+      for (int u = 0; u < MT; ++u) {
+        if (u >= d.mt) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = u * 16 + gr + 8 * h;
+          if (r >= d.rows) continue;
+          float L = 0.0f;
+#pragma unroll
+          for (int k = 0; k < kRowsWarps; ++k) L += ssum[k * SM::kRows + r];
+          const int t = rd[r].token;
+          const int hg = r % a.G, head = d.kvh * a.G + hg;   // a segment of this kernel starts at a token's first head
+          const int dim = warp * (HD / 4) + 2 * tq;
+          if (whole && !w.joined) {
+            const float inv = isnan(L) ? L : L > 0.0f ? 1.0f / L : 0.0f;
+            T* dst = static_cast<T*>(a.out) + t * a.out_stride + static_cast<int64_t>(head) * HD + dim;
+#pragma unroll
+            for (int n = 0; n < NV; ++n)
+              *reinterpret_cast<uint32_t*>(dst + n * 8) = pack2<T>(o[u][n][2 * h] * inv, o[u][n][2 * h + 1] * inv);
+            if (a.lse && warp == 0 && tq == 0)
+              a.lse[static_cast<int64_t>(t) * a.H + head] =
+                  isnan(L) ? L : L > 0.0f ? (m[u][h] + log2f(L)) * 0.6931471805599453f : -INFINITY;
+          } else {
+            const PartRef p = whole ? joined_part<HD>(prefix ? w.pre_o : w.own_o, prefix ? w.pre_ml : w.own_ml, d.kvh, rows_all,
+                                                      t * a.G + hg)
+                                    : slot_part<HD>(w.part_o, w.part_ml, 2 * blockIdx.x + (starts ? 1 : 0), SM::kRows, r);
+#pragma unroll
+            for (int n = 0; n < NV; ++n)
+              *reinterpret_cast<float2*>(p.o + static_cast<int64_t>((dim + n * 8) >> 2) * p.step + (tq & 1) * 2) =
+                  make_float2(o[u][n][2 * h], o[u][n][2 * h + 1]);
+            if (warp == 0 && tq == 0) *p.ml = make_float2(m[u][h], L);
+          }
+        }
+      }
+      if (starts && tid == 0) (prefix ? w.pre_info : w.own_info)[d.info] = make_int2(blockIdx.x, d.last_cta);
+      g += static_cast<uint32_t>(d.cnt);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_empty[slot]);
     }
   }
   griddep_wait();   // a launch that follows must not overtake the one before this
-}
-
-// ============================================================================================
-// Joins the parts of each (token, query head): one warp per row.
-// ============================================================================================
-struct CombineWork {
-  SegWork own, pre;        // the kernels that computed own and prefix segments
-  int32_t own_rt, pre_rt;  // their rows per segment (16 or 256)
-  int32_t share;
-};
-
-template <typename T, int HD>
-__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ CombineWork w) {
-  __shared__ int found;
-  const PrefixAttnArgs& a = w.own.a;
-  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
-  if (tid == 0) found = a.kv.batch;
-  __syncthreads();
-  for (int b = tid; b < a.kv.batch; b += 128) {
-    const SeqRef s = seq_ref(a, b);
-    if (s.valid && t >= s.q0 && t < s.q0 + s.n) atomicMin(&found, b);
-  }
-  __syncthreads();
-  const int b = found, h = blockIdx.y * 4 + (tid >> 5);
-  griddep_wait();
-  if (b >= a.kv.batch || h >= a.H) return;
-  const SeqRef s = seq_ref(a, b);
-  const int kvh = h / a.G, hg = h % a.G;
-  const int64_t row = static_cast<int64_t>(t) * a.H + h;
-
-  // parts: [0, n_pre) of the prefix segment, then those of the own segment
-  const float *pre_o = nullptr, *own_o = nullptr;
-  const float2 *pre_ml = nullptr, *own_ml = nullptr;
-  int n_pre = 0, n_own = 0, pre_c0 = 0, own_c0 = 0, pre_r = 0, own_r = 0;
-  if (w.share) {
-    const int r = t * a.G + hg, rt = r / w.pre_rt;
-    const int2 info = w.pre.pre_info[rt * a.kv.KVH + kvh];
-    n_pre = info.y - info.x + 1;
-    pre_c0 = info.x;
-    pre_r = r - rt * w.pre_rt;
-    pre_o = n_pre == 1 ? w.pre.pre_o + row * HD : w.pre.part_o;
-    pre_ml = n_pre == 1 ? w.pre.pre_ml + row : w.pre.part_ml;
-  }
-  {
-    const int r = (t - s.q0) * a.G + hg, rt = r / w.own_rt;
-    const int r1 = min((rt + 1) * w.own_rt, s.n * a.G);
-    const int nt = w.own_rt == kRowsMax ? own_range<kRowsTile>(w.own, s, r1).nt : own_range<kTileKeys>(w.own, s, r1).nt;
-    if (nt > 0) {
-      const int idx = w.own_rt == kRowsMax ? Walker<kRowsMax, kRowsTile>::own_info_of(a, s.q0, b, rt, kvh)
-                                           : Walker<kTileRows, kTileKeys>::own_info_of(a, s.q0, b, rt, kvh);
-      const int2 info = w.own.own_info[idx];
-      n_own = info.y - info.x + 1;
-      own_c0 = info.x;
-      own_r = r - rt * w.own_rt;
-      if (n_own == 1 && !w.share) return;   // written where it was computed
-      own_o = n_own == 1 ? w.own.own_o + row * HD : w.own.part_o;
-      own_ml = n_own == 1 ? w.own.own_ml + row : w.own.part_ml;
-    }
-  }
-  auto part = [&](int i, const float*& po, const float2*& pm) {
-    const bool pre = i < n_pre;
-    const int k = pre ? i : i - n_pre, n = pre ? n_pre : n_own, c0 = pre ? pre_c0 : own_c0, rt = pre ? w.pre_rt : w.own_rt;
-    const int64_t at = n == 1 ? 0 : static_cast<int64_t>(2 * (c0 + k) + (k == 0 ? 1 : 0)) * rt + (pre ? pre_r : own_r);
-    po = (pre ? pre_o : own_o) + at * HD;
-    pm = (pre ? pre_ml : own_ml) + at;
-  };
-  const int n = n_pre + n_own;
-  constexpr int V = HD / 32;   // values per lane
-  float M = -INFINITY, L = 0.0f, o[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) o[e] = 0.0f;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    float2 ml = make_float2(-INFINITY, 0.0f);
-    const float* po = nullptr;
-    if (i0 + lane < n) {
-      const float2* pm;
-      part(i0 + lane, po, pm);
-      ml = __ldcg(pm);
-    }
-    const float M1 = fmaxf(M, warp_max(ml.x));
-    const float base = M1 > -INFINITY ? M1 : 0.0f;
-    const float f = ex2(M - base), wgt = ex2(ml.x - base);
-    M = M1;
-    L = L * f + warp_sum(ml.y * wgt);   // a poisoned part is NaN whatever its weight
-#pragma unroll
-    for (int e = 0; e < V; ++e) o[e] *= f;
-    const int cnt = min(32, n - i0);
-    for (int k = 0; k < cnt; ++k) {
-      const float wk = __shfl_sync(0xffffffffu, wgt, k);
-      const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(po), k)) + lane * V;
-      if constexpr (V == 4) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
-        o[0] = fmaf(x.x, wk, o[0]);
-        o[1] = fmaf(x.y, wk, o[1]);
-        o[2] = fmaf(x.z, wk, o[2]);
-        o[3] = fmaf(x.w, wk, o[3]);
-      } else {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
-        o[0] = fmaf(x.x, wk, o[0]);
-        o[1] = fmaf(x.y, wk, o[1]);
-      }
-    }
-  }
-  const float inv = isnan(L) ? L : L > 0.0f ? 1.0f / L : 0.0f;
-  T* dst = static_cast<T*>(a.out) + t * a.out_stride + static_cast<int64_t>(h) * HD + lane * V;
-  if constexpr (V == 4) {
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv));
-  } else {
-    *reinterpret_cast<uint32_t*>(dst) = pack2<T>(o[0] * inv, o[1] * inv);
-  }
-  if (a.lse && lane == 0) a.lse[row] = isnan(L) ? L : L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
 }
 
 // ============================================================================================
@@ -1149,8 +1147,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const bool direct = starts && ends && !w.joined;
         const int t = on ? wk.token(r) : 0, h = on ? wk.head(r) : 0;
         const int64_t row = static_cast<int64_t>(t) * a.H + h;
-        const int64_t at = starts && ends ? row : static_cast<int64_t>(2 * blockIdx.x + (starts ? 1 : 0)) * kTileRows + r;
-        float* po = (starts && ends ? (wk.prefix ? w.pre_o : w.own_o) : w.part_o) + at * HD;
+        const PartRef part = starts && ends ? joined_part<HD>(wk.prefix ? w.pre_o : w.own_o, wk.prefix ? w.pre_ml : w.own_ml,
+                                                              wk.kvh, a.n_tokens * a.G, t * a.G + h - wk.kvh * a.G)
+                                            : slot_part<HD>(w.part_o, w.part_ml, 2 * blockIdx.x + (starts ? 1 : 0), kTileRows, r);
         const float inv = isnan(l) ? l : l > 0.0f ? 1.0f / l : 0.0f;
         T* dst = static_cast<T*>(a.out) + t * a.out_stride + static_cast<int64_t>(h) * HD;
 #pragma unroll
@@ -1179,13 +1178,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           } else if (on) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<float4*>(po + q * 32 + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+              *reinterpret_cast<float4*>(part.o + (q * 8 + i / 4) * part.step) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
           }
         }
         if (on && direct) {
           if (a.lse) a.lse[row] = isnan(l) ? l : l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
         } else if (on) {
-          ((starts && ends ? (wk.prefix ? w.pre_ml : w.own_ml) : w.part_ml) + at)[0] = make_float2(m, l);
+          *part.ml = make_float2(m, l);
         }
         if (starts && tid == 0) {
           int2* info = wk.prefix ? w.pre_info + wk.seg : w.own_info + wk.own_info_index();
@@ -1351,17 +1350,151 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   griddep_wait();
 }
 
+// ============================================================================================
+// Joins the parts of the rows that have several: a block takes eight rows of one K/V head, a warp finds
+// the parts and weights of each, then every thread sums one float4 of one row over the parts.  Parts lie
+// as [head_dim / 4][rows][4], so eight rows of a part are 128 contiguous bytes.
+// ============================================================================================
+struct CombineWork {
+  SegWork own, pre;        // the kernels that computed own and prefix segments
+  int32_t own_rt, pre_rt;  // their rows per segment
+  int32_t own_tile;        // their keys per tile (own segments)
+  int32_t share;
+};
+// Part k of a row: the prefix parts (first CTA parts.x, number parts.y), then the own parts (z, w).
+template <int HD>
+__device__ __forceinline__ PartRef part_of(const CombineWork& w, const int4& parts, int k, int kvh, int rows_all, int rg,
+                                           int own_row) {
+  const bool pre = k < parts.y;
+  const int c0 = pre ? parts.x : parts.z, n = pre ? parts.y : parts.w, i = pre ? k : k - parts.y;
+  const SegWork& s = pre ? w.pre : w.own;
+  if (n == 1) return joined_part<HD>(pre ? s.pre_o : s.own_o, pre ? s.pre_ml : s.own_ml, kvh, rows_all, rg);
+  const int rt = pre ? w.pre_rt : w.own_rt;
+  return slot_part<HD>(s.part_o, s.part_ml, 2 * (c0 + i) + (i == 0 ? 1 : 0), rt, pre ? rg % rt : own_row);
+}
+constexpr int kCombineRows = 8;
+constexpr int kMaxParts = 2 * kRowsPerSm * kSms + 2;   // a row's prefix and own parts
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(HD * 2) combine_kernel(const __grid_constant__ CombineWork w) {
+  constexpr int kThreads = HD * 2;   // eight rows x HD / 4 columns
+  __shared__ int row_seq[kCombineRows];
+  __shared__ int4 row_part[kCombineRows];            // first CTA and number of prefix parts, of own parts
+  __shared__ int row_own[kCombineRows];              // row within its own segment
+  __shared__ float weight[kCombineRows][kMaxParts];
+  const PrefixAttnArgs& a = w.own.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, kvh = blockIdx.y;
+  const int rows_all = a.n_tokens * a.G, rg0 = blockIdx.x * kCombineRows;   // row: token * G + head within the K/V head
+  if (tid < kCombineRows) row_seq[tid] = -1;
+  __syncthreads();
+  {
+    const int t0 = rg0 / a.G, t1 = min(rg0 + kCombineRows - 1, rows_all - 1) / a.G;
+    for (int b = tid; b < a.kv.batch; b += kThreads) {
+      const SeqRef s = seq_ref(a, b);
+      if (!s.valid || s.q0 > t1 || s.q0 + s.n <= t0) continue;
+      for (int i = 0; i < kCombineRows; ++i) {
+        const int t = (rg0 + i) / a.G;
+        if (rg0 + i < rows_all && t >= s.q0 && t < s.q0 + s.n) row_seq[i] = b;
+      }
+    }
+  }
+  __syncthreads();
+  griddep_wait();
+  for (int i = warp; i < kCombineRows; i += kThreads / 32) {
+    const int b = row_seq[i], rg = rg0 + i;
+    int4 parts = make_int4(0, 0, 0, 0);
+    if (b >= 0) {
+      const SeqRef s = seq_ref(a, b);
+      if (w.share) {
+        const int2 info = w.pre.pre_info[rg / w.pre_rt * a.kv.KVH + kvh];
+        parts.x = info.x;
+        parts.y = info.y - info.x + 1;
+      }
+      const int r = rg - s.q0 * a.G, rt = r / w.own_rt, r1 = min((rt + 1) * w.own_rt, s.n * a.G);
+      const int nt = w.own_tile == kRowsTile ? own_range<kRowsTile>(w.own, s, r1).nt : own_range<kTileKeys>(w.own, s, r1).nt;
+      if (nt > 0) {
+        const int2 info = w.own.own_info[own_info_of(a, w.own_rt, s.q0, b, rt, kvh)];
+        parts.z = info.x;
+        parts.w = info.y - info.x + 1;
+      }
+      if (lane == 0) row_own[i] = r - rt * w.own_rt;
+      if (parts.w == 1 && !w.share) parts.w = 0;   // written where it was computed
+      const int n = min(parts.y + parts.w, kMaxParts);
+      float M = -INFINITY;
+      for (int k0 = 0; k0 < n; k0 += 32) {
+        const int k = k0 + lane;
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        if (k < n) {
+          const PartRef p = part_of<HD>(w, parts, k, kvh, rows_all, rg, r - rt * w.own_rt);
+          ml = __ldcg(p.ml);
+          weight[i][k] = ml.x;
+        }
+        M = fmaxf(M, warp_max(ml.x));
+      }
+      __syncwarp();
+      const float base = M > -INFINITY ? M : 0.0f;
+      float L = 0.0f;
+      for (int k = lane; k < n; k += 32) {
+        const PartRef p = part_of<HD>(w, parts, k, kvh, rows_all, rg, r - rt * w.own_rt);
+        const float wgt = ex2(weight[i][k] - base);
+        L += __ldcg(p.ml).y * wgt;   // a poisoned part is NaN whatever its weight
+        weight[i][k] = wgt;
+      }
+      L = warp_sum(L);
+      __syncwarp();
+      const float inv = isnan(L) ? L : L > 0.0f ? 1.0f / L : 0.0f;
+      for (int k = lane; k < n; k += 32) weight[i][k] *= inv;
+      if (a.lse && lane == 0 && n > 0)
+        a.lse[static_cast<int64_t>(rg / a.G) * a.H + kvh * a.G + rg % a.G] =
+            isnan(L) ? L : L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+      parts.w = n - parts.y;
+    }
+    if (lane == 0) row_part[i] = parts;
+  }
+  __syncthreads();
+  const int i = tid & (kCombineRows - 1), c4 = tid / kCombineRows, rg = rg0 + i;
+  const int4 parts = row_part[i];
+  const int n = parts.y + parts.w;
+  if (n <= 0) return;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const int ro = row_own[i];
+  constexpr int kUnroll = 8;
+  for (int k0 = 0; k0 < n; k0 += kUnroll) {
+    float4 x[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      x[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (k0 + u < n) {
+        const PartRef p = part_of<HD>(w, parts, k0 + u, kvh, rows_all, rg, ro);
+        x[u] = __ldcg(reinterpret_cast<const float4*>(p.o + static_cast<int64_t>(c4) * p.step));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const float wgt = k0 + u < n ? weight[i][k0 + u] : 0.0f;
+      o.x = fmaf(x[u].x, wgt, o.x);
+      o.y = fmaf(x[u].y, wgt, o.y);
+      o.z = fmaf(x[u].z, wgt, o.z);
+      o.w = fmaf(x[u].w, wgt, o.w);
+    }
+  }
+  T* dst = static_cast<T*>(a.out) + rg / a.G * a.out_stride + static_cast<int64_t>(kvh * a.G + rg % a.G) * HD + c4 * 4;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(o.x, o.y), pack2<T>(o.z, o.w));
+}
+
 // ---- host ------------------------------------------------------------------------------------
 namespace {
 
 struct Plan {
   bool share, prefix_tile, own_tile;   // prefix / own segments on tile_kernel
+  int rows_mt;                         // row tiles of rows_kernel: 1 or 4 (0: it has nothing to do)
+  int slots;
   size_t o_rows_part, o_rows_ml, o_tile_part, o_tile_ml, o_pre, o_pre_ml, o_own, o_own_ml, o_pre_info, o_own_info, total;
+  int own_rt() const { return own_tile ? kTileRows : rows_mt * kRowsUnit; }
+  int pre_rt() const { return prefix_tile ? kTileRows : rows_mt * kRowsUnit; }
 };
 
-constexpr int kSms = 152;   // of the sm_103 part: workspace sizes and grids, whatever device is current
-
-// Which kernel computes what.  Own segments of at most 16 rows go to rows_kernel.  The prefix is
+// Which kernel computes what.  Segments of at most 64 rows go to rows_kernel.  The prefix is
 // shared when more than one sequence can have queries (n_tokens > max_q) and it fills a key tile; a
 // sequence whose own rows fill a 128-row tile gains nothing from sharing.
 Plan make_plan(const PrefixAttnArgs& a) {
@@ -1370,6 +1503,9 @@ Plan make_plan(const PrefixAttnArgs& a) {
   p.own_tile = own_rows > kRowsMax;
   p.share = a.prefix_len >= kRowsTile && a.n_tokens > a.max_q && own_rows < 128;
   p.prefix_tile = p.share && all_rows > kRowsMax;
+  const int64_t most = p.share && !p.prefix_tile ? all_rows : p.own_tile ? 0 : own_rows;   // rows of a rows_kernel segment
+  p.rows_mt = most == 0 ? 0 : most <= kRowsUnit ? 1 : kRowsMax / kRowsUnit;
+  p.slots = most == 0 ? 1 : static_cast<int>(kRowsMax / ((most + kRowsUnit - 1) / kRowsUnit * kRowsUnit));
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -1378,9 +1514,9 @@ Plan make_plan(const PrefixAttnArgs& a) {
     return o;
   };
   const size_t hd4 = static_cast<size_t>(a.kv.hd) * 4;
-  if (!p.own_tile || (p.share && !p.prefix_tile)) {
-    p.o_rows_part = take(size_t(2) * kRowsPerSm * kSms * kRowsMax * hd4);
-    p.o_rows_ml = take(size_t(2) * kRowsPerSm * kSms * kRowsMax * 8);
+  if (p.rows_mt) {
+    p.o_rows_part = take(size_t(2) * kRowsPerSm * kSms * p.rows_mt * kRowsUnit * hd4);
+    p.o_rows_ml = take(size_t(2) * kRowsPerSm * kSms * p.rows_mt * kRowsUnit * 8);
   }
   if (p.own_tile || p.prefix_tile) {
     p.o_tile_part = take(size_t(2) * kSms * kTileRows * hd4);
@@ -1392,10 +1528,9 @@ Plan make_plan(const PrefixAttnArgs& a) {
     p.o_pre_ml = take(all * 8);
     p.o_own = take(all * hd4);
     p.o_own_ml = take(all * 8);
-    p.o_pre_info = take((all_rows / (p.prefix_tile ? kTileRows : kRowsMax) + 1) * a.kv.KVH * 8);
+    p.o_pre_info = take((all_rows / p.pre_rt() + 1) * a.kv.KVH * 8);
   }
-  p.o_own_info = take((all_rows / (p.own_tile ? kTileRows : kRowsMax) + a.kv.batch + 2 +
-                       own_rows / (p.own_tile ? kTileRows : kRowsMax)) * a.kv.KVH * 8);
+  p.o_own_info = take((all_rows / p.own_rt() + own_rows / p.own_rt() + a.kv.batch + 2) * a.kv.KVH * 8);
   p.total = at;
   return p;
 }
@@ -1440,7 +1575,7 @@ cudaError_t launch(K* kernel, dim3 grid, int threads, uint32_t smem, cudaStream_
 
 template <typename T, int HD>
 cudaError_t launch_hd(const PrefixAttnArgs& a, const Plan& p, uint8_t* ws, cudaStream_t st, int dev, int n_sm) {
-  static std::atomic<uint64_t> rows_set{0}, tile_set{0};
+  static std::atomic<uint64_t> rows1_set{0}, rows4_set{0}, tile_set{0};
   SegWork base = {};
   base.a = a;
   base.share = p.share;
@@ -1454,6 +1589,7 @@ cudaError_t launch_hd(const PrefixAttnArgs& a, const Plan& p, uint8_t* ws, cudaS
   SegWork rows = base, tile = base;
   rows.part_o = reinterpret_cast<float*>(ws + p.o_rows_part);
   rows.part_ml = reinterpret_cast<float2*>(ws + p.o_rows_ml);
+  rows.slots = p.slots;
   rows.do_own = !p.own_tile;
   rows.do_prefix = p.share && !p.prefix_tile;
   tile.part_o = reinterpret_cast<float*>(ws + p.o_tile_part);
@@ -1475,19 +1611,26 @@ cudaError_t launch_hd(const PrefixAttnArgs& a, const Plan& p, uint8_t* ws, cudaS
   if (e == cudaSuccess && (rows.do_own || rows.do_prefix)) {
     CUtensorMap tm;
     if (!page_map(&tm, a.kv, page < kRowsTile ? page : kRowsTile)) return cudaErrorInvalidValue;
-    e = set_smem(rows_kernel<T, HD>, RowsSmem<HD>::kTotal, rows_set, dev);
-    if (e == cudaSuccess)
-      e = launch(rows_kernel<T, HD>, dim3(static_cast<unsigned>(kRowsPerSm * sms)), kRowsThreads, RowsSmem<HD>::kTotal, st, pdl, tm, rows);
+    const dim3 grid(static_cast<unsigned>(kRowsPerSm * sms));
+    if (p.rows_mt == 1) {
+      e = set_smem(rows_kernel<T, HD, 1>, RowsSmem<HD, 1>::kTotal, rows1_set, dev);
+      if (e == cudaSuccess) e = launch(rows_kernel<T, HD, 1>, grid, kRowsThreads, RowsSmem<HD, 1>::kTotal, st, pdl, tm, rows);
+    } else {
+      e = set_smem(rows_kernel<T, HD, 4>, RowsSmem<HD, 4>::kTotal, rows4_set, dev);
+      if (e == cudaSuccess) e = launch(rows_kernel<T, HD, 4>, grid, kRowsThreads, RowsSmem<HD, 4>::kTotal, st, pdl, tm, rows);
+    }
     pdl = true;
   }
   if (e == cudaSuccess) {
     CombineWork c = {};
     c.own = p.own_tile ? tile : rows;
     c.pre = p.prefix_tile ? tile : rows;
-    c.own_rt = p.own_tile ? kTileRows : kRowsMax;
-    c.pre_rt = p.prefix_tile ? kTileRows : kRowsMax;
+    c.own_rt = p.own_rt();
+    c.pre_rt = p.pre_rt();
+    c.own_tile = p.own_tile ? kTileKeys : kRowsTile;
     c.share = p.share;
-    e = launch(combine_kernel<T, HD>, dim3(static_cast<unsigned>(a.n_tokens), static_cast<unsigned>((a.H + 3) / 4)), 128, 0, st, pdl, c);
+    const unsigned groups = static_cast<unsigned>((static_cast<int64_t>(a.n_tokens) * a.G + kCombineRows - 1) / kCombineRows);
+    e = launch(combine_kernel<T, HD>, dim3(groups, static_cast<unsigned>(a.kv.KVH)), HD * 2, 0, st, pdl, c);
   }
   return e;
 }
