@@ -296,12 +296,11 @@ struct AppendArgs {
   const int32_t *seq, *pos, *rope_pos;
   int32_t n_tokens, H, in_fp32, rotate;
   int32_t* rejected;
-  int32_t per_block;    // tokens of a block (set by the launcher)
   // the angle of pair 0 at position 1 in units of 2^-64 of a turn, and theta^(-2 2^b / hd) in
   // units of 2^-64
   uint64_t turn, power[6];
 };
-cudaError_t launch_paged_append(AppendArgs a, cudaStream_t st);
+cudaError_t launch_paged_append(const AppendArgs& a, cudaStream_t st);
 
 struct PrefixAttnArgs {
   PagedKv kv;

@@ -10,9 +10,7 @@ namespace dex {
 
 namespace {
 
-constexpr int kAppendThreads = 256;
-constexpr int kAppendUnroll = 4;   // items a thread holds in flight
-constexpr int kAppendTokens = 8;   // tokens of a block, at most
+constexpr int kAppendWarps = 8;   // of a block
 
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
@@ -37,11 +35,11 @@ __device__ __forceinline__ Vec8<T> load8(const T* p) {
 
 }  // namespace
 
-// A block takes up to kAppendTokens tokens.  An item is 16 elements of one head row: of q and k the
-// eight pairs (x_j, x_{j + HD/2}), j = 8c .. 8c+7, of v the elements 16c .. 16c+15, so each item is two
-// 16-byte loads and two 16-byte stores.  A thread keeps its c and walks the rows of the block's tokens,
-// four items in flight.  The HD/2 angles of a token are the same for all its heads and computed
-// once; the first rows are loaded before that, under the latency of the tokens' table entries.
+// A warp takes one token, or `rows` of its head rows when there are few tokens.  An item is eight pairs
+// (x_j, x_{j + HD/2}), j = 8c .. 8c+7, of one head row of q, k or v: two 16-byte loads and two
+// 16-byte stores of a 16-bit type.  A lane keeps its c, hence its eight (cos, sin), and walks the rows
+// with kUnroll items in flight; the first ones are loaded before the token's table entry is known.
+// Warps share nothing, so there is no block barrier.  Bound by memory: @@
 //
 // Angle: the turn of pair j at position r is r * theta^(-2j/HD) / 2 pi.  With the turn of position
 // 1 as a 64-bit fixed-point fraction, r times it modulo 2^64 is the fraction of a turn left after
@@ -49,49 +47,50 @@ __device__ __forceinline__ Vec8<T> load8(const T* p) {
 // r = 10^6).  Its upper 32 bits as a signed number are half-turns in units of 2^-31.  theta^(-2j/HD)
 // is the product of the powers theta^(-2 2^b / HD) over the bits b of j, each a 64-bit fraction.
 template <typename CT, typename IT, int HD>
-__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __grid_constant__ AppendArgs a) {
-  constexpr int kItems = HD / 16;                     // items per head row
-  constexpr int kStep = kAppendThreads / kItems;      // rows of one pass over the block
-  __shared__ __align__(16) float2 cs[kAppendTokens][HD / 2];
-  __shared__ int64_t dst_row[kAppendTokens];          // element offset of the token's K row, -1: skipped
-  const int tid = threadIdx.x, t0 = blockIdx.x * a.per_block, nt = min(a.per_block, a.n_tokens - t0);
-  const int n_rows = a.H + 2 * a.kv.KVH, v_row0 = a.H + a.kv.KVH;
-  const int c = tid % kItems, first = tid / kItems, n_all = nt * n_rows;
+__global__ void __launch_bounds__(32 * kAppendWarps) paged_append_kernel(const __grid_constant__ AppendArgs a, int rows) {
+  constexpr int kItems = HD / 16, kStep = 32 / kItems;   // items per head row, rows of one pass of the warp
+  constexpr int kUnroll = sizeof(IT) == 2 ? 4 : 2;
+  __shared__ __align__(16) float2 cs[kAppendWarps][HD / 2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % kItems;
+  const int t = blockIdx.x * kAppendWarps + warp;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (t >= a.n_tokens) return;
+  const int end = min((blockIdx.y + 1) * rows, a.H + 2 * a.kv.KVH), v_row0 = a.H + a.kv.KVH;
+  const IT* q = static_cast<const IT*>(a.q) + t * a.q_stride + 8 * c;
+  const IT* k = static_cast<const IT*>(a.k) + t * a.k_stride + 8 * c;
+  const IT* v = static_cast<const IT*>(a.v) + t * a.v_stride + 8 * c;
 
-  Vec8<IT> lo[kAppendUnroll], hi[kAppendUnroll];
-  auto load_items = [&](int base) {
+  Vec8<IT> lo[kUnroll], hi[kUnroll];
+  auto load_items = [&](int row0) {
 #pragma unroll
-    for (int u = 0; u < kAppendUnroll; ++u) {
-      const int p = base + u * kStep;
-      if (p < n_all) {
-        const int tk = p / n_rows, row = p - tk * n_rows;
-        const int64_t t = t0 + tk;
-        const IT* src = row < a.H      ? static_cast<const IT*>(a.q) + t * a.q_stride + static_cast<int64_t>(row) * HD
-                        : row < v_row0 ? static_cast<const IT*>(a.k) + t * a.k_stride + static_cast<int64_t>(row - a.H) * HD
-                                       : static_cast<const IT*>(a.v) + t * a.v_stride + static_cast<int64_t>(row - v_row0) * HD;
-        lo[u] = load8(src + (row < v_row0 ? 8 * c : 16 * c));
-        hi[u] = load8(src + (row < v_row0 ? 8 * c + HD / 2 : 16 * c + 8));
+    for (int u = 0; u < kUnroll; ++u) {
+      const int row = row0 + u * kStep;
+      if (row < end) {
+        const IT* src = row < a.H ? q + row * HD : row < v_row0 ? k + (row - a.H) * HD : v + (row - v_row0) * HD;
+        lo[u] = load8(src);
+        hi[u] = load8(src + HD / 2);
       }
     }
   };
+  const int first = blockIdx.y * rows + lane / kItems;
   load_items(first);
 
-  const int page_size = 1 << a.kv.page_shift;
-  if (tid < nt) {
-    const int seq = __ldg(a.seq + t0 + tid), pos = __ldg(a.pos + t0 + tid), pidx = pos >> a.kv.page_shift;
-    bool ok = seq >= 0 && seq < a.kv.batch && pos >= 0 && pidx < a.kv.table_width;
-    int page = -1;
-    if (ok) {
-      page = __ldg(a.kv.table + static_cast<int64_t>(seq) * a.kv.table_stride + pidx);
-      ok = page >= 0 && page < a.kv.n_pages;
-    }
-    dst_row[tid] = ok ? page * a.kv.page_stride + static_cast<int64_t>(pos & (page_size - 1)) * HD : -1;
-    if (!ok && seq != -1 && a.rejected) atomicAdd(a.rejected, 1);
+  const int seq = __ldg(a.seq + t), pos = __ldg(a.pos + t), pidx = pos >> a.kv.page_shift;
+  bool ok = seq >= 0 && seq < a.kv.batch && pos >= 0 && pidx < a.kv.table_width;
+  int page = -1;
+  if (ok) {
+    page = __ldg(a.kv.table + static_cast<int64_t>(seq) * a.kv.table_stride + pidx);
+    ok = page >= 0 && page < a.kv.n_pages;
   }
+  if (!ok) {
+    if (seq != -1 && a.rejected && lane == 0 && blockIdx.y == 0) atomicAdd(a.rejected, 1);
+    return;
+  }
+  float4 w[4];   // (cos, sin) of the lane's eight pairs
   if (a.rotate) {
-    for (int x = tid; x < nt * (HD / 2); x += kAppendThreads) {
-      const int tk = x / (HD / 2), j = x % (HD / 2);
-      const int rpos = __ldg((a.rope_pos ? a.rope_pos : a.pos) + t0 + tk);
+    const int rpos = a.rope_pos ? __ldg(a.rope_pos + t) : pos;
+    for (int j = lane; j < HD / 2; j += 32) {
       uint64_t turn = a.turn;
 #pragma unroll
       for (int b = 0; b < 6; ++b)
@@ -99,55 +98,75 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
       turn *= static_cast<uint64_t>(static_cast<int64_t>(rpos));
       float s, co;
       sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f, &s, &co);   // 2^-31
-      cs[tk][j] = make_float2(co, s);
+      cs[warp][j] = make_float2(co, s);
     }
-  }
-  __syncthreads();
-
-  const int64_t head_stride = static_cast<int64_t>(page_size) * HD;
-  for (int base = first; base < n_all; base += kAppendUnroll * kStep) {
-    if (base != first) load_items(base);
+    __syncwarp();
 #pragma unroll
-    for (int u = 0; u < kAppendUnroll; ++u) {
-      const int p = base + u * kStep;
-      if (p >= n_all) continue;
-      const int tk = p / n_rows, row = p - tk * n_rows;
-      const int64_t at = dst_row[tk];
-      if (at < 0) continue;
-      const bool is_v = row >= v_row0, turn = a.rotate && !is_v;
+    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(&cs[warp][8 * c + 2 * i]);
+  }
+
+  const int page_size = 1 << a.kv.page_shift, head_stride = page_size * HD;
+  CT* q_out = static_cast<CT*>(a.q_out) + t * a.q_out_stride + 8 * c;
+  CT* kv_out = static_cast<CT*>(a.kv.pages) + page * a.kv.page_stride + (pos & (page_size - 1)) * HD + 8 * c;
+  for (int row0 = first; row0 < end; row0 += kUnroll * kStep) {
+    if (row0 != first) load_items(row0);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int row = row0 + u * kStep;
+      if (row >= end) continue;
       Vec8<CT> x, y;
+      if (a.rotate && row < v_row0) {
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        // (cos, sin) of two pairs
-        const float4 w = turn ? *reinterpret_cast<const float4*>(&cs[tk][8 * c + i]) : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
-        const float p0 = to_f32(lo[u].v[i]), r0 = to_f32(hi[u].v[i]), p1 = to_f32(lo[u].v[i + 1]), r1 = to_f32(hi[u].v[i + 1]);
-        from_f32(x.v[i], turn ? p0 * w.x - r0 * w.y : p0);
-        from_f32(y.v[i], turn ? r0 * w.x + p0 * w.y : r0);
-        from_f32(x.v[i + 1], turn ? p1 * w.z - r1 * w.w : p1);
-        from_f32(y.v[i + 1], turn ? r1 * w.z + p1 * w.w : r1);
+        for (int i = 0; i < 4; ++i) {
+          const float p0 = to_f32(lo[u].v[2 * i]), r0 = to_f32(hi[u].v[2 * i]);
+          const float p1 = to_f32(lo[u].v[2 * i + 1]), r1 = to_f32(hi[u].v[2 * i + 1]);
+          from_f32(x.v[2 * i], p0 * w[i].x - r0 * w[i].y);
+          from_f32(y.v[2 * i], r0 * w[i].x + p0 * w[i].y);
+          from_f32(x.v[2 * i + 1], p1 * w[i].z - r1 * w[i].w);
+          from_f32(y.v[2 * i + 1], r1 * w[i].z + p1 * w[i].w);
+        }
+      } else if constexpr (sizeof(IT) == 2) {
+        x = *reinterpret_cast<const Vec8<CT>*>(&lo[u]);
+        y = *reinterpret_cast<const Vec8<CT>*>(&hi[u]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          from_f32(x.v[i], to_f32(lo[u].v[i]));
+          from_f32(y.v[i], to_f32(hi[u].v[i]));
+        }
       }
-      CT* dst = row < a.H ? static_cast<CT*>(a.q_out) + (t0 + tk) * a.q_out_stride + static_cast<int64_t>(row) * HD
-                          : static_cast<CT*>(a.kv.pages) + at + (row - a.H) * head_stride;   // V heads follow the K heads
-      *reinterpret_cast<uint4*>(dst + (is_v ? 16 * c : 8 * c)) = *reinterpret_cast<const uint4*>(&x);
-      *reinterpret_cast<uint4*>(dst + (is_v ? 16 * c + 8 : 8 * c + HD / 2)) = *reinterpret_cast<const uint4*>(&y);
+      // the V heads of a page follow its K heads
+      CT* dst = row < a.H ? q_out + row * HD : kv_out + static_cast<int64_t>(row - a.H) * head_stride;
+      *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(&x);
+      *reinterpret_cast<uint4*>(dst + HD / 2) = *reinterpret_cast<const uint4*>(&y);
     }
   }
 }
 
-template <typename CT, typename IT>
-static cudaError_t launch_append_hd(const AppendArgs& a, cudaStream_t st) {
-  const int blocks = (a.n_tokens + a.per_block - 1) / a.per_block;
-  if (a.kv.hd == 128) paged_append_kernel<CT, IT, 128><<<blocks, kAppendThreads, 0, st>>>(a);
-  else paged_append_kernel<CT, IT, 64><<<blocks, kAppendThreads, 0, st>>>(a);
-  return cudaGetLastError();
+template <typename CT, typename IT, int HD>
+static cudaError_t launch_append(const AppendArgs& a, cudaStream_t st) {
+  // a warp per token once that fills the GPU with 16 warps per SM, 16 rows per warp below: @@
+  const int n_rows = a.H + 2 * a.kv.KVH, rows = a.n_tokens >= 16 * 152 ? n_rows : 16;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((a.n_tokens + kAppendWarps - 1) / kAppendWarps),
+                     static_cast<unsigned>((n_rows + rows - 1) / rows));
+  cfg.blockDim = dim3(32 * kAppendWarps);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_append_kernel<CT, IT, HD>, a, rows);
+}
+template <typename CT>
+static cudaError_t launch_append_in(const AppendArgs& a, cudaStream_t st) {
+  if (a.in_fp32) return a.kv.hd == 128 ? launch_append<CT, float, 128>(a, st) : launch_append<CT, float, 64>(a, st);
+  return a.kv.hd == 128 ? launch_append<CT, CT, 128>(a, st) : launch_append<CT, CT, 64>(a, st);
 }
 
-cudaError_t launch_paged_append(AppendArgs a, cudaStream_t st) {
-  // one token per block until every SM has six blocks
-  a.per_block = a.n_tokens / (6 * 152) < 1 ? 1 : a.n_tokens / (6 * 152) > kAppendTokens ? kAppendTokens : a.n_tokens / (6 * 152);
-  if (a.kv.fp16) return a.in_fp32 ? launch_append_hd<__half, float>(a, st) : launch_append_hd<__half, __half>(a, st);
-  return a.in_fp32 ? launch_append_hd<__nv_bfloat16, float>(a, st)
-                   : launch_append_hd<__nv_bfloat16, __nv_bfloat16>(a, st);
+cudaError_t launch_paged_append(const AppendArgs& a, cudaStream_t st) {
+  return a.kv.fp16 ? launch_append_in<__half>(a, st) : launch_append_in<__nv_bfloat16>(a, st);
 }
 
 }  // namespace dex
@@ -196,7 +215,7 @@ extern "C" int dex_paged_append(const dex_paged_kv* kv, const dex_append_args* a
     if (!a->k || !a->v || !a->seq || !a->pos || !aligned16(a->k) || !aligned16(a->v) || a->k_stride % vec ||
         a->v_stride % vec || (a->q == nullptr) != (a->q_out == nullptr))
       return DEX_EINVAL;
-    if (a->q && (a->n_heads < 1 || a->n_heads > 131072 || !aligned16(a->q) || !aligned16(a->q_out) || a->q_stride % vec ||
+    if (a->q && (a->n_heads < 1 || a->n_heads > 131072 - 2 * kv->n_kv_heads || !aligned16(a->q) || !aligned16(a->q_out) || a->q_stride % vec ||
                  a->q_out_stride % 8 ||
                  (a->n_tokens > 1 && a->q_out_stride < static_cast<int64_t>(a->n_heads) * kv->head_dim)))
       return DEX_EINVAL;

@@ -19,7 +19,7 @@
 // lengths give the same bits).
 //
 // Two kernels compute segments:
-//  * rows_kernel (at most 64 rows: single tokens, lattice nodes): the keys are the work, so it is a
+//  * rows_kernel (at most 32 rows: single tokens, a few lattice nodes): the keys are the work, so it is a
 //    stream of K and V through a TMA ring into m16n8k16 MMAs on register fragments;
 //  * tile_kernel (up to 256 rows): 5th-generation tensor cores, two 128-row tiles per CTA that
 //    share every K and V tile.
@@ -39,18 +39,36 @@ namespace {
 
 constexpr int kRowsTile = 64;     // keys of a tile of rows_kernel
 constexpr int kRowsUnit = 16;     // its query rows come in m16 tiles
-constexpr int kRowsMax = 64;      // and at most this many
+constexpr int kRowsMax = 32;      // and at most this many
 constexpr int kRowsWarps = 4;     // compute warps
 constexpr int kRowsThreads = 32 * (kRowsWarps + 1);
+constexpr int kRowsSlotRows = 64; // rows of the segments posted ahead
 constexpr int kRowsPerSm = 2;     // resident CTAs
 constexpr int kSms = 152;         // of the sm_103 part: workspace sizes and grids, whatever device is current
 constexpr int kTileKeys = 128;    // keys of a tile of tile_kernel
 constexpr int kTileRows = 256;    // its query rows (two tiles of 128)
+constexpr int kRowsMinTiles = 2, kTileMinTiles = 2;   // key tiles of a CTA, at least
 constexpr int kMaxBatch = 1024;
+
+// Division by a number fixed for the call: n / d for 0 <= n < 2^31 (multiply, add, shift).
+struct FastDiv {
+  uint32_t d, mul, shift;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t div) : d(div), shift(0) {
+    while ((uint64_t(1) << shift) < d) ++shift;
+    mul = static_cast<uint32_t>(((uint64_t(1) << 32) * ((uint64_t(1) << shift) - d)) / d + 1);
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >> shift);
+  }
+};
 
 // What one of the two kernels has to do in a call.
 struct SegWork {
   PrefixAttnArgs a;
+  FastDiv by_g, by_kvh; // query heads per K/V head, K/V heads
+  int32_t first;        // 1: the call's first kernel (it waits for what precedes the call)
+  int32_t min_tiles;    // key tiles of a CTA, at least
   int32_t share;        // 1: positions below prefix_len belong to prefix segments
   int32_t do_prefix;    // this kernel computes the prefix segments
   int32_t do_own;       // this kernel computes the own segments
@@ -129,7 +147,7 @@ template <int TILE>
 __device__ __forceinline__ KeyRange own_range(const SegWork& w, const SeqRef& s, int r1) {
   KeyRange k;
   k.lo = w.share ? w.a.prefix_len : 0;
-  const int last = s.len - s.n + (r1 - 1) / w.a.G;   // position of the last query
+  const int last = s.len - s.n + w.by_g.div(r1 - 1);   // position of the last query
   k.hi = s.bad ? 0 : w.a.tree ? s.len : max(0, last + 1);
   k.t0 = k.lo / TILE;
   k.nt = k.hi > k.lo ? (k.hi + TILE - 1) / TILE - k.t0 : 0;
@@ -143,7 +161,7 @@ __device__ __forceinline__ KeyRange own_range(const SegWork& w, const SeqRef& s,
 
 // Index of an own segment's entry in own_info: distinct for the row tiles of sequences in order.
 __device__ __forceinline__ int own_info_of(const PrefixAttnArgs& a, int RT, int q0, int b, int rt, int kvh) {
-  return (static_cast<int>(static_cast<int64_t>(q0) * a.G / RT) + b + rt) * a.kv.KVH + kvh;
+  return (static_cast<int>(static_cast<uint32_t>(q0 * a.G) / static_cast<uint32_t>(RT)) + b + rt) * a.kv.KVH + kvh;
 }
 
 // The segment that holds a key tile, and the walk to the next one.
@@ -175,8 +193,8 @@ struct Walker {
   __device__ __forceinline__ void set_prefix(int index) {
     prefix = true;
     seg = index;
-    kvh = index % w.a.kv.KVH;
-    rt = index / w.a.kv.KVH;
+    rt = w.by_kvh.div(index);
+    kvh = index - rt * w.a.kv.KVH;
     r0 = rt * RT;
     rows = min(RT, w.a.n_tokens * w.a.G - r0);
     k = KeyRange{0, w.a.prefix_len, 0, pre_nt};
@@ -239,9 +257,12 @@ struct Walker {
       }
     }
   }
-  // Token, query head and position of row r of the segment.
-  __device__ __forceinline__ int token(int r) const { return (prefix ? 0 : s.q0) + (r0 + r) / w.a.G; }
-  __device__ __forceinline__ int head(int r) const { return kvh * w.a.G + (r0 + r) % w.a.G; }
+  // Token and query head of row r of the segment.
+  __device__ __forceinline__ void row_of(int r, int& t, int& h) const {
+    const int i = w.by_g.div(r0 + r);
+    t = (prefix ? 0 : s.q0) + i;
+    h = kvh * w.a.G + r0 + r - i * w.a.G;
+  }
   __device__ __forceinline__ int own_info_index() const { return own_info_of(w.a, RT, s.q0, b, rt, kvh); }
 };
 
@@ -316,16 +337,19 @@ __device__ __forceinline__ uint32_t count_tiles(const Walker<RT, TILE>& wk, uint
   return wk.pre_tiles() + base;
 }
 
-// This CTA's share [g0, g1) of `total` tiles over at most `ctas` CTAs (none is left without a tile
-// between two that have one), and the CTA that holds tile g.
+// Shares of `total` tiles over at most `ctas` CTAs: contiguous, equal within one, none below `least`
+// (but for the last few tiles of a small call); CTA c takes [begin(c), begin(c + 1)).
 struct Share {
-  uint32_t total, ctas;
-  __device__ __forceinline__ Share(uint32_t n, uint32_t c) : total(n), ctas(min(n, c)) {}
-  __device__ __forceinline__ uint32_t begin(uint32_t c) const {
-    return static_cast<uint32_t>(static_cast<uint64_t>(c) * total / ctas);
+  uint32_t ctas, each, more;   // the first `more` CTAs take each + 1 tiles
+  __device__ __forceinline__ Share(uint32_t total, uint32_t grid, uint32_t least) {
+    ctas = min(grid, total > least ? total / least : min(total, 1u));
+    each = ctas ? total / ctas : 0;
+    more = total - each * ctas;
   }
-  __device__ __forceinline__ int owner(uint32_t g) const {
-    return static_cast<int>((static_cast<uint64_t>(g + 1) * ctas - 1) / total);
+  __device__ __forceinline__ uint32_t begin(uint32_t c) const { return c * each + min(c, more); }
+  __device__ __forceinline__ int owner(uint32_t g) const {   // the CTA that holds tile g
+    const uint32_t head = more * (each + 1);
+    return static_cast<int>(g < head ? g / (each + 1) : more + (g - head) / each);
   }
 };
 
@@ -377,13 +401,15 @@ template <int HD, int TILE>
 struct PageLoader {
   const CUtensorMap* map;
   const PagedKv* kv;
-  const int32_t* tab;
+  const int32_t* tab = nullptr;
   int id0, ids, lane;
-  int id_end;   // entries below this one are in use
+  int id_end = 0;   // entries below this one are in use
   __device__ __forceinline__ void start(const int32_t* table, int key_end) {
+    const int end = (key_end + (1 << kv->page_shift) - 1) >> kv->page_shift;
+    if (table == tab && end <= id_end) return;   // the entries at hand are good for this segment too
     tab = table;
     id0 = -(1 << 30);
-    id_end = (key_end + (1 << kv->page_shift) - 1) >> kv->page_shift;
+    id_end = end;
   }
   __device__ __forceinline__ int boxes(int key0, int lo, int hi, int& first) const {   // pages of the tile in use
     const int a = max(key0, lo), b = min(key0 + TILE, hi);
@@ -439,7 +465,7 @@ struct SegDesc {
 };
 constexpr int kSegPrefix = 1, kSegStarts = 2, kSegEnds = 4, kSegBad = 8;
 struct RowDesc {
-  int32_t last, first, token, pad;
+  int32_t last, first, token, head;
   uint64_t word;
 };
 
@@ -450,7 +476,7 @@ struct RowsSmem {
   static constexpr int kSlots = 4;                               // segments posted ahead, at most
   static constexpr uint32_t kBuf = kRowsTile * HD * 2;
   static constexpr uint32_t kQRow = HD * 2 + 16;                 // padded: ldmatrix without bank conflicts
-  static constexpr int kQRows = 64;                              // rows of all slots together
+  static constexpr int kQRows = kRowsSlotRows;                   // rows of all slots together
   static constexpr uint32_t oP = kStages * kBuf;                 // [MT][16][64] probabilities, swizzled
   static constexpr uint32_t oQ = oP + kRows * kRowsTile * 2;
   static constexpr uint32_t oRow = oQ + kQRows * kQRow;          // RowDesc [64]
@@ -495,13 +521,13 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
   }
   if (tid < 64) token_seq[tid] = -1;
   __syncthreads();
+  if (w.first) griddep_wait();
   Walker<SM::kRows, kRowsTile> wk(w);
   const uint32_t total = count_tiles<SM::kRows, kRowsTile, kRowsThreads>(wk, cum, scratch, w.do_prefix ? token_seq : nullptr);
-  const Share sh(total, gridDim.x);
+  const Share sh(total, gridDim.x, w.min_tiles);
   const bool work = blockIdx.x < sh.ctas;
   const uint32_t g0 = work ? sh.begin(blockIdx.x) : 0, g1 = work ? sh.begin(blockIdx.x + 1) : 0;
-  const int tile0 = work ? wk.find(g0, cum) : 0;
-  fence_proxy_async_smem();   // the counts in the ring are read before its first copy
+  fence_proxy_async_smem();   // the counts in the ring are written before its first copy
   __syncthreads();
   griddep_launch_dependents();
   const int n_slots = w.slots;   // 64 / (rows of the call's largest segment), at most kSlots
@@ -512,9 +538,10 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
     ld.map = &tm;
     ld.kv = &a.kv;
     ld.lane = lane;
-    uint32_t n_ld = 0, n_seg = 0;
-    int tile = tile0;
+    uint32_t n_ld = 0, n_seg = 0, phase = 0;
+    int st = 0, tile = work ? wk.find(g0, cum) : 0;
     bool ok = true;
+    fence_proxy_async_smem();   // the counts in the ring are read before its first copy
     for (uint32_t g = g0; g < g1 && ok; ++n_seg) {
       const int cnt = min(wk.k.nt - tile, static_cast<int>(g1 - g));
       // the segment's description, row table and query rows
@@ -525,7 +552,8 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
         for (int r = lane; r < wk.rows; r += 32) {
-          const int t = wk.token(r);
+          int t, h;
+          wk.row_of(r, t, h);
           SeqRef s = wk.s;
           if (wk.prefix) {
             const int b = token_seq[t];
@@ -537,6 +565,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
           d->last = v.last;
           d->first = v.first;
           d->token = t;
+          d->head = h;
           d->word = v.word;
         }
         __syncwarp();
@@ -557,10 +586,12 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
           mbar_arrive_expect_tx(&seg_full[slot], static_cast<uint32_t>(wk.rows * HD * 2));
         }
         __syncwarp();
-        for (int r = lane; r < wk.rows; r += 32)
-          bulk_load_1d(smem + SM::oQ + (row0 + r) * SM::kQRow,
-                       static_cast<const T*>(a.q) + wk.token(r) * a.q_stride + static_cast<int64_t>(wk.head(r)) * HD, HD * 2,
+        for (int r = lane; r < wk.rows; r += 32) {
+          int t, h;
+          wk.row_of(r, t, h);
+          bulk_load_1d(smem + SM::oQ + (row0 + r) * SM::kQRow, static_cast<const T*>(a.q) + t * a.q_stride + h * HD, HD * 2,
                        &seg_full[slot]);
+        }
         ld.start(wk.prefix ? a.prefix_table : a.kv.table + static_cast<int64_t>(wk.b) * a.kv.table_stride, wk.k.hi);
       }
       for (int i = 0; i < cnt && ok; ++i) {
@@ -569,20 +600,22 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
         const int n = ld.boxes(key0, wk.k.lo, wk.k.hi, first);
         ld.prefetch(first, n);
         const bool bad = ld.page_of_lane(first, n, page);
-        for (int which = 0; which < 2 && ok; ++which) {
-          const int st = static_cast<int>(n_ld % SM::kStages);
-          if (n_ld >= SM::kStages && !mbar_wait(&empty[st], (n_ld / SM::kStages - 1) & 1u, nullptr, 0)) ok = false;
+        if (bad && lane == 0 && a.status) atomicOr(a.status, DEX_ATTN_BAD_PAGE);
+        const uint32_t tx = static_cast<uint32_t>(n * ld.box_rows() * HD * 2);
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+          if (n_ld >= SM::kStages) ok = ok && mbar_wait(&empty[st], phase ^ 1u, nullptr, 0);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (lane == 0) {
             bad_stage[st] = bad;
-            if (bad && a.status) atomicOr(a.status, DEX_ATTN_BAD_PAGE);
-            if (n > 0) mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(n * ld.box_rows() * HD * 2));
+            if (n > 0) mbar_arrive_expect_tx(&full[st], tx);
             else mbar_arrive(&full[st]);
           }
           __syncwarp();
           ld.load(smem + st * SM::kBuf, &full[st], which, wk.kvh, key0, first, n, page);
           ++n_ld;
+          if (++st == SM::kStages) st = 0, phase ^= 1u;
         }
       }
       g += static_cast<uint32_t>(cnt);
@@ -604,7 +637,8 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
     float* ssum = reinterpret_cast<float*>(smem + SM::oSum);
     const uint32_t sp = smem_u32(smem + SM::oP);
     const float c = a.scale_log2;
-    uint32_t n_ld = 0, n_seg = 0;
+    uint32_t phase = 0, n_seg = 0;
+    int st = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t n) {
       if (ok && !mbar_wait(bar, n & 1u, nullptr, 0)) {
@@ -619,6 +653,11 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
       const SegDesc d = reinterpret_cast<const SegDesc*>(smem + SM::oSeg)[slot];
       const RowDesc* rd = reinterpret_cast<const RowDesc*>(smem + SM::oRow) + row0;
       const uint32_t sq = smem_u32(smem + SM::oQ) + row0 * SM::kQRow;
+      uint32_t qf[MT == 1 ? HD / 16 : 1][4];   // one row tile's queries stay in registers
+      if constexpr (MT == 1) {
+#pragma unroll
+        for (int ks = 0; ks < HD / 16; ++ks) ldmatrix_x4(sq + (lane & 15) * SM::kQRow + ks * 32 + (lane >> 4) * 16, qf[ks]);
+      }
       float o[MT][NV][4];
       float m[MT][2], l[MT][2];
       int seen_by_all = 0x7fffffff;   // keys up to this one are seen by every row of this thread
@@ -637,10 +676,10 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
       bool bad = d.flags & kSegBad;
       for (int i = 0; i < d.cnt; ++i) {
         // ---- scores of this warp's 16 keys ----
-        const int kst = static_cast<int>(n_ld % SM::kStages);
-        wait(&full[kst], n_ld / SM::kStages);
-        ++n_ld;
-        const int vst = static_cast<int>(n_ld % SM::kStages);
+        const int kst = st;
+        wait(&full[kst], phase);
+        if (++st == SM::kStages) st = 0, phase ^= 1u;
+        const int vst = st;
         bad |= bad_stage[kst] != 0;
         const int key0 = d.key0 + i * kRowsTile + warp * 16;
         const int in0 = max(d.lo - key0, 0), in1 = min(d.hi - key0, 16);   // keys of the segment among them
@@ -662,10 +701,10 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
             float s[2][2][4] = {};   // two chains: even and odd k steps
 #pragma unroll
             for (int ks = 0; ks < HD / 16; ++ks) {
-              uint32_t qf[4];
-              ldmatrix_x4(sq + (u * 16 + (lane & 15)) * SM::kQRow + ks * 32 + (lane >> 4) * 16, qf);
-              mma_16816<T>(s[ks & 1][0], qf, kf[ks][0], kf[ks][1]);
-              mma_16816<T>(s[ks & 1][1], qf, kf[ks][2], kf[ks][3]);
+              const int qi = MT == 1 ? ks : 0;
+              if constexpr (MT > 1) ldmatrix_x4(sq + (u * 16 + (lane & 15)) * SM::kQRow + ks * 32 + (lane >> 4) * 16, qf[qi]);
+              mma_16816<T>(s[ks & 1][0], qf[qi], kf[ks][0], kf[ks][1]);
+              mma_16816<T>(s[ks & 1][1], qf[qi], kf[ks][2], kf[ks][3]);
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -689,8 +728,8 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
             }
           }
         }
-        wait(&full[vst], n_ld / SM::kStages);
-        ++n_ld;
+        wait(&full[vst], phase);
+        if (++st == SM::kStages) st = 0, phase ^= 1u;
         if (edge && ok) {   // rows outside the segment hold anything: p = 0 must meet a finite v
           uint8_t* vt = smem + vst * SM::kBuf;
           for (int z = lane; z < 16 * HD / 8; z += 32) {
@@ -782,7 +821,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
 #pragma unroll
           for (int k = 0; k < kRowsWarps; ++k) L += ssum[k * SM::kRows + r];
           const int t = rd[r].token;
-          const int hg = r % a.G, head = d.kvh * a.G + hg;   // a segment of this kernel starts at a token's first head
+          const int head = rd[r].head, hg = head - d.kvh * a.G;
           const int dim = warp * (HD / 4) + 2 * tq;
           if (whole && !w.joined) {
             const float inv = isnan(L) ? L : L > 0.0f ? 1.0f / L : 0.0f;
@@ -883,6 +922,35 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// Pairs of fp32 in one 64-bit register, two operations per instruction.
+__device__ __forceinline__ uint64_t u32x2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) { return u32x2(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Bits i of columns [32 c, 32 c + 32) of a key tile at key0 that the row sees, within [lo, hi).
@@ -950,9 +1018,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tmem_alloc(tmem_slot, 512);   // S / P of the teams: 128 columns each, then their O
     tmem_relinquish();
   }
+  if (w.first) griddep_wait();
   Walker<kTileRows, kTileKeys> wk(w);
   const uint32_t total = count_tiles<kTileRows, kTileKeys, kTileThreads>(wk, cum, scratch);
-  const Share sh(total, gridDim.x);
+  const Share sh(total, gridDim.x, w.min_tiles);
   const bool work = blockIdx.x < sh.ctas;
   const uint32_t g0 = work ? sh.begin(blockIdx.x) : 0, g1 = work ? sh.begin(blockIdx.x + 1) : 0;
   int tile = work ? wk.find(g0, cum) : 0;
@@ -967,7 +1036,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   };
 
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---------------- softmax teams: one row per thread ----------------
     const int team = warp >> 2, r128 = tid & 127;
     const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -985,32 +1053,36 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int r = alt ? r128 : team * 128 + r128;
       const bool on = r < wk.rows;
       if (!alt || team == 0) {
-        // the row's query, signed as the scale (zero for a zero scale and beyond the segment)
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const T*>(a.q) + (on ? wk.token(r) * a.q_stride + static_cast<int64_t>(wk.head(r)) * HD : 0));
-        const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
-        const bool nz = on && a.scale_log2 != 0.0f;
+        // the team's query rows, HD / 8 threads per row; zero beyond the segment
         uint8_t* dst = smem + SM::oQ + (alt ? 0 : team) * SM::kBuf;
-#pragma unroll
-        for (int e = 0; e < HD / 8; ++e) {
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (nz) {
-            v = __ldg(src + e);
-            v.x ^= flip;
-            v.y ^= flip;
-            v.z ^= flip;
-            v.w ^= flip;
+        const int row0 = alt ? 0 : team * 128;
+#pragma unroll 4
+        for (int i = 0; i < HD / 8; ++i) {
+          const int rr = i * (1024 / HD) + r128 / (HD / 8), e = (r128 % (HD / 8)) * 8;
+          if (row0 + rr < wk.rows) {
+            int t, h;
+            wk.row_of(row0 + rr, t, h);
+            cp_async_16(smem_u32(dst + sw_off(rr, e)), static_cast<const T*>(a.q) + t * a.q_stride + h * HD + e);
+          } else {
+            *reinterpret_cast<uint4*>(dst + sw_off(rr, e)) = make_uint4(0u, 0u, 0u, 0u);
           }
-          *reinterpret_cast<uint4*>(dst + sw_off(r128, e * 8)) = v;
+        }
+        cp_async_commit();
+        cp_async_wait_all();
+        if (a.scale_log2 <= 0.0f) {   // c is positive: the queries take the sign (zero for a zero scale)
+          for (int i = 0; i < HD / 8; ++i) {
+            uint4* v = reinterpret_cast<uint4*>(dst + sw_off(i * (1024 / HD) + r128 / (HD / 8), (r128 % (HD / 8)) * 8));
+            const uint32_t keep = a.scale_log2 < 0.0f ? 0xffffffffu : 0u, flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+            *v = make_uint4((v->x & keep) ^ flip, (v->y & keep) ^ flip, (v->z & keep) ^ flip, (v->w & keep) ^ flip);
+          }
         }
         fence_proxy_async_smem();
         mbar_arrive(&q_full[team]);
       }
+      int t_row = 0, h_row = 0;   // the thread's row
+      if (on) wk.row_of(r, t_row, h_row);
       RowView rv{0x7fffffff, 0, 0, false};
-      if (on) {
-        const int t = wk.token(r);
-        rv = wk.prefix ? row_view(a, seq_ref(a, seq_of_token(a, t)), t) : row_view(a, wk.s, t);
-      }
+      if (on) rv = wk.prefix ? row_view(a, seq_ref(a, seq_of_token(a, t_row)), t_row) : row_view(a, wk.s, t_row);
       float m = -INFINITY, l = 0.0f;
       bool bad = !wk.prefix && wk.s.bad, any = false;   // any: this team had a tile
       for (int j = alt ? team : 0; j < cnt; j += ahead == 2 ? 2 : 1) {
@@ -1021,28 +1093,37 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32_nowait(t_s + q * 32, s[q]);
-        tmem_wait_ld();
         const int key0 = (wk.k.t0 + tile + j) * kTileKeys;
         const bool whole = wk.k.lo <= key0 && wk.k.hi >= key0 + kTileKeys;
-        if (!__all_sync(0xffffffffu, whole && rv.last >= key0 + kTileKeys - 1)) {
+        // the row's maximum, 32 columns at a time; masked scores go back to TMEM as -inf
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        uint32_t s[2][32];
+        tmem_ld32_nowait(t_s, s[0]);
+        if (__all_sync(0xffffffffu, whole && rv.last >= key0 + kTileKeys - 1)) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
+            tmem_wait_ld();
+            if (q < 3) tmem_ld32_nowait(t_s + (q + 1) * 32, s[(q + 1) & 1]);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              mx4[(i >> 1) & 3] = max3(mx4[(i >> 1) & 3], __uint_as_float(s[q & 1][i]), __uint_as_float(s[q & 1][i + 1]));
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            tmem_wait_ld();
             const uint32_t bits = seen_bits(rv, wk.k.lo, wk.k.hi, key0 + q * 32);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!(bits >> i & 1u)) s[q][i] = 0xff800000u;   // -inf
+            for (int i = 0; i < 32; ++i) {
+              if (!(bits >> i & 1u)) s[0][i] = 0xff800000u;   // -inf
+              mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(s[0][i]));
+            }
+            tmem_st32(t_s + q * 32, s[0]);
+            if (q < 3) tmem_ld32_nowait(t_s + (q + 1) * 32, s[0]);
           }
+          tmem_wait_st();
         }
-        float mx4[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          mx4[q] = __uint_as_float(s[q][0]);
-#pragma unroll
-          for (int i = 1; i < 32; ++i) mx4[q] = fmaxf(mx4[q], __uint_as_float(s[q][i]));
-        }
+        tmem_ld32_nowait(t_s, s[0]);   // again, for P (in flight under what follows)
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
         const bool move = mx > m + kRescale || (m == -INFINITY && mx > -INFINITY);
         if (__any_sync(0xffffffffu, move)) {
@@ -1055,7 +1136,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < HD / 32; ++q) {
               uint32_t o[32];
               tmem_ld32_nowait(t_o + q * 32, o);
@@ -1070,21 +1151,27 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         any = true;
         const float sub = m > -INFINITY ? m : 0.0f;
-        float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        uint64_t l2[2] = {0ull, 0ull};   // two fp32 sums each
+        const uint64_t c2 = f32x2(c, c), sub2 = f32x2(-sub, -sub);
 #pragma unroll
-        for (int q = 0; q < 4; q += 2) {
-          uint32_t p[32];
+        for (int q = 0; q < 4; ++q) {
+          tmem_wait_ld();
+          if (q < 3) tmem_ld32_nowait(t_s + (q + 1) * 32, s[(q + 1) & 1]);
+          uint32_t p[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int qq = q + (i >> 4), e = (2 * i) & 31;
-            const float p0 = ex2(fmaf(__uint_as_float(s[qq][e]), c, -sub));
-            const float p1 = ex2(fmaf(__uint_as_float(s[qq][e + 1]), c, -sub));
-            l4[i & 3] += p0 + p1;
+          for (int i = 0; i < 16; ++i) {
+            const uint64_t x = fma2(u32x2(s[q & 1][2 * i], s[q & 1][2 * i + 1]), c2, sub2);
+            const float p0 = ex2(__uint_as_float(static_cast<uint32_t>(x))), p1 = ex2(__uint_as_float(static_cast<uint32_t>(x >> 32)));
+            l2[i & 1] = add2(l2[i & 1], f32x2(p0, p1));
             p[i] = pack2<T>(p0, p1);
           }
-          tmem_st32(t_s + q * 16, p);
+          // P of columns 32 q .. takes the columns 16 q .., whose scores are in registers by now
+          tmem_st16(t_s + q * 16, p);
         }
-        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        {
+          const uint64_t t2 = add2(l2[0], l2[1]);
+          l += __uint_as_float(static_cast<uint32_t>(t2)) + __uint_as_float(static_cast<uint32_t>(t2 >> 32));
+        }
         tmem_wait_st();
         tc_fence_before();
         // V of this tile: rows outside the segment hold anything, and P = 0 must meet a finite v
@@ -1145,7 +1232,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         const bool starts = tile == 0, ends = tile + cnt == wk.k.nt;
         const bool direct = starts && ends && !w.joined;
-        const int t = on ? wk.token(r) : 0, h = on ? wk.head(r) : 0;
+        const int t = t_row, h = h_row;
         const int64_t row = static_cast<int64_t>(t) * a.H + h;
         const PartRef part = starts && ends ? joined_part<HD>(wk.prefix ? w.pre_o : w.own_o, wk.prefix ? w.pre_ml : w.own_ml,
                                                               wk.kvh, a.n_tokens * a.G, t * a.G + h - wk.kvh * a.G)
@@ -1200,7 +1287,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       tile = 0;
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
       // ---------------- producer ----------------
       PageLoader<HD, kTileKeys> lk, lv;
@@ -1351,9 +1437,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 }
 
 // ============================================================================================
-// Joins the parts of the rows that have several: a block takes eight rows of one K/V head, a warp finds
-// the parts and weights of each, then every thread sums one float4 of one row over the parts.  Parts lie
-// as [head_dim / 4][rows][4], so eight rows of a part are 128 contiguous bytes.
+// Joins the parts of the rows that have several.  A block takes 32 rows of one K/V head, a lane per row;
+// each of HD / 16 warps sums 16 head dims over the parts, with the running maximum of the softmax.  In a
+// call of few rows SPLIT such groups of warps take the parts in turn and join in shared memory: the sum
+// over 38 parts of one 128k-token sequence is a chain of loads otherwise (21 us alone, @@ with four).
+// Parts lie as [head_dim / 4][rows][4], so the 32 rows of four head dims are 512 contiguous bytes.
 // ============================================================================================
 struct CombineWork {
   SegWork own, pre;        // the kernels that computed own and prefix segments
@@ -1361,125 +1449,140 @@ struct CombineWork {
   int32_t own_tile;        // their keys per tile (own segments)
   int32_t share;
 };
-// Part k of a row: the prefix parts (first CTA parts.x, number parts.y), then the own parts (z, w).
-template <int HD>
-__device__ __forceinline__ PartRef part_of(const CombineWork& w, const int4& parts, int k, int kvh, int rows_all, int rg,
-                                           int own_row) {
-  const bool pre = k < parts.y;
-  const int c0 = pre ? parts.x : parts.z, n = pre ? parts.y : parts.w, i = pre ? k : k - parts.y;
-  const SegWork& s = pre ? w.pre : w.own;
-  if (n == 1) return joined_part<HD>(pre ? s.pre_o : s.own_o, pre ? s.pre_ml : s.own_ml, kvh, rows_all, rg);
-  const int rt = pre ? w.pre_rt : w.own_rt;
-  return slot_part<HD>(s.part_o, s.part_ml, 2 * (c0 + i) + (i == 0 ? 1 : 0), rt, pre ? rg % rt : own_row);
-}
-constexpr int kCombineRows = 8;
-constexpr int kMaxParts = 2 * kRowsPerSm * kSms + 2;   // a row's prefix and own parts
+constexpr int kCombineRows = 32;
 
-template <typename T, int HD>
-__global__ void __launch_bounds__(HD * 2) combine_kernel(const __grid_constant__ CombineWork w) {
-  constexpr int kThreads = HD * 2;   // eight rows x HD / 4 columns
+template <typename T, int HD, int SPLIT>
+__global__ void __launch_bounds__(HD * 2 * SPLIT) combine_kernel(const __grid_constant__ CombineWork w) {
+  constexpr int kThreads = HD * 2 * SPLIT;
   __shared__ int row_seq[kCombineRows];
-  __shared__ int4 row_part[kCombineRows];            // first CTA and number of prefix parts, of own parts
-  __shared__ int row_own[kCombineRows];              // row within its own segment
-  __shared__ float weight[kCombineRows][kMaxParts];
+  __shared__ float join[SPLIT > 1 ? SPLIT / 2 : 1][SPLIT > 1 ? 18 : 1][HD * 2];
   const PrefixAttnArgs& a = w.own.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, kvh = blockIdx.y;
-  const int rows_all = a.n_tokens * a.G, rg0 = blockIdx.x * kCombineRows;   // row: token * G + head within the K/V head
+  const int tid = threadIdx.x, group = tid / (HD * 2), warp = (tid >> 5) % (HD / 16), lane = tid & 31, kvh = blockIdx.y;
+  const int rows_all = a.n_tokens * a.G, rg = blockIdx.x * kCombineRows + lane;   // row: token * G + head within the K/V head
+  const int t = w.own.by_g.div(rg);
   if (tid < kCombineRows) row_seq[tid] = -1;
   __syncthreads();
   {
-    const int t0 = rg0 / a.G, t1 = min(rg0 + kCombineRows - 1, rows_all - 1) / a.G;
+    const int t0 = __shfl_sync(0xffffffffu, t, 0), t1 = __shfl_sync(0xffffffffu, t, 31);
     for (int b = tid; b < a.kv.batch; b += kThreads) {
       const SeqRef s = seq_ref(a, b);
-      if (!s.valid || s.q0 > t1 || s.q0 + s.n <= t0) continue;
-      for (int i = 0; i < kCombineRows; ++i) {
-        const int t = (rg0 + i) / a.G;
-        if (rg0 + i < rows_all && t >= s.q0 && t < s.q0 + s.n) row_seq[i] = b;
-      }
+      if (!s.valid) continue;
+      const int first = max(s.q0, t0), last = min(s.q0 + s.n - 1, t1);   // tokens of the block, then rows
+      for (int r = max(first * a.G, rg - lane); first <= last && r < min((last + 1) * a.G, rg - lane + kCombineRows); ++r)
+        row_seq[r - (rg - lane)] = b;
     }
   }
   __syncthreads();
+  const int b = row_seq[lane];
+  const SeqRef s = seq_ref(a, max(b, 0));
+  const int r = rg - s.q0 * a.G, rt = b >= 0 ? r / w.own_rt : 0, r1 = min((rt + 1) * w.own_rt, s.n * a.G);
   griddep_wait();
-  for (int i = warp; i < kCombineRows; i += kThreads / 32) {
-    const int b = row_seq[i], rg = rg0 + i;
-    int4 parts = make_int4(0, 0, 0, 0);
-    if (b >= 0) {
-      const SeqRef s = seq_ref(a, b);
-      if (w.share) {
-        const int2 info = w.pre.pre_info[rg / w.pre_rt * a.kv.KVH + kvh];
-        parts.x = info.x;
-        parts.y = info.y - info.x + 1;
+  // this row's parts: prefix parts of CTAs pre_c0 .., then own parts of CTAs own_c0 ..
+  int pre_c0 = 0, n_pre = 0, own_c0 = 0, n_own = 0;
+  if (b >= 0) {
+    if (w.share) {
+      const int2 info = w.pre.pre_info[rg / w.pre_rt * a.kv.KVH + kvh];
+      pre_c0 = info.x;
+      n_pre = info.y - info.x + 1;
+    }
+    const int nt = w.own_tile == kRowsTile ? own_range<kRowsTile>(w.own, s, r1).nt : own_range<kTileKeys>(w.own, s, r1).nt;
+    if (nt > 0) {
+      const int2 info = w.own.own_info[own_info_of(a, w.own_rt, s.q0, b, rt, kvh)];
+      own_c0 = info.x;
+      n_own = info.y - info.x + 1;
+      if (n_own == 1 && !w.share) n_own = 0;   // written where it was computed
+    }
+  }
+  const int n = n_pre + n_own;
+  if (__all_sync(0xffffffffu, n <= 0)) return;   // the same in all warps
+  float M = -INFINITY, L = 0.0f;
+  float4 o[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) o[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  constexpr int kUnroll = 2;
+  for (int k0 = group * kUnroll; k0 < n; k0 += kUnroll * SPLIT) {
+    float2 ml[kUnroll];
+    float4 x[kUnroll][4];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int k = k0 + u;
+      ml[u] = make_float2(-INFINITY, 0.0f);
+      if (k < n) {
+        const bool pre = k < n_pre;
+        const SegWork& sw = pre ? w.pre : w.own;
+        const int i = pre ? k : k - n_pre, rows = pre ? w.pre_rt : w.own_rt;
+        const PartRef p = (pre ? n_pre : n_own) == 1
+                              ? joined_part<HD>(pre ? sw.pre_o : sw.own_o, pre ? sw.pre_ml : sw.own_ml, kvh, rows_all, rg)
+                              : slot_part<HD>(sw.part_o, sw.part_ml, 2 * ((pre ? pre_c0 : own_c0) + i) + (i == 0 ? 1 : 0), rows,
+                                              pre ? rg % rows : r - rt * rows);
+        ml[u] = *p.ml;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[u][q] = *reinterpret_cast<const float4*>(p.o + (warp * 4 + q) * p.step);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[u][q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
-      const int r = rg - s.q0 * a.G, rt = r / w.own_rt, r1 = min((rt + 1) * w.own_rt, s.n * a.G);
-      const int nt = w.own_tile == kRowsTile ? own_range<kRowsTile>(w.own, s, r1).nt : own_range<kTileKeys>(w.own, s, r1).nt;
-      if (nt > 0) {
-        const int2 info = w.own.own_info[own_info_of(a, w.own_rt, s.q0, b, rt, kvh)];
-        parts.z = info.x;
-        parts.w = info.y - info.x + 1;
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const float M1 = fmaxf(M, ml[u].x), base = M1 > -INFINITY ? M1 : 0.0f;
+      const float f = ex2(M - base), g = ex2(ml[u].x - base);
+      M = M1;
+      L = L * f + ml[u].y * g;   // a poisoned part is NaN whatever its weight
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        o[q].x = o[q].x * f + x[u][q].x * g;
+        o[q].y = o[q].y * f + x[u][q].y * g;
+        o[q].z = o[q].z * f + x[u][q].z * g;
+        o[q].w = o[q].w * f + x[u][q].w * g;
       }
-      if (lane == 0) row_own[i] = r - rt * w.own_rt;
-      if (parts.w == 1 && !w.share) parts.w = 0;   // written where it was computed
-      const int n = min(parts.y + parts.w, kMaxParts);
-      float M = -INFINITY;
-      for (int k0 = 0; k0 < n; k0 += 32) {
-        const int k = k0 + lane;
-        float2 ml = make_float2(-INFINITY, 0.0f);
-        if (k < n) {
-          const PartRef p = part_of<HD>(w, parts, k, kvh, rows_all, rg, r - rt * w.own_rt);
-          ml = __ldcg(p.ml);
-          weight[i][k] = ml.x;
+    }
+  }
+  if constexpr (SPLIT > 1) {
+#pragma unroll
+    for (int half = SPLIT / 2; half > 0; half >>= 1) {   // groups half .. 2 half - 1 join groups 0 .. half - 1
+      const int x = tid % (HD * 2);
+      if (group >= half && group < 2 * half) {
+        float(*dst)[HD * 2] = join[group - half];
+        dst[0][x] = M;
+        dst[1][x] = L;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          dst[2 + 4 * q][x] = o[q].x;
+          dst[3 + 4 * q][x] = o[q].y;
+          dst[4 + 4 * q][x] = o[q].z;
+          dst[5 + 4 * q][x] = o[q].w;
         }
-        M = fmaxf(M, warp_max(ml.x));
       }
-      __syncwarp();
-      const float base = M > -INFINITY ? M : 0.0f;
-      float L = 0.0f;
-      for (int k = lane; k < n; k += 32) {
-        const PartRef p = part_of<HD>(w, parts, k, kvh, rows_all, rg, r - rt * w.own_rt);
-        const float wgt = ex2(weight[i][k] - base);
-        L += __ldcg(p.ml).y * wgt;   // a poisoned part is NaN whatever its weight
-        weight[i][k] = wgt;
+      __syncthreads();
+      if (group < half) {
+        const float(*src)[HD * 2] = join[group];
+        const float M1 = fmaxf(M, src[0][x]), base = M1 > -INFINITY ? M1 : 0.0f;
+        const float f = ex2(M - base), g = ex2(src[0][x] - base);
+        M = M1;
+        L = L * f + src[1][x] * g;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          o[q].x = o[q].x * f + src[2 + 4 * q][x] * g;
+          o[q].y = o[q].y * f + src[3 + 4 * q][x] * g;
+          o[q].z = o[q].z * f + src[4 + 4 * q][x] * g;
+          o[q].w = o[q].w * f + src[5 + 4 * q][x] * g;
+        }
       }
-      L = warp_sum(L);
-      __syncwarp();
-      const float inv = isnan(L) ? L : L > 0.0f ? 1.0f / L : 0.0f;
-      for (int k = lane; k < n; k += 32) weight[i][k] *= inv;
-      if (a.lse && lane == 0 && n > 0)
-        a.lse[static_cast<int64_t>(rg / a.G) * a.H + kvh * a.G + rg % a.G] =
-            isnan(L) ? L : L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
-      parts.w = n - parts.y;
+      __syncthreads();
     }
-    if (lane == 0) row_part[i] = parts;
+    if (group > 0) return;
   }
-  __syncthreads();
-  const int i = tid & (kCombineRows - 1), c4 = tid / kCombineRows, rg = rg0 + i;
-  const int4 parts = row_part[i];
-  const int n = parts.y + parts.w;
   if (n <= 0) return;
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  const int ro = row_own[i];
-  constexpr int kUnroll = 8;
-  for (int k0 = 0; k0 < n; k0 += kUnroll) {
-    float4 x[kUnroll];
+  const float inv = isnan(L) ? L : L > 0.0f ? 1.0f / L : 0.0f;
+  const int h = kvh * a.G + rg - t * a.G;
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + t * a.out_stride + h * HD + warp * 16);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      x[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (k0 + u < n) {
-        const PartRef p = part_of<HD>(w, parts, k0 + u, kvh, rows_all, rg, ro);
-        x[u] = __ldcg(reinterpret_cast<const float4*>(p.o + static_cast<int64_t>(c4) * p.step));
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const float wgt = k0 + u < n ? weight[i][k0 + u] : 0.0f;
-      o.x = fmaf(x[u].x, wgt, o.x);
-      o.y = fmaf(x[u].y, wgt, o.y);
-      o.z = fmaf(x[u].z, wgt, o.z);
-      o.w = fmaf(x[u].w, wgt, o.w);
-    }
-  }
-  T* dst = static_cast<T*>(a.out) + rg / a.G * a.out_stride + static_cast<int64_t>(kvh * a.G + rg % a.G) * HD + c4 * 4;
-  *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(o.x, o.y), pack2<T>(o.z, o.w));
+  for (int q = 0; q < 4; q += 2)
+    dst[q / 2] = make_uint4(pack2<T>(o[q].x * inv, o[q].y * inv), pack2<T>(o[q].z * inv, o[q].w * inv),
+                            pack2<T>(o[q + 1].x * inv, o[q + 1].y * inv), pack2<T>(o[q + 1].z * inv, o[q + 1].w * inv));
+  if (a.lse && warp == 0)
+    a.lse[static_cast<int64_t>(t) * a.H + h] = isnan(L) ? L : L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
 }
 
 // ---- host ------------------------------------------------------------------------------------
@@ -1487,14 +1590,14 @@ namespace {
 
 struct Plan {
   bool share, prefix_tile, own_tile;   // prefix / own segments on tile_kernel
-  int rows_mt;                         // row tiles of rows_kernel: 1 or 4 (0: it has nothing to do)
+  int rows_mt;                         // row tiles of rows_kernel: 1 or 2 (0: it has nothing to do)
   int slots;
   size_t o_rows_part, o_rows_ml, o_tile_part, o_tile_ml, o_pre, o_pre_ml, o_own, o_own_ml, o_pre_info, o_own_info, total;
   int own_rt() const { return own_tile ? kTileRows : rows_mt * kRowsUnit; }
   int pre_rt() const { return prefix_tile ? kTileRows : rows_mt * kRowsUnit; }
 };
 
-// Which kernel computes what.  Segments of at most 64 rows go to rows_kernel.  The prefix is
+// Which kernel computes what.  Segments of at most 32 rows go to rows_kernel.  The prefix is
 // shared when more than one sequence can have queries (n_tokens > max_q) and it fills a key tile; a
 // sequence whose own rows fill a 128-row tile gains nothing from sharing.
 Plan make_plan(const PrefixAttnArgs& a) {
@@ -1505,7 +1608,7 @@ Plan make_plan(const PrefixAttnArgs& a) {
   p.prefix_tile = p.share && all_rows > kRowsMax;
   const int64_t most = p.share && !p.prefix_tile ? all_rows : p.own_tile ? 0 : own_rows;   // rows of a rows_kernel segment
   p.rows_mt = most == 0 ? 0 : most <= kRowsUnit ? 1 : kRowsMax / kRowsUnit;
-  p.slots = most == 0 ? 1 : static_cast<int>(kRowsMax / ((most + kRowsUnit - 1) / kRowsUnit * kRowsUnit));
+  p.slots = most == 0 ? 1 : static_cast<int>(kRowsSlotRows / ((most + kRowsUnit - 1) / kRowsUnit * kRowsUnit));
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -1575,9 +1678,11 @@ cudaError_t launch(K* kernel, dim3 grid, int threads, uint32_t smem, cudaStream_
 
 template <typename T, int HD>
 cudaError_t launch_hd(const PrefixAttnArgs& a, const Plan& p, uint8_t* ws, cudaStream_t st, int dev, int n_sm) {
-  static std::atomic<uint64_t> rows1_set{0}, rows4_set{0}, tile_set{0};
+  static std::atomic<uint64_t> rows1_set{0}, rows2_set{0}, tile_set{0};
   SegWork base = {};
   base.a = a;
+  base.by_g = FastDiv(static_cast<uint32_t>(a.G));
+  base.by_kvh = FastDiv(static_cast<uint32_t>(a.kv.KVH));
   base.share = p.share;
   base.joined = p.share;
   base.pre_o = reinterpret_cast<float*>(ws + p.o_pre);
@@ -1596,17 +1701,19 @@ cudaError_t launch_hd(const PrefixAttnArgs& a, const Plan& p, uint8_t* ws, cudaS
   tile.part_ml = reinterpret_cast<float2*>(ws + p.o_tile_ml);
   tile.do_own = p.own_tile;
   tile.do_prefix = p.prefix_tile;
+  tile.first = 1;
+  rows.first = !(tile.do_own || tile.do_prefix);
+  rows.min_tiles = kRowsMinTiles;
+  tile.min_tiles = kTileMinTiles;
   const int page = 1 << a.kv.page_shift;
   const int sms = n_sm < kSms ? n_sm : kSms;
-  bool pdl = false;
   cudaError_t e = cudaSuccess;
   if (tile.do_own || tile.do_prefix) {
     CUtensorMap tm;
     if (!page_map(&tm, a.kv, page < kTileKeys ? page : kTileKeys)) return cudaErrorInvalidValue;
     e = set_smem(tile_kernel<T, HD>, TileSmem<HD>::kTotal, tile_set, dev);
     if (e == cudaSuccess)
-      e = launch(tile_kernel<T, HD>, dim3(static_cast<unsigned>(sms)), kTileThreads, TileSmem<HD>::kTotal, st, pdl, tm, tile);
-    pdl = true;
+      e = launch(tile_kernel<T, HD>, dim3(static_cast<unsigned>(sms)), kTileThreads, TileSmem<HD>::kTotal, st, true, tm, tile);
   }
   if (e == cudaSuccess && (rows.do_own || rows.do_prefix)) {
     CUtensorMap tm;
@@ -1614,12 +1721,11 @@ cudaError_t launch_hd(const PrefixAttnArgs& a, const Plan& p, uint8_t* ws, cudaS
     const dim3 grid(static_cast<unsigned>(kRowsPerSm * sms));
     if (p.rows_mt == 1) {
       e = set_smem(rows_kernel<T, HD, 1>, RowsSmem<HD, 1>::kTotal, rows1_set, dev);
-      if (e == cudaSuccess) e = launch(rows_kernel<T, HD, 1>, grid, kRowsThreads, RowsSmem<HD, 1>::kTotal, st, pdl, tm, rows);
+      if (e == cudaSuccess) e = launch(rows_kernel<T, HD, 1>, grid, kRowsThreads, RowsSmem<HD, 1>::kTotal, st, true, tm, rows);
     } else {
-      e = set_smem(rows_kernel<T, HD, 4>, RowsSmem<HD, 4>::kTotal, rows4_set, dev);
-      if (e == cudaSuccess) e = launch(rows_kernel<T, HD, 4>, grid, kRowsThreads, RowsSmem<HD, 4>::kTotal, st, pdl, tm, rows);
+      e = set_smem(rows_kernel<T, HD, 2>, RowsSmem<HD, 2>::kTotal, rows2_set, dev);
+      if (e == cudaSuccess) e = launch(rows_kernel<T, HD, 2>, grid, kRowsThreads, RowsSmem<HD, 2>::kTotal, st, true, tm, rows);
     }
-    pdl = true;
   }
   if (e == cudaSuccess) {
     CombineWork c = {};
@@ -1629,8 +1735,11 @@ cudaError_t launch_hd(const PrefixAttnArgs& a, const Plan& p, uint8_t* ws, cudaS
     c.pre_rt = p.pre_rt();
     c.own_tile = p.own_tile ? kTileKeys : kRowsTile;
     c.share = p.share;
-    const unsigned groups = static_cast<unsigned>((static_cast<int64_t>(a.n_tokens) * a.G + kCombineRows - 1) / kCombineRows);
-    e = launch(combine_kernel<T, HD>, dim3(groups, static_cast<unsigned>(a.kv.KVH)), HD * 2, 0, st, pdl, c);
+    const unsigned groups = static_cast<unsigned>((a.n_tokens * a.G + kCombineRows - 1) / kCombineRows);
+    const dim3 grid(groups, static_cast<unsigned>(a.kv.KVH));
+    // four groups of warps per row while the blocks leave SMs idle
+    e = groups * a.kv.KVH < static_cast<unsigned>(sms) ? launch(combine_kernel<T, HD, 4>, grid, HD * 8, 0, st, true, c)
+                                                       : launch(combine_kernel<T, HD, 1>, grid, HD * 2, 0, st, true, c);
   }
   return e;
 }
