@@ -269,6 +269,8 @@ struct Walker {
 // The sequence whose queries can hold token t: the last b with q_start[b] <= t.
 __device__ __forceinline__ int seq_of_token(const PrefixAttnArgs& a, int t) {
   int lo = 0, hi = a.kv.batch - 1;
+  // with one query per sequence it is t itself: two loads instead of a chain of them
+  if (t <= hi && __ldg(a.q_start + t) <= t && (t == hi || __ldg(a.q_start + t + 1) > t)) return t;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (__ldg(a.q_start + mid) <= t) lo = mid;
@@ -365,6 +367,19 @@ __device__ __forceinline__ bool named_bar_and(int id, int n, bool ok) {
       : "r"(id), "r"(n), "r"(static_cast<int>(ok))
       : "memory");
   return r != 0;
+}
+
+// mbar_wait without the clock on the way of a short wait: it is first read after 1024 tries.
+__device__ __forceinline__ bool pipe_wait(uint64_t* bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+    if ((it & 1023u) == 0) {
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      else if (now - t0 > kWaitLimitNs) return false;
+    }
+  }
+  return true;
 }
 
 // ---- device primitives beyond common.cuh ------------------------------------------------------
@@ -547,7 +562,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
       // the segment's description, row table and query rows
       const int slot = static_cast<int>(n_seg % n_slots), row0 = slot * (SM::kQRows / n_slots);
       if (n_seg >= static_cast<uint32_t>(n_slots) &&
-          !mbar_wait(&seg_empty[slot], (n_seg / n_slots - 1) & 1u, nullptr, 0))
+          !pipe_wait(&seg_empty[slot], (n_seg / n_slots - 1) & 1u))
         ok = false;
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
@@ -604,7 +619,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
         const uint32_t tx = static_cast<uint32_t>(n * ld.box_rows() * HD * 2);
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
-          if (n_ld >= SM::kStages) ok = ok && mbar_wait(&empty[st], phase ^ 1u, nullptr, 0);
+          if (n_ld >= SM::kStages) ok = ok && pipe_wait(&empty[st], phase ^ 1u);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (lane == 0) {
@@ -625,9 +640,9 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
     if (!ok) {   // let the copies in flight land before the CTA goes
       if (lane == 0 && a.status) atomicOr(a.status, DEX_ATTN_TIMEOUT);
       for (uint32_t j = n_ld > SM::kStages ? n_ld - SM::kStages : 0; j < n_ld; ++j)
-        mbar_wait(&full[j % SM::kStages], (j / SM::kStages) & 1u, nullptr, 0);
+        pipe_wait(&full[j % SM::kStages], (j / SM::kStages) & 1u);
       for (uint32_t j = n_seg > static_cast<uint32_t>(n_slots) ? n_seg - n_slots : 0; j < n_seg; ++j)
-        mbar_wait(&seg_full[j % n_slots], (j / n_slots) & 1u, nullptr, 0);
+        pipe_wait(&seg_full[j % n_slots], (j / n_slots) & 1u);
     }
   } else {
     // ---------------- compute ----------------
@@ -641,7 +656,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
     int st = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t n) {
-      if (ok && !mbar_wait(bar, n & 1u, nullptr, 0)) {
+      if (ok && !pipe_wait(bar, n & 1u)) {
         if (a.status && lane == 0) atomicOr(a.status, DEX_ATTN_TIMEOUT);
         ok = false;
       }
@@ -866,8 +881,9 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
 // within 2^8, which both 16-bit types hold), so O is rescaled rarely: a rescale reads and writes
 // all of it through registers between two MMAs.
 // ============================================================================================
-constexpr int kTileThreads = 384;   // two softmax teams; producer, MMA issuer and two idle warps
+constexpr int kTileThreads = 384;   // two softmax teams; producer, an MMA issuer for each team, an idle warp
 constexpr float kRescale = 8.0f;
+
 
 template <int HD>
 struct TileSmem {
@@ -877,8 +893,8 @@ struct TileSmem {
   static constexpr uint32_t oMl = oRing + kStages * kBuf;            // float2 [128]
   static constexpr uint32_t oBar = oMl + 128 * 8;
   static constexpr uint32_t kBars = 2 * kStages + 9;
-  static constexpr uint32_t oMisc = oBar + kBars * 8;                // bad flags [stages], scratch [12], TMEM address
-  static constexpr uint32_t kTotal = oMisc + (kStages + 13) * 4 + 1024;
+  static constexpr uint32_t oMisc = oBar + kBars * 8;                // bad flags [stages], scratch [12], TMEM address, segment flag
+  static constexpr uint32_t kTotal = oMisc + (kStages + 15) * 4 + 1024;
   static_assert(kStages * kBuf >= kMaxBatch * 4, "tile counts use the ring before the first copy");
 };
 static_assert(TileSmem<128>::kTotal <= 227 * 1024, "tile_kernel shared memory");
@@ -888,28 +904,37 @@ namespace {
 __device__ __forceinline__ uint32_t sw_off(int row, int col) {   // element offset in a [128 rows][HD] tile, 64-column halves
   return static_cast<uint32_t>((col >> 6) * (128 * 128) + row * 128 + ((((col >> 3) & 7) ^ (row & 7)) << 4));
 }
-// K-major A or B descriptor: sw128_kmajor_desc of common.cuh; V as an MN-major B operand: 64 dims per
-// 128-byte row, keys 128 bytes apart in 1024-byte atoms, lbo between the 64-dim halves.
-__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>((128u * 128u) >> 4) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
-}
+// Shared-memory operand descriptors (128-byte swizzle, 1024-byte atoms) as two words; the upper one is the
+// same for all.  K-major (Q, K): rows of 64 dims; MN-major (V as the B operand): 64 dims per
+// 128-byte row, keys 128 bytes apart, the 64-dim halves 16 KB apart.  The issuing thread adds 16-byte
+// units to the lower word and nothing else: with descriptors built from scratch for every MMA it, not
+// the tensor pipe, set the pace (95 cycles per MMA of 64).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t k_desc(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t mn_desc(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (((128u * 128u) >> 4) << 16); }
 // kind::f16 with fp32 accumulators: type bits of A and B (0 fp16, 1 bf16), B MN-major or not
 __host__ __device__ constexpr uint32_t idesc(bool fp16, bool b_mn, int N) {
   return (1u << 4) | (fp16 ? 0u : (1u << 7) | (1u << 10)) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
          (8u << 24);
 }
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint64_t bdesc, uint32_t id, uint32_t accumulate) {
+// D (+)= A B with A in shared memory (descriptor) or in TMEM; accumulate is a compile-time choice but for
+// an accumulator's first MMA.
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t id, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a_tmem), "l"(bdesc), "r"(id), "r"(accumulate)
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(id), "r"(static_cast<uint32_t>(accumulate)), "n"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t id, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(id), "r"(static_cast<uint32_t>(accumulate)), "n"(kDescHi)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
@@ -972,6 +997,7 @@ __device__ __forceinline__ uint32_t seen_bits(const RowView& v, int lo, int hi, 
 
 // Loads of a segment's cnt tiles: K of the first `ahead` tiles, then V of tile j and K of tile
 // j + ahead in turn -- the order in which the MMAs take them.
+__device__ __forceinline__ int k_load(int j, int cnt, int ahead) { return j < ahead ? j : ahead + 2 * (j - ahead) + 1; }
 __device__ __forceinline__ int v_load(int j, int cnt, int ahead) {   // index of V_j among the 2 cnt loads
   const int a = min(ahead, cnt);
   return a + j + min(j, cnt - a);
@@ -990,11 +1016,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint64_t* q_full = empty + SM::kStages;   // [2] query tile of a team written
   uint64_t* s_full = q_full + 2;            // [2] scores of a team's tile in TMEM
   uint64_t* p_full = s_full + 2;            // [2] its probabilities in TMEM
-  uint64_t* pv_done = p_full + 2;           // [2] its PV complete
-  uint64_t* o_full = pv_done + 2;           // every MMA of the segment complete
+  uint64_t* turn = p_full + 2;              // [2] a team's issuer may go (two row tiles)
+  uint64_t* o_full = turn + 2;              // every MMA of the segment complete
   volatile int* bad_stage = reinterpret_cast<volatile int*>(smem + SM::oMisc);
   uint32_t* scratch = reinterpret_cast<uint32_t*>(smem + SM::oMisc) + SM::kStages;
   uint32_t* tmem_slot = scratch + 12;
+  volatile int* seg_bad = reinterpret_cast<volatile int*>(tmem_slot + 1);   // [2] the segment met a bad page (before o_full)
   uint32_t* cum = reinterpret_cast<uint32_t*>(smem + SM::oRing);
   const PrefixAttnArgs& a = w.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1002,15 +1029,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < SM::kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 2);   // both teams
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 128);
+      // one arrival per warp: 128 of them on one word take longer than a softmax
+      mbar_init(&q_full[i], 4);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
-      mbar_init(&pv_done[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&turn[i], 1);
     }
-    mbar_init(o_full, 1);
+    mbar_init(o_full, 4);   // both issuers: their MMAs and their word on the segment's pages
     fence_mbar_init();
     tma_prefetch(&tm);
   }
@@ -1045,6 +1073,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     float* join = reinterpret_cast<float*>(smem + SM::oQ);   // [HD][128] O of team 1
     float2* join_ml = reinterpret_cast<float2*>(smem + SM::oMl);
     uint32_t n_s = 0, n_seg = 0, base = 0;   // score tiles of this team, segments, loads so far
+    auto free_load = [&](uint32_t load, bool both) {   // the stage of a load goes back (both: for the other team too)
+      uint64_t* bar = &empty[load % SM::kStages];
+      mbar_arrive(bar);
+      if (both) mbar_arrive(bar);
+    };
     bool ok = true;
     for (uint32_t g = g0; g < g1;) {
       const int cnt = min(wk.k.nt - tile, static_cast<int>(g1 - g));
@@ -1054,45 +1087,52 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const bool on = r < wk.rows;
       if (!alt || team == 0) {
         // the team's query rows, HD / 8 threads per row; zero beyond the segment
-        uint8_t* dst = smem + SM::oQ + (alt ? 0 : team) * SM::kBuf;
-        const int row0 = alt ? 0 : team * 128;
+        constexpr int kStep = 1024 / HD;   // rows of one pass, a multiple of the swizzle's eight
+        const int row0 = alt ? 0 : team * 128, e = (r128 % (HD / 8)) * 8;
+        uint8_t* dst = smem + SM::oQ + (alt ? 0 : team) * SM::kBuf + sw_off(r128 / (HD / 8), e);
 #pragma unroll 4
-        for (int i = 0; i < HD / 8; ++i) {
-          const int rr = i * (1024 / HD) + r128 / (HD / 8), e = (r128 % (HD / 8)) * 8;
+        for (int rr = r128 / (HD / 8); rr < 128; rr += kStep, dst += kStep * 128) {
           if (row0 + rr < wk.rows) {
             int t, h;
             wk.row_of(row0 + rr, t, h);
-            cp_async_16(smem_u32(dst + sw_off(rr, e)), static_cast<const T*>(a.q) + t * a.q_stride + h * HD + e);
+            cp_async_16(smem_u32(dst), static_cast<const T*>(a.q) + t * a.q_stride + h * HD + e);
           } else {
-            *reinterpret_cast<uint4*>(dst + sw_off(rr, e)) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
           }
         }
         cp_async_commit();
         cp_async_wait_all();
         if (a.scale_log2 <= 0.0f) {   // c is positive: the queries take the sign (zero for a zero scale)
           for (int i = 0; i < HD / 8; ++i) {
-            uint4* v = reinterpret_cast<uint4*>(dst + sw_off(i * (1024 / HD) + r128 / (HD / 8), (r128 % (HD / 8)) * 8));
+            uint4* v = reinterpret_cast<uint4*>(dst -= kStep * 128);
             const uint32_t keep = a.scale_log2 < 0.0f ? 0xffffffffu : 0u, flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
             *v = make_uint4((v->x & keep) ^ flip, (v->y & keep) ^ flip, (v->z & keep) ^ flip, (v->w & keep) ^ flip);
           }
         }
         fence_proxy_async_smem();
-        mbar_arrive(&q_full[team]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[team]);
       }
       int t_row = 0, h_row = 0;   // the thread's row
       if (on) wk.row_of(r, t_row, h_row);
       RowView rv{0x7fffffff, 0, 0, false};
       if (on) rv = wk.prefix ? row_view(a, seq_ref(a, seq_of_token(a, t_row)), t_row) : row_view(a, wk.s, t_row);
       float m = -INFINITY, l = 0.0f;
-      bool bad = !wk.prefix && wk.s.bad, any = false;   // any: this team had a tile
+      bool any = false;   // this team had a tile
+      int last = -1;      // its last one
       for (int j = alt ? team : 0; j < cnt; j += ahead == 2 ? 2 : 1) {
-        if (ok && !mbar_wait(&s_full[team], n_s & 1u, nullptr, 0)) {
+        if (ok && !pipe_wait(&s_full[team], n_s & 1u)) {
           timed_out();
           ok = false;
         }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
+        if (r128 == 0) {   // K of this tile and V of the team's tile before it are read
+          free_load(base + static_cast<uint32_t>(k_load(j, cnt, ahead)), alt);
+          if (any) free_load(base + static_cast<uint32_t>(v_load(j - ahead, cnt, ahead)), alt);
+          last = j;
+        }
         const int key0 = (wk.k.t0 + tile + j) * kTileKeys;
         const bool whole = wk.k.lo <= key0 && wk.k.hi >= key0 + kTileKeys;
         // the row's maximum, 32 columns at a time; masked scores go back to TMEM as -inf
@@ -1128,14 +1168,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const bool move = mx > m + kRescale || (m == -INFINITY && mx > -INFINITY);
         if (__any_sync(0xffffffffu, move)) {
           const float f = move ? ex2(m - mx) : 1.0f;
-          if (any) {
-            if (!mbar_wait(&pv_done[team], (n_s - 1) & 1u, nullptr, 0)) {
-              timed_out();
-              ok = false;
-            }
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc_fence_after();
+          if (any) {   // the PV before is complete: its issuer committed the scores after it
 #pragma unroll 1
             for (int q = 0; q < HD / 32; ++q) {
               uint32_t o[32];
@@ -1150,6 +1183,24 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           l *= f;
         }
         any = true;
+        if (!whole) {
+          // rows of V outside the segment hold anything, and P = 0 must meet a finite v
+          const uint32_t vl = base + static_cast<uint32_t>(v_load(j, cnt, ahead));
+          const int st = static_cast<int>(vl % SM::kStages);
+          if (!pipe_wait(&full[st], (vl / SM::kStages) & 1u)) {
+            timed_out();
+            ok = false;
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          uint8_t* vt = smem + SM::oRing + st * SM::kBuf;
+          for (int x = r128; x < kTileKeys * HD / 8; x += 128) {
+            const int row = x / (HD / 8), ch = x % (HD / 8);
+            if (key0 + row < wk.k.lo || key0 + row >= wk.k.hi)
+              *reinterpret_cast<uint4*>(vt + (ch >> 3) * (128 * 128) + row * 128 + (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
         const float sub = m > -INFINITY ? m : 0.0f;
         uint64_t l2[2] = {0ull, 0ull};   // two fp32 sums each
         const uint64_t c2 = f32x2(c, c), sub2 = f32x2(-sub, -sub);
@@ -1168,42 +1219,25 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           // P of columns 32 q .. takes the columns 16 q .., whose scores are in registers by now
           tmem_st16(t_s + q * 16, p);
         }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[team]);
         {
           const uint64_t t2 = add2(l2[0], l2[1]);
           l += __uint_as_float(static_cast<uint32_t>(t2)) + __uint_as_float(static_cast<uint32_t>(t2 >> 32));
         }
-        tmem_wait_st();
-        tc_fence_before();
-        // V of this tile: rows outside the segment hold anything, and P = 0 must meet a finite v
-        const uint32_t vl = base + static_cast<uint32_t>(v_load(j, cnt, ahead));
-        const int st = static_cast<int>(vl % SM::kStages);
-        if (!mbar_wait(&full[st], (vl / SM::kStages) & 1u, nullptr, 0)) {
-          timed_out();
-          ok = false;
-        }
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        bad |= bad_stage[st] != 0;
-        if (!whole) {
-          uint8_t* vt = smem + SM::oRing + st * SM::kBuf;
-          for (int x = r128; x < kTileKeys * HD / 8; x += 128) {
-            const int row = x / (HD / 8), ch = x % (HD / 8);
-            if (key0 + row < wk.k.lo || key0 + row >= wk.k.hi)
-              *reinterpret_cast<uint4*>(vt + (ch >> 3) * (128 * 128) + row * 128 + (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-        }
-        mbar_arrive(&p_full[team]);
         ++n_s;
       }
       // ---------------- the segment's result ----------------
-      if (ok && !mbar_wait(o_full, n_seg & 1u, nullptr, 0)) {
+      if (ok && !pipe_wait(o_full, n_seg & 1u)) {
         timed_out();
         ok = false;
       }
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
-      if (bad || !ok) l = quiet_nan();
+      if (r128 == 0 && last >= 0) free_load(base + static_cast<uint32_t>(v_load(last, cnt, ahead)), alt);
+      if (!ok || seg_bad[0] || seg_bad[1] || (!wk.prefix && wk.s.bad)) l = quiet_nan();
       const bool read = ok && any;   // warp-uniform
       if (alt && team == 1) {
         join_ml[r128] = make_float2(m, l);
@@ -1300,7 +1334,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         int first = 0, page;
         const int n = ld.boxes(key0, wk.k.lo, wk.k.hi, first);
         ld.prefetch(first, n);
-        if (n_ld >= SM::kStages && !mbar_wait(&empty[st], (n_ld / SM::kStages - 1) & 1u, nullptr, 0)) ok = false;
+        if (n_ld >= SM::kStages && !pipe_wait(&empty[st], (n_ld / SM::kStages - 1) & 1u)) ok = false;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) {
           if (lane == 0) timed_out();
@@ -1334,96 +1368,101 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       if (!ok) {   // let the copies in flight land before the CTA goes
         for (uint32_t i = n_ld > SM::kStages ? n_ld - SM::kStages : 0; i < n_ld; ++i)
-          mbar_wait(&full[i % SM::kStages], (i / SM::kStages) & 1u, nullptr, 0);
+          pipe_wait(&full[i % SM::kStages], (i / SM::kStages) & 1u);
       }
-    } else if (warp == 9 && lane == 0) {
-      // ---------------- MMA issuer ----------------
+    } else if (warp < 11 && lane == 0) {
+      // ---------------- MMA issuer of a team ----------------
+      // One thread for both teams cannot keep the tensor pipe fed: waits, commits and bookkeeping between
+      // two blocks of MMAs take longer than the few MMAs that are queued (850 cycles per block of 512).
+      // With two row tiles the issuers take turns, a PV and the next scores each: left alone the teams fall
+      // into step, both in their softmax and then both waiting for their MMAs.
+      // A commit costs it as much as an MMA, so there is one per key tile: the scores' commit also tells the
+      // team that its PV before is complete and that the stages of both are free.
+      const int team = warp - 9;
       constexpr bool kFp16 = std::is_same<T, __half>::value;
       constexpr uint32_t id_qk = idesc(kFp16, false, kTileKeys), id_pv = idesc(kFp16, true, HD);
-      const uint32_t q0 = smem_u32(smem + SM::oQ), ring = smem_u32(smem + SM::oRing);
-      uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_ld = 0;
+      const uint32_t q_desc = k_desc(smem_u32(smem + SM::oQ)), ring_k = k_desc(smem_u32(smem + SM::oRing));
+      const uint32_t ring_v = mn_desc(smem_u32(smem + SM::oRing));
+      const uint32_t t_s = tmem + static_cast<uint32_t>(team) * 128, t_o = t_s + 256;
+      uint32_t n_seg = 0, n_q1 = 0, n_p = 0, n_turn = 0, st = 0, phase = 0;   // st, phase: the next load of the ring
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t n) {
-        if (ok && !mbar_wait(bar, n & 1u, nullptr, 0)) {
+        if (ok && !pipe_wait(bar, n & 1u)) {
           timed_out();
           ok = false;
         }
         tc_fence_after();
         return ok;
       };
-      auto wait_load = [&] { return wait(&full[n_ld % SM::kStages], n_ld / SM::kStages); };
-      auto qk = [&](int team, int q, uint32_t kt) {
+      auto skip_load = [&] {   // the next load's stage, without waiting for it
+        const uint32_t at = st;
+        if (++st == SM::kStages) st = 0, phase ^= 1u;
+        return at;
+      };
+      auto next_load = [&] {
+        wait(&full[st], phase);
+        return skip_load();
+      };
+      auto qk = [&](uint32_t q, uint32_t stage) {
+        const uint32_t a0 = q_desc + q, b0 = ring_k + stage * (SM::kBuf >> 4);
 #pragma unroll
         for (int ks = 0; ks < HD / 16; ++ks) {
-          const uint32_t off = static_cast<uint32_t>((ks >> 2) * 128 * 128 + (ks & 3) * 32);
-          umma_bf16(tmem + static_cast<uint32_t>(team) * 128, sw128_kmajor_desc(q0 + static_cast<uint32_t>(q) * SM::kBuf + off),
-                    sw128_kmajor_desc(kt + off), id_qk, ks > 0 ? 1u : 0u);
+          const uint32_t off = static_cast<uint32_t>((ks >> 2) * 128 * 128 + (ks & 3) * 32) >> 4;
+          umma_ss(t_s, a0 + off, b0 + off, id_qk, ks > 0);
         }
         umma_commit(&s_full[team]);
       };
-      auto pv = [&](int team, uint32_t vt, bool first) {
+      auto pv = [&](uint32_t stage, bool first) {
+        const uint32_t b0 = ring_v + stage * (SM::kBuf >> 4);
 #pragma unroll
         for (int ks = 0; ks < kTileKeys / 16; ++ks)
-          umma_ts(tmem + 256 + static_cast<uint32_t>(team) * 128, tmem + static_cast<uint32_t>(team) * 128 + ks * 8,
-                  mn_desc(vt + ks * 16 * 128), id_pv, first && ks == 0 ? 0u : 1u);
-        umma_commit(&pv_done[team]);
+          umma_ts(t_o, t_s + ks * 8, b0 + ks * 128, id_pv, ks > 0 || !first);
       };
-      for (uint32_t g = g0; g < g1 && ok;) {
+      for (uint32_t g = g0; g < g1 && ok; ++n_seg) {
         const int cnt = min(wk.k.nt - tile, static_cast<int>(g1 - g));
         const bool alt = wk.rows <= 128;
-        if (!wait(&q_full[0], n_q[0]++)) break;
-        if (!alt && !wait(&q_full[1], n_q[1]++)) break;
         const int ahead = alt ? 2 : 1;
-        for (int j = 0; j < min(ahead, cnt) && wait_load(); ++j) {
-          const uint32_t st = n_ld++ % SM::kStages, kt = ring + st * SM::kBuf;
-          if (alt) {
-            qk(j, 0, kt);
-          } else {
-            qk(0, 0, kt);
-            qk(1, 1, kt);
+        const uint32_t q = alt ? 0 : static_cast<uint32_t>(team) * (SM::kBuf >> 4);
+        int bad = 0;
+        if (alt || team == 0) wait(&q_full[0], n_seg);
+        else wait(&q_full[1], n_q1++);
+        for (int j = 0; j < min(ahead, cnt) && ok; ++j) {
+          if (alt && j != team) {
+            skip_load();
+            continue;
           }
-          umma_commit(&empty[st]);
+          const uint32_t k = next_load();
+          if (!ok) break;
+          qk(q, k);
         }
         for (int j = 0; j < cnt && ok; ++j) {
-          if (!wait_load()) break;
-          const uint32_t vst = n_ld++ % SM::kStages, vt = ring + vst * SM::kBuf;
           const bool more = j + ahead < cnt;
-          if (alt) {
-            const int team = j & 1;
-            if (!wait(&p_full[team], n_p[team]++)) break;
-            pv(team, vt, j < 2);
-            umma_commit(&empty[vst]);
-            if (more) {
-              if (!wait_load()) break;
-              const uint32_t st = n_ld++ % SM::kStages;
-              qk(team, 0, ring + st * SM::kBuf);
-              umma_commit(&empty[st]);
-            }
-          } else {
-            uint32_t st = 0;
-            for (int team = 0; team < 2 && ok; ++team) {
-              if (!wait(&p_full[team], n_p[team]++)) break;
-              pv(team, vt, j == 0);
-              if (team == 1) umma_commit(&empty[vst]);
-              if (more) {
-                if (team == 0) {
-                  if (!wait_load()) break;
-                  st = n_ld++ % SM::kStages;
-                }
-                qk(team, team, ring + st * SM::kBuf);
-                if (team == 1) umma_commit(&empty[st]);
-              }
-            }
+          if (alt && (j & 1) != team) {
+            skip_load();
+            if (more) skip_load();
+            continue;
           }
+          const uint32_t v = next_load();
+          if (!ok) break;
+          bad |= bad_stage[v];
+          const uint32_t k = more ? next_load() : 0;
+          wait(&p_full[team], n_p++);
+          if (!alt) {
+            if (team == 1) wait(&turn[1], n_turn);
+            else if (n_turn > 0) wait(&turn[0], n_turn - 1);
+            ++n_turn;
+          }
+          if (!ok) break;
+          pv(v, j < ahead);
+          if (more) qk(q, k);
+          if (!alt) mbar_arrive(&turn[team ^ 1]);
         }
+        seg_bad[team] = bad || !ok;   // the teams read it after o_full
         umma_commit(o_full);
+        mbar_arrive(o_full);
         g += static_cast<uint32_t>(cnt);
         if (g < g1) wk.next();
         tile = 0;
-      }
-      if (!ok) {   // every MMA issued is complete before TMEM goes
-        umma_commit(o_full);
-        // the phase is not known after a break; the teams' bounded waits give the MMAs their time
       }
     }
   }
