@@ -1128,61 +1128,49 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        if (r128 == 0) {   // K of this tile and V of the team's tile before it are read
-          free_load(base + static_cast<uint32_t>(k_load(j, cnt, ahead)), alt);
-          if (any) free_load(base + static_cast<uint32_t>(v_load(j - ahead, cnt, ahead)), alt);
-          last = j;
-        }
         const int key0 = (wk.k.t0 + tile + j) * kTileKeys;
         const bool whole = wk.k.lo <= key0 && wk.k.hi >= key0 + kTileKeys;
-        // the row's maximum, 32 columns at a time; masked scores go back to TMEM as -inf
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         uint32_t s[2][32];
-        tmem_ld32_nowait(t_s, s[0]);
-        if (__all_sync(0xffffffffu, whole && rv.last >= key0 + kTileKeys - 1)) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            tmem_wait_ld();
-            if (q < 3) tmem_ld32_nowait(t_s + (q + 1) * 32, s[(q + 1) & 1]);
-#pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              mx4[(i >> 1) & 3] = max3(mx4[(i >> 1) & 3], __uint_as_float(s[q & 1][i]), __uint_as_float(s[q & 1][i + 1]));
-          }
-        } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            tmem_wait_ld();
-            const uint32_t bits = seen_bits(rv, wk.k.lo, wk.k.hi, key0 + q * 32);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              if (!(bits >> i & 1u)) s[0][i] = 0xff800000u;   // -inf
-              mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(s[0][i]));
-            }
-            tmem_st32(t_s + q * 32, s[0]);
-            if (q < 3) tmem_ld32_nowait(t_s + (q + 1) * 32, s[0]);
-          }
-          tmem_wait_st();
-        }
-        tmem_ld32_nowait(t_s, s[0]);   // again, for P (in flight under what follows)
-        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
-        const bool move = mx > m + kRescale || (m == -INFINITY && mx > -INFINITY);
-        if (__any_sync(0xffffffffu, move)) {
-          const float f = move ? ex2(m - mx) : 1.0f;
+        float tile_l, tile_m = -INFINITY;   // sum and maximum of this tile
+        // Moves the row's m to the tile's maximum where that is larger by more than kRescale (or the first).
+        auto move_m = [&] {
+          const bool move = tile_m > m + kRescale || (m == -INFINITY && tile_m > -INFINITY);
+          if (!__any_sync(0xffffffffu, move)) return false;
+          const float f = move ? ex2(m - tile_m) : 1.0f;
           if (any) {   // the PV before is complete: its issuer committed the scores after it
 #pragma unroll 1
             for (int q = 0; q < HD / 32; ++q) {
-              uint32_t o[32];
+              uint32_t(&o)[32] = s[0];
               tmem_ld32_nowait(t_o + q * 32, o);
               tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
               tmem_st32(t_o + q * 32, o);
             }
+            tmem_wait_st();
           }
-          if (move) m = mx;
+          if (move) m = tile_m;
           l *= f;
+          return true;
+        };
+        if (!any || !__all_sync(0xffffffffu, whole && rv.last >= key0 + kTileKeys - 1)) {
+          // a team's first tile needs its maximum first; masked scores go back to TMEM as -inf
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            tmem_ld32_nowait(t_s + q * 32, s[0]);
+            tmem_wait_ld();
+            const uint32_t bits = seen_bits(rv, wk.k.lo, wk.k.hi, key0 + q * 32);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              if (!(bits >> i & 1u)) s[0][i] = 0xff800000u;   // -inf
+              tile_m = fmaxf(tile_m, __uint_as_float(s[0][i]));
+            }
+            tmem_st32(t_s + q * 32, s[0]);
+          }
+          tmem_wait_st();
+          tile_m *= c;
+          move_m();
         }
-        any = true;
         if (!whole) {
           // rows of V outside the segment hold anything, and P = 0 must meet a finite v
           const uint32_t vl = base + static_cast<uint32_t>(v_load(j, cnt, ahead));
@@ -1201,31 +1189,45 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
           fence_proxy_async_smem();
         }
-        const float sub = m > -INFINITY ? m : 0.0f;
-        uint64_t l2[2] = {0ull, 0ull};   // two fp32 sums each
-        const uint64_t c2 = f32x2(c, c), sub2 = f32x2(-sub, -sub);
+        // P with the m at hand, and the maximum on the way: it rarely asks for another m, and then the
+        // scores are still in TMEM
+        uint32_t p[4][16];
+        do {
+          const float sub = m > -INFINITY ? m : 0.0f;
+          uint64_t l2[2] = {0ull, 0ull};   // two fp32 sums each
+          const uint64_t c2 = f32x2(c, c), sub2 = f32x2(-sub, -sub);
+          float mx[2] = {-INFINITY, -INFINITY};
+          tmem_ld32_nowait(t_s, s[0]);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          tmem_wait_ld();
-          if (q < 3) tmem_ld32_nowait(t_s + (q + 1) * 32, s[(q + 1) & 1]);
-          uint32_t p[16];
+          for (int q = 0; q < 4; ++q) {
+            tmem_wait_ld();
+            if (q < 3) tmem_ld32_nowait(t_s + (q + 1) * 32, s[(q + 1) & 1]);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint64_t x = fma2(u32x2(s[q & 1][2 * i], s[q & 1][2 * i + 1]), c2, sub2);
-            const float p0 = ex2(__uint_as_float(static_cast<uint32_t>(x))), p1 = ex2(__uint_as_float(static_cast<uint32_t>(x >> 32)));
-            l2[i & 1] = add2(l2[i & 1], f32x2(p0, p1));
-            p[i] = pack2<T>(p0, p1);
+            for (int i = 0; i < 16; ++i) {
+              const uint32_t s0 = s[q & 1][2 * i], s1 = s[q & 1][2 * i + 1];
+              mx[i & 1] = max3(mx[i & 1], __uint_as_float(s0), __uint_as_float(s1));
+              const uint64_t x = fma2(u32x2(s0, s1), c2, sub2);
+              const float p0 = ex2(__uint_as_float(static_cast<uint32_t>(x))), p1 = ex2(__uint_as_float(static_cast<uint32_t>(x >> 32)));
+              l2[i & 1] = add2(l2[i & 1], f32x2(p0, p1));
+              p[q][i] = pack2<T>(p0, p1);
+            }
           }
-          // P of columns 32 q .. takes the columns 16 q .., whose scores are in registers by now
-          tmem_st16(t_s + q * 16, p);
-        }
+          const uint64_t t2 = add2(l2[0], l2[1]);
+          tile_l = __uint_as_float(static_cast<uint32_t>(t2)) + __uint_as_float(static_cast<uint32_t>(t2 >> 32));
+          tile_m = fmaxf(mx[0], mx[1]) * c;
+        } while (move_m());
+        l += tile_l;
+        any = true;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_st16(t_s + q * 16, p[q]);   // over the scores
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[team]);
-        {
-          const uint64_t t2 = add2(l2[0], l2[1]);
-          l += __uint_as_float(static_cast<uint32_t>(t2)) + __uint_as_float(static_cast<uint32_t>(t2 >> 32));
+        if (r128 == 0) {   // K of this tile and V of the team's tile before it are read
+          free_load(base + static_cast<uint32_t>(k_load(j, cnt, ahead)), alt);
+          if (last >= 0) free_load(base + static_cast<uint32_t>(v_load(last, cnt, ahead)), alt);
+          last = j;
         }
         ++n_s;
       }
@@ -1446,16 +1448,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (!ok) break;
           bad |= bad_stage[v];
           const uint32_t k = more ? next_load() : 0;
-          wait(&p_full[team], n_p++);
           if (!alt) {
             if (team == 1) wait(&turn[1], n_turn);
             else if (n_turn > 0) wait(&turn[0], n_turn - 1);
             ++n_turn;
           }
-          if (!ok) break;
+          if (!wait(&p_full[team], n_p++)) break;
           pv(v, j < ahead);
-          if (more) qk(q, k);
           if (!alt) mbar_arrive(&turn[team ^ 1]);
+          if (more) qk(q, k);
         }
         seg_bad[team] = bad || !ok;   // the teams read it after o_full
         umma_commit(o_full);
