@@ -425,27 +425,37 @@ class PagedCache:
         # the geometry checks of the library, which look at the sizes alone
         dex_prefix_attention_workspace(self.kv, dex_attention_args(n_heads=kvh, max_q=1, scale=1.0))
         self._on_device(table=table)
+        # what every call needs: a small one is bound by the time it takes to get to its launch
+        self._dev = pages.get_device() if pages.is_cuda else None
+        self._kv_ref, self._dtype, self._i32 = C.byref(self.kv), pages.dtype, torch.int32
+        self._lib_append, self._lib_attention = lib().dex_paged_append, lib().dex_prefix_attention
 
     def _on_device(self, **tensors):
         for name, t in tensors.items():
             _need(t is None or (t.is_cuda and t.device == self.device), f"{name} must be on the pages' CUDA device")
 
-    def _rows(self, name, t, heads, n=None):
-        """[n, heads, head_dim] with the rows of a token contiguous; the stride between tokens."""
-        hd = self.head_dim
-        _need(t.dim() == 3 and t.shape[2] == hd and (heads is None or t.shape[1] == heads) and
-              (n is None or t.shape[0] == n) and t.stride(2) == 1 and (t.stride(1) == hd or t.shape[1] == 1),
-              f"{name} must be [tokens{'' if n is None else f' = {n}'}, {heads or 'heads'}, {hd}] with contiguous heads")
-        return t.stride(0) if t.shape[0] > 1 else t.shape[1] * hd
+    def _rows(self, name, t, heads, n):
+        """[n, heads, head_dim] with the rows of a token contiguous: the stride between tokens."""
+        shape, stride, hd = t.shape, t.stride(), self.head_dim
+        if not (len(shape) == 3 and shape[2] == hd and (heads is None or shape[1] == heads) and shape[0] == n and
+                stride[2] == 1 and (stride[1] == hd or shape[1] == 1)):
+            raise DexError(DEX_EINVAL, f"{name} must be [tokens = {n}, {heads or 'heads'}, {hd}] with contiguous heads")
+        return stride[0] if n > 1 else shape[1] * hd
 
-    def _index(self, name, t, n, dtype=None):
-        _need(t.dim() == 1 and t.shape[0] == n and t.is_contiguous() and t.dtype == (dtype or self._torch.int32),
-              f"{name} must be a contiguous {dtype or self._torch.int32} vector of {n}")
+    def _vector(self, name, t, n, dtype):
+        if not (t.dtype == dtype and t.dim() == 1 and t.shape[0] == n and t.is_contiguous()):
+            raise DexError(DEX_EINVAL, f"{name} must be a contiguous {dtype} vector of {n}")
         return t.data_ptr()
 
-    def _run(self, fn, *args):
-        with self._torch.cuda.device(self.device):
-            fn(*args, self._torch.cuda.current_stream().cuda_stream)
+    def _run(self, fn, where, *args):
+        cuda = self._torch._C
+        if cuda._cuda_getDevice() == self._dev:
+            rc = fn(*args, cuda._cuda_getCurrentRawStream(self._dev))
+        else:
+            with self._torch.cuda.device(self._dev):
+                rc = fn(*args, cuda._cuda_getCurrentRawStream(self._dev))
+        if rc != DEX_OK:
+            check(rc, where)
 
     def append(self, k, v, seq, pos, q=None, q_out=None, theta: float = 10000.0, rope_pos=None, rejected=None):
         """Store k (rotated) and v of token t at position pos[t] of sequence seq[t]; return q rotated.
@@ -456,29 +466,31 @@ class PagedCache:
         [tokens, heads, head_dim] in the cache's type, allocated when not given; it may be q itself.
         rejected: int32 [1], receives the number of tokens out of range, which are skipped.
         """
-        torch = self._torch
-        n = k.shape[0]
-        _need(k.dtype == v.dtype and (k.dtype == self.pages.dtype or k.dtype == torch.float32),
-              "k and v must have the cache's type or fp32")
-        a = dex_append_args(k=k.data_ptr(), v=v.data_ptr(), k_stride=self._rows("k", k, self.kv_heads),
-                            v_stride=self._rows("v", v, self.kv_heads, n), seq=self._index("seq", seq, n),
-                            pos=self._index("pos", pos, n), n_tokens=n, rope_theta=theta,
-                            in_dtype=DEX_DT_FP32 if k.dtype == torch.float32 else self.kv.dtype)
-        if rope_pos is not None:
-            a.rope_pos = self._index("rope_pos", rope_pos, n)
+        n, f32 = k.shape[0], self._torch.float32
+        if not (k.dtype == v.dtype and (k.dtype == self._dtype or k.dtype == f32)):
+            raise DexError(DEX_EINVAL, "k and v must have the cache's type or fp32")
+        a = dex_append_args(None, k.data_ptr(), v.data_ptr(), None, 0, self._rows("k", k, self.kv_heads, n),
+                            self._rows("v", v, self.kv_heads, n), 0, self._vector("seq", seq, n, self._i32),
+                            self._vector("pos", pos, n, self._i32),
+                            None if rope_pos is None else self._vector("rope_pos", rope_pos, n, self._i32), n, 0,
+                            DEX_DT_FP32 if k.dtype == f32 else self.kv.dtype, theta)
         _need(q is not None or q_out is None, "q_out needs q")
         if q is not None:
             a.q_stride = self._rows("q", q, None, n)
-            _need(q.dtype == k.dtype, "q must have the type of k")
+            if q.dtype != k.dtype:
+                raise DexError(DEX_EINVAL, "q must have the type of k")
+            heads = q.shape[1]
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=self.pages.dtype, device=q.device)
-            a.q_out_stride = self._rows("q_out", q_out, q.shape[1], n)
-            _need(q_out.dtype == self.pages.dtype, "q_out must have the cache's type")
-            a.q, a.q_out, a.n_heads = q.data_ptr(), q_out.data_ptr(), q.shape[1]
-        if rejected is not None:
-            self._index("rejected", rejected, 1)
-        self._on_device(k=k, v=v, q=q, q_out=q_out, seq=seq, pos=pos, rope_pos=rope_pos, rejected=rejected)
-        self._run(dex_paged_append, self.kv, a, 0 if rejected is None else rejected.data_ptr())
+                q_out = self._torch.empty(q.shape, dtype=self._dtype, device=q.device)
+            a.q_out_stride = self._rows("q_out", q_out, heads, n)
+            if q_out.dtype != self._dtype:
+                raise DexError(DEX_EINVAL, "q_out must have the cache's type")
+            a.q, a.q_out, a.n_heads = q.data_ptr(), q_out.data_ptr(), heads
+        rejected_ptr = None if rejected is None else self._vector("rejected", rejected, 1, self._i32)
+        for t in (k, v, q, q_out, seq, pos, rope_pos, rejected):
+            if t is not None and t.get_device() != self._dev:
+                self._on_device(k=k, v=v, q=q, q_out=q_out, seq=seq, pos=pos, rope_pos=rope_pos, rejected=rejected)
+        self._run(self._lib_append, "dex_paged_append", self._kv_ref, C.byref(a), rejected_ptr)
         return q_out
 
     def attention_workspace(self, q, max_q: int, prefix_len: int = 0):
@@ -501,36 +513,40 @@ class PagedCache:
         attention_workspace(), allocated when not given.  status: int32 [1], receives DEX_ATTN_* bits.
         Rows of out and lse that belong to no sequence are left as they were.
         """
-        torch = self._torch
-        n, batch = q.shape[0], self.kv.batch
-        _need(0 <= prefix_len < 2 ** 31 and 0 < max_q < 2 ** 31, "prefix_len or max_q out of range")
-        a = dex_attention_args(q=q.data_ptr(), q_stride=self._rows("q", q, None), n_tokens=n, n_heads=q.shape[1],
-                               q_start=self._index("q_start", q_start, batch + 1),
-                               seq_len=self._index("seq_len", seq_len, batch), max_q=max_q, prefix_len=prefix_len,
-                               scale=self.head_dim ** -0.5 if scale is None else scale)
-        _need(q.dtype == self.pages.dtype, "q must have the cache's type")
+        i32, batch = self._i32, self.kv.batch
+        n, heads = q.shape[0], q.shape[1]
+        if not (0 <= prefix_len < 2 ** 31 and 0 < max_q < 2 ** 31):
+            raise DexError(DEX_EINVAL, "prefix_len or max_q out of range")
+        if q.dtype != self._dtype:
+            raise DexError(DEX_EINVAL, "q must have the cache's type")
         if out is None:
-            out = torch.empty((n, q.shape[1], self.head_dim), dtype=q.dtype, device=q.device)
-        _need(out.dtype == q.dtype, "out must have the cache's type")
-        a.out, a.out_stride = out.data_ptr(), self._rows("out", out, q.shape[1], n)
+            out = self._torch.empty((n, heads, self.head_dim), dtype=q.dtype, device=q.device)
+        elif out.dtype != q.dtype:
+            raise DexError(DEX_EINVAL, "out must have the cache's type")
+        a = dex_attention_args(q.data_ptr(), out.data_ptr(), None, self._rows("q", q, None, n),
+                               self._rows("out", out, heads, n), self._vector("q_start", q_start, batch + 1, i32),
+                               self._vector("seq_len", seq_len, batch, i32), None, None, n, heads, max_q, prefix_len,
+                               self.head_dim ** -0.5 if scale is None else scale)
         if prefix_table is not None:
-            a.prefix_table = self._index("prefix_table", prefix_table, prefix_table.numel())
+            a.prefix_table = self._vector("prefix_table", prefix_table, prefix_table.numel(), i32)
             _need(prefix_table.numel() * self.kv.page_size >= prefix_len, "prefix_table is shorter than prefix_len")
         if tree_mask is not None:
-            a.tree_mask = self._index("tree_mask", tree_mask, n, torch.int64)
+            a.tree_mask = self._vector("tree_mask", tree_mask, n, self._torch.int64)
         if lse is not None:
-            _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == q.shape[:2],
-                  "lse must be contiguous fp32 [tokens, heads]")
+            if not (lse.dtype == self._torch.float32 and lse.is_contiguous() and lse.shape == q.shape[:2]):
+                raise DexError(DEX_EINVAL, "lse must be contiguous fp32 [tokens, heads]")
             a.lse = lse.data_ptr()
-        if status is not None:
-            self._index("status", status, 1)
+        status_ptr = None if status is None else self._vector("status", status, 1, i32)
         if workspace is None:
             workspace = self.attention_workspace(q, max_q, prefix_len)
-        _need(workspace.is_contiguous(), "workspace must be contiguous")
-        self._on_device(q=q, out=out, q_start=q_start, seq_len=seq_len, prefix_table=prefix_table,
-                        tree_mask=tree_mask, lse=lse, workspace=workspace, status=status)
-        self._run(dex_prefix_attention, self.kv, a, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                  0 if status is None else status.data_ptr())
+        elif not workspace.is_contiguous():
+            raise DexError(DEX_EINVAL, "workspace must be contiguous")
+        for t in (q, out, q_start, seq_len, workspace, prefix_table, tree_mask, lse, status):
+            if t is not None and t.get_device() != self._dev:
+                self._on_device(q=q, out=out, q_start=q_start, seq_len=seq_len, prefix_table=prefix_table,
+                                tree_mask=tree_mask, lse=lse, workspace=workspace, status=status)
+        self._run(self._lib_attention, "dex_prefix_attention", self._kv_ref, C.byref(a), workspace.data_ptr(),
+                  workspace.nbytes, status_ptr)
         return out
 
 
