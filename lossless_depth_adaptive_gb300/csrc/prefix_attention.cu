@@ -285,9 +285,6 @@ struct RowView {
   int first;       // tree: position of the first query
   uint64_t word;
   bool owned;      // the row belongs to a sequence (its result is written)
-  __device__ __forceinline__ bool sees(int j) const {
-    return j <= last || (word != 0 && j >= first && j - first < 64 && ((word >> (j - first)) & 1));
-  }
 };
 __device__ __forceinline__ RowView row_view(const PrefixAttnArgs& a, const SeqRef& s, int t) {
   RowView v;
@@ -298,6 +295,23 @@ __device__ __forceinline__ RowView row_view(const PrefixAttnArgs& a, const SeqRe
   if (s.bad) v.last = -1, v.word = 0;
   if (!v.owned) v.last = 0x7fffffff;   // its result is not used: no reason to mask
   return v;
+}
+
+// Which of the 32 keys from `at` on a row sees, within [lo, hi).
+__device__ __forceinline__ uint32_t range_bits(int from, int to) {   // bits from .. to - 1 of a word
+  from = max(from, 0);
+  to = min(to, 32);
+  if (to <= from) return 0u;
+  return (0xffffffffu >> (32 - (to - from))) << from;
+}
+__device__ __forceinline__ uint32_t seen_bits(const RowView& v, int lo, int hi, int at) {
+  uint32_t bits = range_bits(0, v.last >= at + 31 ? 32 : v.last - at + 1);
+  if (v.word) {
+    const int sh = v.first - at;   // column of the first query's position
+    if (sh >= 0) bits |= sh < 32 ? static_cast<uint32_t>(v.word << sh) : 0u;
+    else if (sh > -64) bits |= static_cast<uint32_t>(v.word >> -sh);
+  }
+  return bits & range_bits(lo - at, hi - at);
 }
 
 // Own tiles of every sequence, as running totals in cum[0 .. batch]; the block's threads together.
@@ -411,7 +425,7 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
 }
 
 // Loads key tiles (TILE positions) of a segment: K and V boxes of the pages that hold a key of [lo, hi),
-// one page per lane; the whole warp takes part.  ids holds the page ids of table entries id0 + lane.
+// one box per lane; the whole warp takes part.  ids holds the page ids of table entries id0 + lane.
 template <int HD, int TILE>
 struct PageLoader {
   const CUtensorMap* map;
@@ -440,23 +454,34 @@ struct PageLoader {
       ids = first + lane < id_end ? __ldg(tab + first + lane) : -1;
     }
   }
-  // This lane's page of the tile, n_pages (beyond the tensor: the copy fills zeros) for an id out of
-  // range; returns whether any lane's was.
-  __device__ __forceinline__ bool page_of_lane(int first, int n, int& page) const {
-    page = __shfl_sync(0xffffffffu, ids, (first - id0 + lane) & 31);
-    const bool bad = lane < n && (page < 0 || page >= kv->n_pages);
-    if (bad) page = kv->n_pages;
-    return __any_sync(0xffffffffu, bad);
+  // Whether a page of the tile has an id out of range.
+  __device__ __forceinline__ bool bad_page(int first, int n) const {
+    const int page = __shfl_sync(0xffffffffu, ids, (first - id0 + lane) & 31);
+    return __any_sync(0xffffffffu, lane < n && (page < 0 || page >= kv->n_pages));
   }
-  // dst: [HD/64][TILE rows][128 B]; which: 0 K, 1 V
-  __device__ __forceinline__ void load(uint8_t* dst, uint64_t* bar, int which, int kvh, int key0, int first, int n,
-                                       int page) const {
-    if (lane >= n) return;
-    const int row = first + lane - (key0 >> kv->page_shift);   // page within the tile
-    const int y = key0 & ((1 << kv->page_shift) - 1);          // tile within the page (pages larger than a tile)
-#pragma unroll
-    for (int h = 0; h < HD / 64; ++h)
-      tma_load_4d(dst + h * TILE * 128 + (row << kv->page_shift) * 128, map, bar, h * 64, y, which * kv->KVH + kvh, page);
+  // One box per lane: the tile's pages in use x the 64-dim halves, into dst [HD/64][TILE rows][128 B];
+  // which: 0 K, 1 V.
+  __device__ __forceinline__ void load(uint8_t* dst, uint64_t* bar, int which, int kvh, int key0, int first, int n) const {
+    const int i = lane / (HD / 64), h = lane % (HD / 64);
+    const int page = page_at(first + i);
+    if (i < n) box(dst, bar, which, kvh, key0, first + i, page, h);
+  }
+  // K and V of a tile likewise: lanes of K, then of V.
+  __device__ __forceinline__ void load_kv(uint8_t* k, uint64_t* k_bar, uint8_t* v, uint64_t* v_bar, int kvh, int key0, int first,
+                                          int n) const {
+    const int i = lane / (HD / 32), h = lane % (HD / 64), which = lane / (HD / 64) % 2;
+    const int page = page_at(first + i);
+    if (i < n) box(which ? v : k, which ? v_bar : k_bar, which, kvh, key0, first + i, page, h);
+  }
+  // The page of a table entry at hand, n_pages (beyond the tensor: the copy fills zeros) for a bad id.
+  __device__ __forceinline__ int page_at(int entry) const {
+    const int page = __shfl_sync(0xffffffffu, ids, (entry - id0) & 31);
+    return page < 0 || page >= kv->n_pages ? kv->n_pages : page;
+  }
+  __device__ __forceinline__ void box(uint8_t* dst, uint64_t* bar, int which, int kvh, int key0, int entry, int page, int h) const {
+    const int row = entry - (key0 >> kv->page_shift);    // page within the tile
+    const int y = key0 & ((1 << kv->page_shift) - 1);    // tile within the page (pages larger than a tile)
+    tma_load_4d(dst + h * TILE * 128 + (row << kv->page_shift) * 128, map, bar, h * 64, y, which * kv->KVH + kvh, page);
   }
 };
 
@@ -472,16 +497,15 @@ struct PageLoader {
 // (128-byte swizzle: the ldmatrix reads are free of bank conflicts) and posts each segment's
 // description and query rows ahead of its tiles.
 // ============================================================================================
-struct SegDesc {
-  int32_t rows, mt, lo, hi, key0, cnt;      // key0: first tile's first position
-  int32_t kvh, flags;                       // kSeg* bits
-  int32_t info;                             // index into pre_info / own_info (first part only)
-  int32_t last_cta;                         // CTA of the segment's last tile
+struct alignas(16) SegDesc {
+  int32_t rows, mt, lo, hi;
+  int32_t key0, cnt, kvh, flags;            // key0: first tile's first position; flags: kSeg* bits
+  int32_t info, last_cta, pad0, pad1;       // entry of pre_info / own_info, CTA of the last tile (first part only)
 };
 constexpr int kSegPrefix = 1, kSegStarts = 2, kSegEnds = 4, kSegBad = 8;
-struct RowDesc {
+struct alignas(16) RowDesc {
   int32_t last, first, token, head;
-  uint64_t word;
+  uint64_t word, pad;
 };
 
 template <int HD, int MT>
@@ -566,9 +590,9 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
         ok = false;
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
-        for (int r = lane; r < wk.rows; r += 32) {
-          int t, h;
-          wk.row_of(r, t, h);
+        int t = 0, h = 0;   // a row per lane
+        if (lane < wk.rows) {
+          wk.row_of(lane, t, h);
           SeqRef s = wk.s;
           if (wk.prefix) {
             const int b = token_seq[t];
@@ -576,62 +600,55 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
             else s = SeqRef{0, 0, 0, false, false};
           }
           const RowView v = row_view(a, s, t);
-          RowDesc* d = reinterpret_cast<RowDesc*>(smem + SM::oRow) + row0 + r;
-          d->last = v.last;
-          d->first = v.first;
-          d->token = t;
-          d->head = h;
+          RowDesc* d = reinterpret_cast<RowDesc*>(smem + SM::oRow) + row0 + lane;
+          *reinterpret_cast<int4*>(d) = make_int4(v.last, v.first, t, h);
           d->word = v.word;
         }
         __syncwarp();
         if (lane == 0) {
-          SegDesc* d = reinterpret_cast<SegDesc*>(smem + SM::oSeg) + slot;
+          int4* d = reinterpret_cast<int4*>(smem + SM::oSeg + slot * sizeof(SegDesc));
           const bool starts = tile == 0, ends = tile + cnt == wk.k.nt;
-          d->rows = wk.rows;
-          d->mt = (wk.rows + kRowsUnit - 1) / kRowsUnit;
-          d->lo = wk.k.lo;
-          d->hi = wk.k.hi;
-          d->key0 = (wk.k.t0 + tile) * kRowsTile;
-          d->cnt = cnt;
-          d->kvh = wk.kvh;
-          d->flags = (wk.prefix ? kSegPrefix : 0) | (starts ? kSegStarts : 0) | (ends ? kSegEnds : 0) |
-                     (!wk.prefix && wk.s.bad ? kSegBad : 0);
-          d->info = wk.prefix ? wk.seg : wk.own_info_index();
-          d->last_cta = starts ? sh.owner(g + static_cast<uint32_t>(wk.k.nt) - 1) : 0;
+          d[0] = make_int4(wk.rows, (wk.rows + kRowsUnit - 1) / kRowsUnit, wk.k.lo, wk.k.hi);
+          d[1] = make_int4((wk.k.t0 + tile) * kRowsTile, cnt, wk.kvh,
+                           (wk.prefix ? kSegPrefix : 0) | (starts ? kSegStarts : 0) | (ends ? kSegEnds : 0) |
+                               (!wk.prefix && wk.s.bad ? kSegBad : 0));
+          d[2] = make_int4(wk.prefix ? wk.seg : wk.own_info_index(), starts ? sh.owner(g + static_cast<uint32_t>(wk.k.nt) - 1) : 0, 0, 0);
           mbar_arrive_expect_tx(&seg_full[slot], static_cast<uint32_t>(wk.rows * HD * 2));
         }
         __syncwarp();
-        for (int r = lane; r < wk.rows; r += 32) {
-          int t, h;
-          wk.row_of(r, t, h);
-          bulk_load_1d(smem + SM::oQ + (row0 + r) * SM::kQRow, static_cast<const T*>(a.q) + t * a.q_stride + h * HD, HD * 2,
+        if (lane < wk.rows)
+          bulk_load_1d(smem + SM::oQ + (row0 + lane) * SM::kQRow, static_cast<const T*>(a.q) + t * a.q_stride + h * HD, HD * 2,
                        &seg_full[slot]);
-        }
         ld.start(wk.prefix ? a.prefix_table : a.kv.table + static_cast<int64_t>(wk.b) * a.kv.table_stride, wk.k.hi);
       }
       for (int i = 0; i < cnt && ok; ++i) {
         const int key0 = (wk.k.t0 + tile + i) * kRowsTile;
-        int first = 0, page;
+        int first = 0;
         const int n = ld.boxes(key0, wk.k.lo, wk.k.hi, first);
         ld.prefetch(first, n);
-        const bool bad = ld.page_of_lane(first, n, page);
-        if (bad && lane == 0 && a.status) atomicOr(a.status, DEX_ATTN_BAD_PAGE);
-        const uint32_t tx = static_cast<uint32_t>(n * ld.box_rows() * HD * 2);
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-          if (n_ld >= SM::kStages) ok = ok && pipe_wait(&empty[st], phase ^ 1u);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (lane == 0) {
-            bad_stage[st] = bad;
-            if (n > 0) mbar_arrive_expect_tx(&full[st], tx);
-            else mbar_arrive(&full[st]);
+        const bool bad = ld.bad_page(first, n);
+        const int kst = st;
+        if (n_ld >= SM::kStages) ok = ok && pipe_wait(&empty[kst], phase ^ 1u);
+        if (++st == SM::kStages) st = 0, phase ^= 1u;
+        const int vst = st;
+        if (n_ld + 1 >= SM::kStages) ok = ok && pipe_wait(&empty[vst], phase ^ 1u);
+        if (++st == SM::kStages) st = 0, phase ^= 1u;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane < 2) {
+          const int x = lane ? vst : kst;
+          if (n > 0) {
+            bad_stage[x] = bad;
+            mbar_arrive_expect_tx(&full[x], static_cast<uint32_t>(n * ld.box_rows() * HD * 2));
+          } else {
+            bad_stage[x] = 0;
+            mbar_arrive(&full[x]);
           }
-          __syncwarp();
-          ld.load(smem + st * SM::kBuf, &full[st], which, wk.kvh, key0, first, n, page);
-          ++n_ld;
-          if (++st == SM::kStages) st = 0, phase ^= 1u;
+          if (bad && lane && a.status) atomicOr(a.status, DEX_ATTN_BAD_PAGE);
         }
+        __syncwarp();
+        ld.load_kv(smem + kst * SM::kBuf, &full[kst], smem + vst * SM::kBuf, &full[vst], wk.kvh, key0, first, n);
+        n_ld += 2;
       }
       g += static_cast<uint32_t>(cnt);
       if (g < g1) wk.next();
@@ -730,11 +747,11 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
                 const int r = u * 16 + gr + 8 * h;
                 RowView v{0x7fffffff, 0, 0, false};
                 if (r < d.rows) v.last = rd[r].last, v.first = rd[r].first, v.word = rd[r].word;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const int kk = 2 * tq + (e & 1) + (e >> 1) * 8;
-                  if (kk < in0 || kk >= in1 || !v.sees(key0 + kk)) x[u][h][e] = -INFINITY;
-                }
+                const uint32_t bits = seen_bits(v, d.lo, d.hi, key0) >> (2 * tq);
+                if (!(bits & 1u)) x[u][h][0] = -INFINITY;
+                if (!(bits & 2u)) x[u][h][1] = -INFINITY;
+                if (!(bits & 256u)) x[u][h][2] = -INFINITY;
+                if (!(bits & 512u)) x[u][h][3] = -INFINITY;
               }
               float mx = fmaxf(fmaxf(x[u][h][0], x[u][h][1]), fmaxf(x[u][h][2], x[u][h][3]));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -977,23 +994,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Bits i of columns [32 c, 32 c + 32) of a key tile at key0 that the row sees, within [lo, hi).
-__device__ __forceinline__ uint32_t range_bits(int from, int to) {   // bits from .. to - 1 of a word
-  from = max(from, 0);
-  to = min(to, 32);
-  if (to <= from) return 0u;
-  return (0xffffffffu >> (32 - (to - from))) << from;
-}
-__device__ __forceinline__ uint32_t seen_bits(const RowView& v, int lo, int hi, int at) {
-  uint32_t bits = range_bits(0, v.last >= at + 31 ? 32 : v.last - at + 1);
-  if (v.word) {
-    const int sh = v.first - at;   // column of the first query's position
-    if (sh >= 0) bits |= sh < 32 ? static_cast<uint32_t>(v.word << sh) : 0u;
-    else if (sh > -64) bits |= static_cast<uint32_t>(v.word >> -sh);
-  }
-  return bits & range_bits(lo - at, hi - at);
-}
 
 // Loads of a segment's cnt tiles: K of the first `ahead` tiles, then V of tile j and K of tile
 // j + ahead in turn -- the order in which the MMAs take them.
@@ -1333,7 +1333,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       bool ok = true;
       auto load = [&](PageLoader<HD, kTileKeys>& ld, int which, int j) {
         const int st = static_cast<int>(n_ld % SM::kStages), key0 = (wk.k.t0 + tile + j) * kTileKeys;
-        int first = 0, page;
+        int first = 0;
         const int n = ld.boxes(key0, wk.k.lo, wk.k.hi, first);
         ld.prefetch(first, n);
         if (n_ld >= SM::kStages && !pipe_wait(&empty[st], (n_ld / SM::kStages - 1) & 1u)) ok = false;
@@ -1342,7 +1342,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (lane == 0) timed_out();
           return;
         }
-        const bool bad = ld.page_of_lane(first, n, page);
+        const bool bad = ld.bad_page(first, n);
         if (lane == 0) {
           bad_stage[st] = bad;
           if (bad && a.status) atomicOr(a.status, DEX_ATTN_BAD_PAGE);
@@ -1350,7 +1350,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           else mbar_arrive(&full[st]);
         }
         __syncwarp();
-        ld.load(smem + SM::oRing + st * SM::kBuf, &full[st], which, wk.kvh, key0, first, n, page);
+        ld.load(smem + SM::oRing + st * SM::kBuf, &full[st], which, wk.kvh, key0, first, n);
         ++n_ld;
       };
       for (uint32_t g = g0; g < g1 && ok;) {
