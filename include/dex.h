@@ -356,7 +356,7 @@ int dex_prefix_attention_workspace(const dex_paged_kv* kv, const dex_attention_a
  * (DEX_ECAPACITY otherwise); calls that may overlap on the GPU need workspaces of their own.
  * Constraints: the cache's, n_heads a multiple of n_kv_heads with at most 128 query heads per
  * K/V head, q and out 16-byte aligned, prefix_len within the table, and (n_tokens * (n_heads /
- * n_kv_heads) / 256 + batch + 2) * n_kv_heads * (table_width * page_size / 64 + 2) < 2^31.  Runs on the current device;
+ * n_kv_heads) / 256 + batch + 2) * n_kv_heads * (table_width * page_size / 64 + 6) < 2^31.  Runs on the current device;
  * stream-ordered, no allocation, no sync, capturable: lengths, tables and masks are read
  * on the device, so a captured call can be replayed on new ones. */
 int dex_prefix_attention(const dex_paged_kv* kv, const dex_attention_args* a, void* workspace, size_t workspace_bytes,

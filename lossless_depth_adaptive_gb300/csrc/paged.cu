@@ -261,8 +261,8 @@ static int attention_args(const dex_paged_kv* kv, const dex_attention_args* a, d
   d->H = a->n_heads;
   d->G = a->n_heads / kv->n_kv_heads;
   d->max_q = a->max_q < a->n_tokens ? a->max_q : a->n_tokens > 0 ? a->n_tokens : 1;
-  // key tiles are counted in 32 bits
-  const int64_t tiles = static_cast<int64_t>(kv->table_width) * kv->page_size / 64 + 2;
+  // key tiles, and what segments cost beside them, are counted in 32 bits
+  const int64_t tiles = static_cast<int64_t>(kv->table_width) * kv->page_size / 64 + 6;
   const int64_t segs = (static_cast<int64_t>(a->n_tokens) * d->G / 256 + kv->batch + 2) * kv->n_kv_heads;
   if (tiles * segs >= (int64_t(1) << 31)) return DEX_EINVAL;
   d->prefix_len = a->prefix_len;

@@ -12,8 +12,9 @@
 //    for up to 256 rows;
 //  * own segment: rows of one sequence against its positions from prefix_len on (from 0 when
 //    nothing is shared).
-// Key tiles of all segments are laid end to end and cut into equal contiguous ranges, one per
-// CTA of a persistent grid, so lengths need no plan on the host and any mix of lengths balances.
+// Key tiles of all segments are laid end to end, each segment behind a few units that stand for what it
+// costs beside its tiles, and cut into equal contiguous ranges, one per CTA of a persistent grid, so
+// lengths need no plan on the host and any mix of lengths balances.
 // A segment that lies in one CTA is finished there; one that is cut leaves a partial (m, l, O) per
 // CTA, and combine_kernel joins the parts of each row in a fixed order (no atomics: the same
 // lengths give the same bits).
@@ -47,7 +48,10 @@ constexpr int kRowsPerSm = 2;     // resident CTAs
 constexpr int kSms = 152;         // of the sm_103 part: workspace sizes and grids, whatever device is current
 constexpr int kTileKeys = 128;    // keys of a tile of tile_kernel
 constexpr int kTileRows = 256;    // its query rows (two tiles of 128)
-constexpr int kRowsMinTiles = 2, kTileMinTiles = 2;   // key tiles of a CTA, at least
+// What a segment costs a CTA beside its key tiles, in tiles (queries, start and end of its pipeline, result), and the
+// units (tiles and these) of a CTA, at least.
+constexpr int kRowsSegCost = 1, kTileSegCost = 3;
+constexpr int kRowsMinUnits = 3, kTileMinUnits = 5;
 constexpr int kMaxBatch = 1024;
 
 // Division by a number fixed for the call: n / d for 0 <= n < 2^31 (multiply, add, shift).
@@ -68,7 +72,6 @@ struct SegWork {
   PrefixAttnArgs a;
   FastDiv by_g, by_kvh; // query heads per K/V head, K/V heads
   int32_t first;        // 1: the call's first kernel (it waits for what precedes the call)
-  int32_t min_tiles;    // key tiles of a CTA, at least
   int32_t share;        // 1: positions below prefix_len belong to prefix segments
   int32_t do_prefix;    // this kernel computes the prefix segments
   int32_t do_own;       // this kernel computes the own segments
@@ -164,8 +167,16 @@ __device__ __forceinline__ int own_info_of(const PrefixAttnArgs& a, int RT, int 
   return (static_cast<int>(static_cast<uint32_t>(q0 * a.G) / static_cast<uint32_t>(RT)) + b + rt) * a.kv.KVH + kvh;
 }
 
-// The segment that holds a key tile, and the walk to the next one.
-template <int RT, int TILE>
+// The part of a segment that a CTA's range of units covers.
+struct Piece {
+  int tile, cnt;      // first key tile, number of tiles (none where the range ends before the first)
+  uint32_t units;
+  bool starts, ends;  // it holds the segment's first, last tile
+};
+
+// The segment that holds a unit, and the walk to the next one.  A segment is COST units followed by its
+// key tiles.
+template <int RT, int TILE, int COST>
 struct Walker {
   const SegWork& w;
   int n_pre, pre_nt;       // prefix segments of this kernel and their tiles
@@ -180,15 +191,24 @@ struct Walker {
     n_pre = w.do_prefix ? (pre_rows + RT - 1) / RT * w.a.kv.KVH : 0;
     pre_nt = (w.a.prefix_len + TILE - 1) / TILE;
   }
-  __device__ __forceinline__ uint32_t pre_tiles() const {
-    return static_cast<uint32_t>(n_pre) * static_cast<uint32_t>(pre_nt);
-  }
-  // tiles of one K/V head over the row tiles of sequence b
-  __device__ __forceinline__ uint32_t seq_tiles(const SeqRef& q) const {
+  __device__ __forceinline__ static uint32_t units(int nt) { return nt > 0 ? static_cast<uint32_t>(nt + COST) : 0u; }
+  __device__ __forceinline__ uint32_t pre_units() const { return static_cast<uint32_t>(n_pre) * units(pre_nt); }
+  // units of one K/V head over the row tiles of sequence b
+  __device__ __forceinline__ uint32_t seq_units(const SeqRef& q) const {
     if (!q.valid) return 0;
     uint32_t n = 0;
-    for (int r = 0; r < q.n * w.a.G; r += RT) n += own_range<TILE>(w, q, min(r + RT, q.n * w.a.G)).nt;
+    for (int r = 0; r < q.n * w.a.G; r += RT) n += units(own_range<TILE>(w, q, min(r + RT, q.n * w.a.G)).nt);
     return n;
+  }
+  // The part of the segment from unit `off` on that `left` more units cover.
+  __device__ __forceinline__ Piece piece(int off, uint32_t left) const {
+    Piece p;
+    p.units = min(units(k.nt) - static_cast<uint32_t>(off), left);
+    p.tile = max(off - COST, 0);
+    p.cnt = max(off + static_cast<int>(p.units) - COST, 0) - p.tile;
+    p.starts = p.tile == 0;
+    p.ends = p.tile + p.cnt == k.nt;
+    return p;
   }
   __device__ __forceinline__ void set_prefix(int index) {
     prefix = true;
@@ -205,15 +225,15 @@ struct Walker {
     rows = min(RT, s.n * w.a.G - r0);
     k = own_range<TILE>(w, s, r0 + rows);
   }
-  // Segment of tile g (cum[b]: own tiles of all K/V heads before sequence b); returns the tile within it.
+  // Segment of unit g (cum[b]: own units of all K/V heads before sequence b); returns the unit within it.
   __device__ __forceinline__ int find(uint32_t g, const uint32_t* cum) {
-    if (g < pre_tiles()) {
-      set_prefix(static_cast<int>(g / static_cast<uint32_t>(pre_nt)));
-      return static_cast<int>(g % static_cast<uint32_t>(pre_nt));
+    if (g < pre_units()) {
+      set_prefix(static_cast<int>(g / units(pre_nt)));
+      return static_cast<int>(g % units(pre_nt));
     }
-    g -= pre_tiles();
+    g -= pre_units();
     int lo = 0, hi = w.a.kv.batch - 1;
-    while (lo < hi) {   // last b with cum[b] <= g: a sequence with tiles, since the total is beyond g
+    while (lo < hi) {   // last b with cum[b] <= g: a sequence with units, since the total is beyond g
       const int mid = (lo + hi + 1) >> 1;
       if (cum[mid] <= g) lo = mid;
       else hi = mid - 1;
@@ -223,12 +243,12 @@ struct Walker {
     s = seq_ref(w.a, b);
     for (rt = 0;; ++rt) {
       set_own();
-      const uint32_t cnt = static_cast<uint32_t>(k.nt) * static_cast<uint32_t>(w.a.kv.KVH);
+      const uint32_t cnt = units(k.nt) * static_cast<uint32_t>(w.a.kv.KVH);
       if (g < cnt) break;
       g -= cnt;
     }
-    kvh = static_cast<int>(g / static_cast<uint32_t>(k.nt));
-    return static_cast<int>(g % static_cast<uint32_t>(k.nt));
+    kvh = static_cast<int>(g / units(k.nt));
+    return static_cast<int>(g % units(k.nt));
   }
   // The next segment that has tiles (the caller knows that there is one).
   __device__ __forceinline__ void next() {
@@ -314,11 +334,11 @@ __device__ __forceinline__ uint32_t seen_bits(const RowView& v, int lo, int hi, 
   return bits & range_bits(lo - at, hi - at);
 }
 
-// Own tiles of every sequence, as running totals in cum[0 .. batch]; the block's threads together.
+// Own units of every sequence, as running totals in cum[0 .. batch]; the block's threads together.
 // scratch: a word per warp.  token_seq (at most 64 tokens, or null) receives each token's sequence.
-// Returns the total number of tiles of the kernel.
-template <int RT, int TILE, int THREADS>
-__device__ __forceinline__ uint32_t count_tiles(const Walker<RT, TILE>& wk, uint32_t* cum, uint32_t* scratch,
+// Returns the total number of units of the kernel.
+template <int THREADS, typename W>
+__device__ __forceinline__ uint32_t count_units(const W& wk, uint32_t* cum, uint32_t* scratch,
                                                 int* token_seq = nullptr) {
   const SegWork& w = wk.w;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = w.do_own ? w.a.kv.batch : 0;
@@ -329,7 +349,7 @@ __device__ __forceinline__ uint32_t count_tiles(const Walker<RT, TILE>& wk, uint
     if (b < B) {
       bool report;
       const SeqRef s = seq_ref(w.a, b, &report);
-      n = wk.seq_tiles(s) * static_cast<uint32_t>(w.a.kv.KVH);
+      n = wk.seq_units(s) * static_cast<uint32_t>(w.a.kv.KVH);
       if (token_seq)
         for (int i = 0; i < s.n; ++i) token_seq[s.q0 + i] = b;
       if (report && blockIdx.x == 0 && w.a.status) atomicOr(w.a.status, DEX_ATTN_BAD_RANGE);
@@ -350,20 +370,20 @@ __device__ __forceinline__ uint32_t count_tiles(const Walker<RT, TILE>& wk, uint
     if (b < B) cum[b] = before + x - n;
     __syncthreads();
   }
-  return wk.pre_tiles() + base;
+  return wk.pre_units() + base;
 }
 
-// Shares of `total` tiles over at most `ctas` CTAs: contiguous, equal within one, none below `least`
-// (but for the last few tiles of a small call); CTA c takes [begin(c), begin(c + 1)).
+// Shares of `total` units over at most `grid` CTAs: contiguous, equal within one, none below `least`
+// (but in a call that has no more); CTA c takes [begin(c), begin(c + 1)).
 struct Share {
-  uint32_t ctas, each, more;   // the first `more` CTAs take each + 1 tiles
+  uint32_t ctas, each, more;   // the first `more` CTAs take each + 1 units
   __device__ __forceinline__ Share(uint32_t total, uint32_t grid, uint32_t least) {
     ctas = min(grid, total > least ? total / least : min(total, 1u));
     each = ctas ? total / ctas : 0;
     more = total - each * ctas;
   }
   __device__ __forceinline__ uint32_t begin(uint32_t c) const { return c * each + min(c, more); }
-  __device__ __forceinline__ int owner(uint32_t g) const {   // the CTA that holds tile g
+  __device__ __forceinline__ int owner(uint32_t g) const {   // the CTA that holds unit g
     const uint32_t head = more * (each + 1);
     return static_cast<int>(g < head ? g / (each + 1) : more + (g - head) / each);
   }
@@ -502,7 +522,7 @@ struct alignas(16) SegDesc {
   int32_t key0, cnt, kvh, flags;            // key0: first tile's first position; flags: kSeg* bits
   int32_t info, last_cta, pad0, pad1;       // entry of pre_info / own_info, CTA of the last tile (first part only)
 };
-constexpr int kSegPrefix = 1, kSegStarts = 2, kSegEnds = 4, kSegBad = 8;
+constexpr int kSegPrefix = 1, kSegStarts = 2, kSegEnds = 4, kSegBad = 8, kSegLast = 16;
 struct alignas(16) RowDesc {
   int32_t last, first, token, head;
   uint64_t word, pad;
@@ -525,7 +545,7 @@ struct RowsSmem {
   static constexpr uint32_t oBar = oSeg + kSlots * sizeof(SegDesc);   // full, empty, seg_full, seg_empty
   static constexpr uint32_t oMisc = oBar + (2 * kStages + 2 * kSlots) * 8;   // bad flags, scratch [32], sequence of a token [64]
   static constexpr uint32_t kTotal = oMisc + (kStages + 32 + 64) * 4 + 1024;
-  static_assert(kStages * kBuf >= kMaxBatch * 4, "tile counts use the ring before the first copy");
+  static_assert(kStages * kBuf >= kMaxBatch * 4, "the counts use the ring before the first copy");
   static_assert(kRowsPerSm * (kTotal + 1024) <= 228 * 1024, "resident CTAs");
 };
 
@@ -561,9 +581,9 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
   if (tid < 64) token_seq[tid] = -1;
   __syncthreads();
   if (w.first) griddep_wait();
-  Walker<SM::kRows, kRowsTile> wk(w);
-  const uint32_t total = count_tiles<SM::kRows, kRowsTile, kRowsThreads>(wk, cum, scratch, w.do_prefix ? token_seq : nullptr);
-  const Share sh(total, gridDim.x, w.min_tiles);
+  Walker<SM::kRows, kRowsTile, kRowsSegCost> wk(w);
+  const uint32_t total = count_units<kRowsThreads>(wk, cum, scratch, w.do_prefix ? token_seq : nullptr);
+  const Share sh(total, gridDim.x, kRowsMinUnits);
   const bool work = blockIdx.x < sh.ctas;
   const uint32_t g0 = work ? sh.begin(blockIdx.x) : 0, g1 = work ? sh.begin(blockIdx.x + 1) : 0;
   fence_proxy_async_smem();   // the counts in the ring are written before its first copy
@@ -578,11 +598,12 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
     ld.kv = &a.kv;
     ld.lane = lane;
     uint32_t n_ld = 0, n_seg = 0, phase = 0;
-    int st = 0, tile = work ? wk.find(g0, cum) : 0;
+    int st = 0, off = work ? wk.find(g0, cum) : 0;
     bool ok = true;
     fence_proxy_async_smem();   // the counts in the ring are read before its first copy
     for (uint32_t g = g0; g < g1 && ok; ++n_seg) {
-      const int cnt = min(wk.k.nt - tile, static_cast<int>(g1 - g));
+      const Piece pc = wk.piece(off, g1 - g);
+      if (pc.cnt == 0) break;   // only at the end of the range
       // the segment's description, row table and query rows
       const int slot = static_cast<int>(n_seg % n_slots), row0 = slot * (SM::kQRows / n_slots);
       if (n_seg >= static_cast<uint32_t>(n_slots) &&
@@ -607,12 +628,12 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
         __syncwarp();
         if (lane == 0) {
           int4* d = reinterpret_cast<int4*>(smem + SM::oSeg + slot * sizeof(SegDesc));
-          const bool starts = tile == 0, ends = tile + cnt == wk.k.nt;
           d[0] = make_int4(wk.rows, (wk.rows + kRowsUnit - 1) / kRowsUnit, wk.k.lo, wk.k.hi);
-          d[1] = make_int4((wk.k.t0 + tile) * kRowsTile, cnt, wk.kvh,
-                           (wk.prefix ? kSegPrefix : 0) | (starts ? kSegStarts : 0) | (ends ? kSegEnds : 0) |
-                               (!wk.prefix && wk.s.bad ? kSegBad : 0));
-          d[2] = make_int4(wk.prefix ? wk.seg : wk.own_info_index(), starts ? sh.owner(g + static_cast<uint32_t>(wk.k.nt) - 1) : 0, 0, 0);
+          d[1] = make_int4((wk.k.t0 + pc.tile) * kRowsTile, pc.cnt, wk.kvh,
+                           (wk.prefix ? kSegPrefix : 0) | (pc.starts ? kSegStarts : 0) | (pc.ends ? kSegEnds : 0) |
+                               (!wk.prefix && wk.s.bad ? kSegBad : 0) | (g1 - g - pc.units <= kRowsSegCost ? kSegLast : 0));
+          d[2] = make_int4(wk.prefix ? wk.seg : wk.own_info_index(),
+                           pc.starts ? sh.owner(g - static_cast<uint32_t>(off) + wk.units(wk.k.nt) - 1) : 0, 0, 0);
           mbar_arrive_expect_tx(&seg_full[slot], static_cast<uint32_t>(wk.rows * HD * 2));
         }
         __syncwarp();
@@ -621,8 +642,8 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
                        &seg_full[slot]);
         ld.start(wk.prefix ? a.prefix_table : a.kv.table + static_cast<int64_t>(wk.b) * a.kv.table_stride, wk.k.hi);
       }
-      for (int i = 0; i < cnt && ok; ++i) {
-        const int key0 = (wk.k.t0 + tile + i) * kRowsTile;
+      for (int i = 0; i < pc.cnt && ok; ++i) {
+        const int key0 = (wk.k.t0 + pc.tile + i) * kRowsTile;
         int first = 0;
         const int n = ld.boxes(key0, wk.k.lo, wk.k.hi, first);
         ld.prefetch(first, n);
@@ -650,9 +671,9 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
         ld.load_kv(smem + kst * SM::kBuf, &full[kst], smem + vst * SM::kBuf, &full[vst], wk.kvh, key0, first, n);
         n_ld += 2;
       }
-      g += static_cast<uint32_t>(cnt);
+      g += pc.units;
       if (g < g1) wk.next();
-      tile = 0;
+      off = 0;
     }
     if (!ok) {   // let the copies in flight land before the CTA goes
       if (lane == 0 && a.status) atomicOr(a.status, DEX_ATTN_TIMEOUT);
@@ -678,7 +699,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
         ok = false;
       }
     };
-    for (uint32_t g = g0; g < g1; ++n_seg) {
+    for (bool more = work; more; ++n_seg) {
       const int slot = static_cast<int>(n_seg % n_slots), row0 = slot * (SM::kQRows / n_slots);
       wait(&seg_full[slot], n_seg / n_slots);
       if (!named_bar_and(1, kRowsWarps * 32, ok)) break;   // all four warps or none: they meet at barriers
@@ -877,7 +898,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
         }
       }
       if (starts && tid == 0) (prefix ? w.pre_info : w.own_info)[d.info] = make_int2(blockIdx.x, d.last_cta);
-      g += static_cast<uint32_t>(d.cnt);
+      more = !(d.flags & kSegLast);
       __syncwarp();
       if (lane == 0) mbar_arrive(&seg_empty[slot]);
     }
@@ -912,7 +933,7 @@ struct TileSmem {
   static constexpr uint32_t kBars = 2 * kStages + 9;
   static constexpr uint32_t oMisc = oBar + kBars * 8;                // bad flags [stages], scratch [12], TMEM address, segment flag
   static constexpr uint32_t kTotal = oMisc + (kStages + 15) * 4 + 1024;
-  static_assert(kStages * kBuf >= kMaxBatch * 4, "tile counts use the ring before the first copy");
+  static_assert(kStages * kBuf >= kMaxBatch * 4, "the counts use the ring before the first copy");
 };
 static_assert(TileSmem<128>::kTotal <= 227 * 1024, "tile_kernel shared memory");
 
@@ -1047,12 +1068,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tmem_relinquish();
   }
   if (w.first) griddep_wait();
-  Walker<kTileRows, kTileKeys> wk(w);
-  const uint32_t total = count_tiles<kTileRows, kTileKeys, kTileThreads>(wk, cum, scratch);
-  const Share sh(total, gridDim.x, w.min_tiles);
+  Walker<kTileRows, kTileKeys, kTileSegCost> wk(w);
+  const uint32_t total = count_units<kTileThreads>(wk, cum, scratch);
+  const Share sh(total, gridDim.x, kTileMinUnits);
   const bool work = blockIdx.x < sh.ctas;
   const uint32_t g0 = work ? sh.begin(blockIdx.x) : 0, g1 = work ? sh.begin(blockIdx.x + 1) : 0;
-  int tile = work ? wk.find(g0, cum) : 0;
+  int off = work ? wk.find(g0, cum) : 0;
   fence_proxy_async_smem();   // the counts in the ring are read before its first copy
   tc_fence_before();
   __syncthreads();
@@ -1080,7 +1101,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     };
     bool ok = true;
     for (uint32_t g = g0; g < g1;) {
-      const int cnt = min(wk.k.nt - tile, static_cast<int>(g1 - g));
+      const Piece pc = wk.piece(off, g1 - g);
+      const int tile = pc.tile, cnt = pc.cnt;
+      if (cnt == 0) break;   // only at the end of the range
       const bool alt = wk.rows <= 128;   // the teams share the rows and take alternate key tiles
       const int ahead = alt ? 2 : 1;
       const int r = alt ? r128 : team * 128 + r128;
@@ -1266,7 +1289,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           l = l * f0 + other.y * f1;
           m = M;
         }
-        const bool starts = tile == 0, ends = tile + cnt == wk.k.nt;
+        const bool starts = pc.starts, ends = pc.ends;
         const bool direct = starts && ends && !w.joined;
         const int t = t_row, h = h_row;
         const int64_t row = static_cast<int64_t>(t) * a.H + h;
@@ -1311,16 +1334,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         if (starts && tid == 0) {
           int2* info = wk.prefix ? w.pre_info + wk.seg : w.own_info + wk.own_info_index();
-          *info = make_int2(blockIdx.x, sh.owner(g + static_cast<uint32_t>(wk.k.nt) - 1));
+          *info = make_int2(blockIdx.x, sh.owner(g - static_cast<uint32_t>(off) + wk.units(wk.k.nt) - 1));
         }
       }
       if (alt) named_bar_sync(2, 256);   // the query tiles may be written again
       tc_fence_before();                 // O is read before the next segment's p_full
       ++n_seg;
       base += 2u * static_cast<uint32_t>(cnt);
-      g += static_cast<uint32_t>(cnt);
+      g += pc.units;
       if (g < g1) wk.next();
-      tile = 0;
+      off = 0;
     }
   } else {
     if (warp == 8) {
@@ -1331,8 +1354,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       lk.lane = lv.lane = lane;
       uint32_t n_ld = 0;
       bool ok = true;
-      auto load = [&](PageLoader<HD, kTileKeys>& ld, int which, int j) {
-        const int st = static_cast<int>(n_ld % SM::kStages), key0 = (wk.k.t0 + tile + j) * kTileKeys;
+      auto load = [&](PageLoader<HD, kTileKeys>& ld, int which, int j) {   // j: tile of the segment
+        const int st = static_cast<int>(n_ld % SM::kStages), key0 = (wk.k.t0 + j) * kTileKeys;
         int first = 0;
         const int n = ld.boxes(key0, wk.k.lo, wk.k.hi, first);
         ld.prefetch(first, n);
@@ -1354,19 +1377,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         ++n_ld;
       };
       for (uint32_t g = g0; g < g1 && ok;) {
-        const int cnt = min(wk.k.nt - tile, static_cast<int>(g1 - g));
+        const Piece pc = wk.piece(off, g1 - g);
+        const int tile = pc.tile, cnt = pc.cnt;
         const int ahead = wk.rows <= 128 ? 2 : 1;
         const int32_t* tab = wk.prefix ? a.prefix_table : a.kv.table + static_cast<int64_t>(wk.b) * a.kv.table_stride;
         lk.start(tab, wk.k.hi);
         lv.start(tab, wk.k.hi);
-        for (int j = 0; j < min(ahead, cnt) && ok; ++j) load(lk, 0, j);
+        for (int j = 0; j < min(ahead, cnt) && ok; ++j) load(lk, 0, tile + j);
         for (int j = 0; j < cnt && ok; ++j) {
-          load(lv, 1, j);
-          if (ok && j + ahead < cnt) load(lk, 0, j + ahead);
+          load(lv, 1, tile + j);
+          if (ok && j + ahead < cnt) load(lk, 0, tile + j + ahead);
         }
-        g += static_cast<uint32_t>(cnt);
+        g += pc.units;
         if (g < g1) wk.next();
-        tile = 0;
+        off = 0;
       }
       if (!ok) {   // let the copies in flight land before the CTA goes
         for (uint32_t i = n_ld > SM::kStages ? n_ld - SM::kStages : 0; i < n_ld; ++i)
@@ -1421,7 +1445,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           umma_ts(t_o, t_s + ks * 8, b0 + ks * 128, id_pv, ks > 0 || !first);
       };
       for (uint32_t g = g0; g < g1 && ok; ++n_seg) {
-        const int cnt = min(wk.k.nt - tile, static_cast<int>(g1 - g));
+        const Piece pc = wk.piece(off, g1 - g);
+        const int cnt = pc.cnt;
+        if (cnt == 0) break;
         const bool alt = wk.rows <= 128;
         const int ahead = alt ? 2 : 1;
         const uint32_t q = alt ? 0 : static_cast<uint32_t>(team) * (SM::kBuf >> 4);
@@ -1461,9 +1487,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         seg_bad[team] = bad || !ok;   // the teams read it after o_full
         umma_commit(o_full);
         mbar_arrive(o_full);
-        g += static_cast<uint32_t>(cnt);
+        g += pc.units;
         if (g < g1) wk.next();
-        tile = 0;
+        off = 0;
       }
     }
   }
@@ -1477,43 +1503,56 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 }
 
 // ============================================================================================
-// Joins the parts of the rows that have several.  A block takes 32 rows of one K/V head, a lane per row;
-// each of HD / 16 warps sums 16 head dims over the parts, with the running maximum of the softmax.  In a
-// call of few rows SPLIT such groups of warps take the parts in turn and join in shared memory: the sum
-// over 38 parts of one 128k-token sequence is a chain of loads otherwise (21 us alone, @@ with four).
-// Parts lie as [head_dim / 4][rows][4], so the 32 rows of four head dims are 512 contiguous bytes.
+// Joins the parts of the rows that have several.  A block takes 2^row_bits <= 32 rows of one K/V head and
+// DIMS of their head dims; each of DIMS / 16 warps sums 16 of them over the parts, with the running
+// maximum of the softmax.  Lanes beyond the rows, and in a call of few rows SPLIT groups of warps, take the
+// parts in turn and join by shuffles and through shared memory: one after the other, the 38 parts of
+// a 128k-token sequence are a chain of loads.  Parts lie as [head_dim / 4][rows][4], so 32 rows of
+// four head dims are 512 contiguous bytes.
 // ============================================================================================
 struct CombineWork {
   SegWork own, pre;        // the kernels that computed own and prefix segments
   int32_t own_rt, pre_rt;  // their rows per segment
   int32_t own_tile;        // their keys per tile (own segments)
   int32_t share;
+  int32_t row_bits;
 };
-constexpr int kCombineRows = 32;
 
-template <typename T, int HD, int SPLIT>
-__global__ void __launch_bounds__(HD * 2 * SPLIT) combine_kernel(const __grid_constant__ CombineWork w) {
-  constexpr int kThreads = HD * 2 * SPLIT;
-  __shared__ int row_seq[kCombineRows];
-  __shared__ float join[SPLIT > 1 ? SPLIT / 2 : 1][SPLIT > 1 ? 18 : 1][HD * 2];
+// (M, L, O) of a row over some parts, joined with that over others.
+__device__ __forceinline__ void join_parts(float& M, float& L, float4 (&o)[4], float m2, float l2, const float4 (&o2)[4]) {
+  const float M1 = fmaxf(M, m2), base = M1 > -INFINITY ? M1 : 0.0f;
+  const float f = ex2(M - base), g = ex2(m2 - base);
+  M = M1;
+  L = L * f + l2 * g;   // a poisoned part is NaN whatever its weight
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    o[q] = make_float4(o[q].x * f + o2[q].x * g, o[q].y * f + o2[q].y * g, o[q].z * f + o2[q].z * g, o[q].w * f + o2[q].w * g);
+}
+
+template <typename T, int HD, int DIMS, int SPLIT>
+__global__ void __launch_bounds__(DIMS * 2 * SPLIT) combine_kernel(const __grid_constant__ CombineWork w) {
+  constexpr int kThreads = DIMS * 2 * SPLIT;
+  __shared__ int row_seq[32];
+  __shared__ float join[SPLIT > 1 ? SPLIT / 2 : 1][SPLIT > 1 ? 18 : 1][DIMS * 2];
   const PrefixAttnArgs& a = w.own.a;
-  const int tid = threadIdx.x, group = tid / (HD * 2), warp = (tid >> 5) % (HD / 16), lane = tid & 31, kvh = blockIdx.y;
-  const int rows_all = a.n_tokens * a.G, rg = blockIdx.x * kCombineRows + lane;   // row: token * G + head within the K/V head
+  const int tid = threadIdx.x, group = tid / (DIMS * 2), warp = blockIdx.z * (DIMS / 16) + (tid >> 5) % (DIMS / 16), lane = tid & 31, kvh = blockIdx.y;
+  const int n_rows = 1 << w.row_bits, li = lane & (n_rows - 1), slot = lane >> w.row_bits, n_slots = 32 >> w.row_bits;
+  const int rows_all = a.n_tokens * a.G, rg0 = blockIdx.x << w.row_bits;
+  const int rg = rg0 + li;   // row: token * G + head within the K/V head
   const int t = w.own.by_g.div(rg);
-  if (tid < kCombineRows) row_seq[tid] = -1;
+  if (tid < 32) row_seq[tid] = -1;
   __syncthreads();
   {
-    const int t0 = __shfl_sync(0xffffffffu, t, 0), t1 = __shfl_sync(0xffffffffu, t, 31);
+    const int t0 = w.own.by_g.div(rg0), t1 = w.own.by_g.div(rg0 + n_rows - 1);
     for (int b = tid; b < a.kv.batch; b += kThreads) {
       const SeqRef s = seq_ref(a, b);
       if (!s.valid) continue;
       const int first = max(s.q0, t0), last = min(s.q0 + s.n - 1, t1);   // tokens of the block, then rows
-      for (int r = max(first * a.G, rg - lane); first <= last && r < min((last + 1) * a.G, rg - lane + kCombineRows); ++r)
-        row_seq[r - (rg - lane)] = b;
+      for (int r = max(first * a.G, rg0); first <= last && r < min((last + 1) * a.G, rg0 + n_rows); ++r) row_seq[r - rg0] = b;
     }
   }
   __syncthreads();
-  const int b = row_seq[lane];
+  const int b = row_seq[li];
   const SeqRef s = seq_ref(a, max(b, 0));
   const int r = rg - s.q0 * a.G, rt = b >= 0 ? r / w.own_rt : 0, r1 = min((rt + 1) * w.own_rt, s.n * a.G);
   griddep_wait();
@@ -1540,12 +1579,13 @@ __global__ void __launch_bounds__(HD * 2 * SPLIT) combine_kernel(const __grid_co
 #pragma unroll
   for (int q = 0; q < 4; ++q) o[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   constexpr int kUnroll = 2;
-  for (int k0 = group * kUnroll; k0 < n; k0 += kUnroll * SPLIT) {
+  const int step = n_slots * SPLIT;   // parts taken at once
+  for (int k0 = slot * SPLIT + group; k0 < n; k0 += kUnroll * step) {
     float2 ml[kUnroll];
     float4 x[kUnroll][4];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int k = k0 + u;
+      const int k = k0 + u * step;
       ml[u] = make_float2(-INFINITY, 0.0f);
       if (k < n) {
         const bool pre = k < n_pre;
@@ -1564,26 +1604,23 @@ __global__ void __launch_bounds__(HD * 2 * SPLIT) combine_kernel(const __grid_co
       }
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const float M1 = fmaxf(M, ml[u].x), base = M1 > -INFINITY ? M1 : 0.0f;
-      const float f = ex2(M - base), g = ex2(ml[u].x - base);
-      M = M1;
-      L = L * f + ml[u].y * g;   // a poisoned part is NaN whatever its weight
+    for (int u = 0; u < kUnroll; ++u) join_parts(M, L, o, ml[u].x, ml[u].y, x[u]);
+  }
+  for (int other = n_rows; other < 32; other <<= 1) {   // lanes that took other parts of the row
+    float4 o2[4];
+    const float m2 = __shfl_xor_sync(0xffffffffu, M, other), l2 = __shfl_xor_sync(0xffffffffu, L, other);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        o[q].x = o[q].x * f + x[u][q].x * g;
-        o[q].y = o[q].y * f + x[u][q].y * g;
-        o[q].z = o[q].z * f + x[u][q].z * g;
-        o[q].w = o[q].w * f + x[u][q].w * g;
-      }
-    }
+    for (int q = 0; q < 4; ++q)
+      o2[q] = make_float4(__shfl_xor_sync(0xffffffffu, o[q].x, other), __shfl_xor_sync(0xffffffffu, o[q].y, other),
+                          __shfl_xor_sync(0xffffffffu, o[q].z, other), __shfl_xor_sync(0xffffffffu, o[q].w, other));
+    join_parts(M, L, o, m2, l2, o2);
   }
   if constexpr (SPLIT > 1) {
 #pragma unroll
     for (int half = SPLIT / 2; half > 0; half >>= 1) {   // groups half .. 2 half - 1 join groups 0 .. half - 1
-      const int x = tid % (HD * 2);
+      const int x = tid % (DIMS * 2);
       if (group >= half && group < 2 * half) {
-        float(*dst)[HD * 2] = join[group - half];
+        float(*dst)[DIMS * 2] = join[group - half];
         dst[0][x] = M;
         dst[1][x] = L;
 #pragma unroll
@@ -1596,24 +1633,17 @@ __global__ void __launch_bounds__(HD * 2 * SPLIT) combine_kernel(const __grid_co
       }
       __syncthreads();
       if (group < half) {
-        const float(*src)[HD * 2] = join[group];
-        const float M1 = fmaxf(M, src[0][x]), base = M1 > -INFINITY ? M1 : 0.0f;
-        const float f = ex2(M - base), g = ex2(src[0][x] - base);
-        M = M1;
-        L = L * f + src[1][x] * g;
+        const float(*src)[DIMS * 2] = join[group];
+        float4 o2[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          o[q].x = o[q].x * f + src[2 + 4 * q][x] * g;
-          o[q].y = o[q].y * f + src[3 + 4 * q][x] * g;
-          o[q].z = o[q].z * f + src[4 + 4 * q][x] * g;
-          o[q].w = o[q].w * f + src[5 + 4 * q][x] * g;
-        }
+        for (int q = 0; q < 4; ++q) o2[q] = make_float4(src[2 + 4 * q][x], src[3 + 4 * q][x], src[4 + 4 * q][x], src[5 + 4 * q][x]);
+        join_parts(M, L, o, src[0][x], src[1][x], o2);
       }
       __syncthreads();
     }
     if (group > 0) return;
   }
-  if (n <= 0) return;
+  if (n <= 0 || slot > 0) return;
   const float inv = isnan(L) ? L : L > 0.0f ? 1.0f / L : 0.0f;
   const int h = kvh * a.G + rg - t * a.G;
   uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + t * a.out_stride + h * HD + warp * 16);
@@ -1743,8 +1773,6 @@ cudaError_t launch_hd(const PrefixAttnArgs& a, const Plan& p, uint8_t* ws, cudaS
   tile.do_prefix = p.prefix_tile;
   tile.first = 1;
   rows.first = !(tile.do_own || tile.do_prefix);
-  rows.min_tiles = kRowsMinTiles;
-  tile.min_tiles = kTileMinTiles;
   const int page = 1 << a.kv.page_shift;
   const int sms = n_sm < kSms ? n_sm : kSms;
   cudaError_t e = cudaSuccess;
@@ -1775,11 +1803,14 @@ cudaError_t launch_hd(const PrefixAttnArgs& a, const Plan& p, uint8_t* ws, cudaS
     c.pre_rt = p.pre_rt();
     c.own_tile = p.own_tile ? kTileKeys : kRowsTile;
     c.share = p.share;
-    const unsigned groups = static_cast<unsigned>((a.n_tokens * a.G + kCombineRows - 1) / kCombineRows);
+    while (c.row_bits < 5 && (1 << c.row_bits) < a.n_tokens * a.G) ++c.row_bits;
+    const unsigned groups = static_cast<unsigned>((a.n_tokens * a.G + (1 << c.row_bits) - 1) >> c.row_bits);
     const dim3 grid(groups, static_cast<unsigned>(a.kv.KVH));
-    // four groups of warps per row while the blocks leave SMs idle
-    e = groups * a.kv.KVH < static_cast<unsigned>(sms) ? launch(combine_kernel<T, HD, 4>, grid, HD * 8, 0, st, true, c)
-                                                       : launch(combine_kernel<T, HD, 1>, grid, HD * 2, 0, st, true, c);
+    // eight groups of warps per row and the head dims over several blocks while the blocks leave SMs idle
+    if (groups * a.kv.KVH < static_cast<unsigned>(sms))
+      e = launch(combine_kernel<T, HD, 32, 8>, dim3(groups, static_cast<unsigned>(a.kv.KVH), HD / 32), 512, 0, st, true, c);
+    else
+      e = launch(combine_kernel<T, HD, HD, 1>, grid, HD * 2, 0, st, true, c);
   }
   return e;
 }
