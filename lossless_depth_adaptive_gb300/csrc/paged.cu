@@ -10,7 +10,7 @@ namespace dex {
 
 namespace {
 
-constexpr int kAppendWarps = 8;   // of a block
+constexpr int kAppendWarps = 4;   // of a block
 
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
@@ -29,7 +29,7 @@ __device__ __forceinline__ Vec8<T> load8(const T* p) {
   const uint4* s = reinterpret_cast<const uint4*>(p);
   uint4* d = reinterpret_cast<uint4*>(&r);
 #pragma unroll
-  for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i) d[i] = __ldcs(s + i);
+  for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i) d[i] = __ldg(s + i);
   return r;
 }
 
@@ -37,9 +37,11 @@ __device__ __forceinline__ Vec8<T> load8(const T* p) {
 
 // A warp takes one token, or `rows` of its head rows when there are few tokens.  An item is eight pairs
 // (x_j, x_{j + HD/2}), j = 8c .. 8c+7, of one head row of q, k or v: two 16-byte loads and two
-// 16-byte stores of a 16-bit type.  A lane keeps its c, hence its eight (cos, sin), and walks the rows
-// with kUnroll items in flight; the first ones are loaded before the token's table entry is known.
-// Warps share nothing, so there is no block barrier.  Bound by memory: @@
+// 16-byte stores of a 16-bit type.  A lane keeps its c, hence its eight (cos, sin), and walks the rows;
+// the first are loaded before the token's table entry is known.  Warps share nothing, so there is no
+// block barrier.  Bound by memory: 13498 tokens of 32 + 2 x 8 heads x 128 (332 MB) take 57 us, 5.8 TB/s.
+// That takes warps more than loads per warp: 32 of 64 registers per SM with one item each 58 us, with two
+// 66 us; 24 warps with two to four items 80 us, 40 warps (48 registers, spills) 70 us.
 //
 // Angle: the turn of pair j at position r is r * theta^(-2j/HD) / 2 pi.  With the turn of position
 // 1 as a 64-bit fixed-point fraction, r times it modulo 2^64 is the fraction of a turn left after
@@ -47,9 +49,8 @@ __device__ __forceinline__ Vec8<T> load8(const T* p) {
 // r = 10^6).  Its upper 32 bits as a signed number are half-turns in units of 2^-31.  theta^(-2j/HD)
 // is the product of the powers theta^(-2 2^b / HD) over the bits b of j, each a 64-bit fraction.
 template <typename CT, typename IT, int HD>
-__global__ void __launch_bounds__(32 * kAppendWarps) paged_append_kernel(const __grid_constant__ AppendArgs a, int rows) {
+__global__ void __launch_bounds__(32 * kAppendWarps, 8) paged_append_kernel(const __grid_constant__ AppendArgs a, int rows) {
   constexpr int kItems = HD / 16, kStep = 32 / kItems;   // items per head row, rows of one pass of the warp
-  constexpr int kUnroll = sizeof(IT) == 2 ? 4 : 2;
   __shared__ __align__(16) float2 cs[kAppendWarps][HD / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % kItems;
   const int t = blockIdx.x * kAppendWarps + warp;
@@ -61,20 +62,14 @@ __global__ void __launch_bounds__(32 * kAppendWarps) paged_append_kernel(const _
   const IT* k = static_cast<const IT*>(a.k) + t * a.k_stride + 8 * c;
   const IT* v = static_cast<const IT*>(a.v) + t * a.v_stride + 8 * c;
 
-  Vec8<IT> lo[kUnroll], hi[kUnroll];
-  auto load_items = [&](int row0) {
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int row = row0 + u * kStep;
-      if (row < end) {
-        const IT* src = row < a.H ? q + row * HD : row < v_row0 ? k + (row - a.H) * HD : v + (row - v_row0) * HD;
-        lo[u] = load8(src);
-        hi[u] = load8(src + HD / 2);
-      }
-    }
+  Vec8<IT> lo, hi;
+  auto load_item = [&](int row) {
+    const IT* src = row < a.H ? q + row * HD : row < v_row0 ? k + (row - a.H) * HD : v + (row - v_row0) * HD;
+    lo = load8(src);
+    hi = load8(src + HD / 2);
   };
   const int first = blockIdx.y * rows + lane / kItems;
-  load_items(first);
+  if (first < end) load_item(first);
 
   const int seq = __ldg(a.seq + t), pos = __ldg(a.pos + t), pidx = pos >> a.kv.page_shift;
   bool ok = seq >= 0 && seq < a.kv.batch && pos >= 0 && pidx < a.kv.table_width;
@@ -108,45 +103,42 @@ __global__ void __launch_bounds__(32 * kAppendWarps) paged_append_kernel(const _
   const int page_size = 1 << a.kv.page_shift, head_stride = page_size * HD;
   CT* q_out = static_cast<CT*>(a.q_out) + t * a.q_out_stride + 8 * c;
   CT* kv_out = static_cast<CT*>(a.kv.pages) + page * a.kv.page_stride + (pos & (page_size - 1)) * HD + 8 * c;
-  for (int row0 = first; row0 < end; row0 += kUnroll * kStep) {
-    if (row0 != first) load_items(row0);
+  for (int row = first; row < end; row += kStep) {
+    if (row != first) load_item(row);
+    Vec8<CT> x, y;
+    if (a.rotate && row < v_row0) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int row = row0 + u * kStep;
-      if (row >= end) continue;
-      Vec8<CT> x, y;
-      if (a.rotate && row < v_row0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float p0 = to_f32(lo[u].v[2 * i]), r0 = to_f32(hi[u].v[2 * i]);
-          const float p1 = to_f32(lo[u].v[2 * i + 1]), r1 = to_f32(hi[u].v[2 * i + 1]);
-          from_f32(x.v[2 * i], p0 * w[i].x - r0 * w[i].y);
-          from_f32(y.v[2 * i], r0 * w[i].x + p0 * w[i].y);
-          from_f32(x.v[2 * i + 1], p1 * w[i].z - r1 * w[i].w);
-          from_f32(y.v[2 * i + 1], r1 * w[i].z + p1 * w[i].w);
-        }
-      } else if constexpr (sizeof(IT) == 2) {
-        x = *reinterpret_cast<const Vec8<CT>*>(&lo[u]);
-        y = *reinterpret_cast<const Vec8<CT>*>(&hi[u]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          from_f32(x.v[i], to_f32(lo[u].v[i]));
-          from_f32(y.v[i], to_f32(hi[u].v[i]));
-        }
+      for (int i = 0; i < 4; ++i) {
+        const float p0 = to_f32(lo.v[2 * i]), r0 = to_f32(hi.v[2 * i]);
+        const float p1 = to_f32(lo.v[2 * i + 1]), r1 = to_f32(hi.v[2 * i + 1]);
+        from_f32(x.v[2 * i], p0 * w[i].x - r0 * w[i].y);
+        from_f32(y.v[2 * i], r0 * w[i].x + p0 * w[i].y);
+        from_f32(x.v[2 * i + 1], p1 * w[i].z - r1 * w[i].w);
+        from_f32(y.v[2 * i + 1], r1 * w[i].z + p1 * w[i].w);
       }
-      // the V heads of a page follow its K heads
-      CT* dst = row < a.H ? q_out + row * HD : kv_out + static_cast<int64_t>(row - a.H) * head_stride;
-      *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(&x);
-      *reinterpret_cast<uint4*>(dst + HD / 2) = *reinterpret_cast<const uint4*>(&y);
+    } else if constexpr (sizeof(IT) == 2) {
+      x = *reinterpret_cast<const Vec8<CT>*>(&lo);
+      y = *reinterpret_cast<const Vec8<CT>*>(&hi);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        from_f32(x.v[i], to_f32(lo.v[i]));
+        from_f32(y.v[i], to_f32(hi.v[i]));
+      }
     }
+    // the V heads of a page follow its K heads
+    CT* dst = row < a.H ? q_out + row * HD : kv_out + static_cast<int64_t>(row - a.H) * head_stride;
+    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(&x);
+    *reinterpret_cast<uint4*>(dst + HD / 2) = *reinterpret_cast<const uint4*>(&y);
   }
 }
 
 template <typename CT, typename IT, int HD>
 static cudaError_t launch_append(const AppendArgs& a, cudaStream_t st) {
-  // a warp per token once that fills the GPU with 16 warps per SM, 16 rows per warp below: @@
-  const int n_rows = a.H + 2 * a.kv.KVH, rows = a.n_tokens >= 16 * 152 ? n_rows : 16;
+  // A warp per token once that gives every SM 16 warps (13498 tokens: 57 us, with 24 rows per warp, which
+  // computes the angles twice, 60 us); eight rows per warp below, where latency counts (eight tokens of 48
+  // rows: 3.0 us, with 16 rows 3.7 us).
+  const int n_rows = a.H + 2 * a.kv.KVH, rows = a.n_tokens >= 16 * 152 ? n_rows : 8;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((a.n_tokens + kAppendWarps - 1) / kAppendWarps),
                      static_cast<unsigned>((n_rows + rows - 1) / rows));

@@ -1667,15 +1667,18 @@ struct Plan {
   int pre_rt() const { return prefix_tile ? kTileRows : rows_mt * kRowsUnit; }
 };
 
-// Which kernel computes what.  Segments of at most 32 rows go to rows_kernel.  The prefix is
+// Which kernel computes what.  Segments of at most 32 rows go to rows_kernel, unless tile_kernel runs
+// for the prefix and there are few of them: a launch less (13 sequences of 4 K/V heads behind 777 positions
+// 20.4 -> 17.9 us).  With 16 rows as the limit, 8 x 8 segments of 32 prefix rows take 23.4 us instead of 14.9,
+// 32 of 32 rows 48.9 instead of 41.8.  The prefix is
 // shared when more than one sequence can have queries (n_tokens > max_q) and it fills a key tile; a
 // sequence whose own rows fill a 128-row tile gains nothing from sharing.
 Plan make_plan(const PrefixAttnArgs& a) {
   Plan p = {};
   const int64_t own_rows = static_cast<int64_t>(a.max_q) * a.G, all_rows = static_cast<int64_t>(a.n_tokens) * a.G;
-  p.own_tile = own_rows > kRowsMax;
   p.share = a.prefix_len >= kRowsTile && a.n_tokens > a.max_q && own_rows < 128;
   p.prefix_tile = p.share && all_rows > kRowsMax;
+  p.own_tile = own_rows > kRowsMax || (p.prefix_tile && a.kv.batch * a.kv.KVH <= kSms / 2);
   const int64_t most = p.share && !p.prefix_tile ? all_rows : p.own_tile ? 0 : own_rows;   // rows of a rows_kernel segment
   p.rows_mt = most == 0 ? 0 : most <= kRowsUnit ? 1 : kRowsMax / kRowsUnit;
   p.slots = most == 0 ? 1 : static_cast<int>(kRowsSlotRows / ((most + kRowsUnit - 1) / kRowsUnit * kRowsUnit));
@@ -1806,11 +1809,12 @@ cudaError_t launch_hd(const PrefixAttnArgs& a, const Plan& p, uint8_t* ws, cudaS
     while (c.row_bits < 5 && (1 << c.row_bits) < a.n_tokens * a.G) ++c.row_bits;
     const unsigned groups = static_cast<unsigned>((a.n_tokens * a.G + (1 << c.row_bits) - 1) >> c.row_bits);
     const dim3 grid(groups, static_cast<unsigned>(a.kv.KVH));
-    // eight groups of warps per row and the head dims over several blocks while the blocks leave SMs idle
-    if (groups * a.kv.KVH < static_cast<unsigned>(sms))
-      e = launch(combine_kernel<T, HD, 32, 8>, dim3(groups, static_cast<unsigned>(a.kv.KVH), HD / 32), 512, 0, st, true, c);
-    else
-      e = launch(combine_kernel<T, HD, HD, 1>, grid, HD * 2, 0, st, true, c);
+    // the fewer blocks there are, the more warps share a row's parts and head dims
+    const unsigned blocks = groups * static_cast<unsigned>(a.kv.KVH);
+    const dim3 split(groups, static_cast<unsigned>(a.kv.KVH), HD / 32);
+    if (blocks < static_cast<unsigned>(sms)) e = launch(combine_kernel<T, HD, 32, 8>, split, 512, 0, st, true, c);
+    else if (blocks < 4u * sms) e = launch(combine_kernel<T, HD, 32, 2>, split, 128, 0, st, true, c);
+    else e = launch(combine_kernel<T, HD, HD, 1>, grid, HD * 2, 0, st, true, c);
   }
   return e;
 }
