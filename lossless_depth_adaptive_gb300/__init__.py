@@ -436,11 +436,12 @@ class PagedCache:
 
     def _rows(self, name, t, heads, n):
         """[n, heads, head_dim] with the rows of a token contiguous: the stride between tokens."""
-        shape, stride, hd = t.shape, t.stride(), self.head_dim
-        if not (len(shape) == 3 and shape[2] == hd and (heads is None or shape[1] == heads) and shape[0] == n and
-                stride[2] == 1 and (stride[1] == hd or shape[1] == 1)):
-            raise DexError(DEX_EINVAL, f"{name} must be [tokens = {n}, {heads or 'heads'}, {hd}] with contiguous heads")
-        return stride[0] if n > 1 else shape[1] * hd
+        hd = self.head_dim
+        if t.dim() == 3:
+            (rows, h, d), (between, s1, s2) = t.shape, t.stride()
+            if rows == n and d == hd and s2 == 1 and (s1 == hd or h == 1) and (h == heads or heads is None):
+                return between if n > 1 else h * hd
+        raise DexError(DEX_EINVAL, f"{name} must be [tokens = {n}, {heads or 'heads'}, {hd}] with contiguous heads")
 
     def _vector(self, name, t, n, dtype):
         if not (t.dtype == dtype and t.dim() == 1 and t.shape[0] == n and t.is_contiguous()):
@@ -466,30 +467,37 @@ class PagedCache:
         [tokens, heads, head_dim] in the cache's type, allocated when not given; it may be q itself.
         rejected: int32 [1], receives the number of tokens out of range, which are skipped.
         """
-        n, f32 = k.shape[0], self._torch.float32
-        if not (k.dtype == v.dtype and (k.dtype == self._dtype or k.dtype == f32)):
+        n, dt, dev = k.shape[0], k.dtype, self._dev
+        f32 = dt == self._torch.float32
+        if v.dtype != dt or not (f32 or dt == self._dtype):
             raise DexError(DEX_EINVAL, "k and v must have the cache's type or fp32")
-        a = dex_append_args(None, k.data_ptr(), v.data_ptr(), None, 0, self._rows("k", k, self.kv_heads, n),
-                            self._rows("v", v, self.kv_heads, n), 0, self._vector("seq", seq, n, self._i32),
-                            self._vector("pos", pos, n, self._i32),
-                            None if rope_pos is None else self._vector("rope_pos", rope_pos, n, self._i32), n, 0,
-                            DEX_DT_FP32 if k.dtype == f32 else self.kv.dtype, theta)
-        _need(q is not None or q_out is None, "q_out needs q")
+        k_stride, v_stride = self._rows("k", k, self.kv_heads, n), self._rows("v", v, self.kv_heads, n)
+        here = k.get_device() == dev and v.get_device() == dev and seq.get_device() == dev and pos.get_device() == dev
+        q_ptr, out_ptr, q_stride, out_stride, heads = None, None, 0, 0, 0
         if q is not None:
-            a.q_stride = self._rows("q", q, None, n)
-            if q.dtype != k.dtype:
-                raise DexError(DEX_EINVAL, "q must have the type of k")
             heads = q.shape[1]
+            q_stride = self._rows("q", q, None, n)
+            if q.dtype != dt:
+                raise DexError(DEX_EINVAL, "q must have the type of k")
             if q_out is None:
                 q_out = self._torch.empty(q.shape, dtype=self._dtype, device=q.device)
-            a.q_out_stride = self._rows("q_out", q_out, heads, n)
-            if q_out.dtype != self._dtype:
+            elif q_out.dtype != self._dtype:
                 raise DexError(DEX_EINVAL, "q_out must have the cache's type")
-            a.q, a.q_out, a.n_heads = q.data_ptr(), q_out.data_ptr(), heads
+            out_stride = self._rows("q_out", q_out, heads, n)
+            q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+            here = here and q.get_device() == dev and q_out.get_device() == dev
+        elif q_out is not None:
+            raise DexError(DEX_EINVAL, "q_out needs q")
+        rope_ptr = None
+        if rope_pos is not None:
+            rope_ptr = self._vector("rope_pos", rope_pos, n, self._i32)
+            here = here and rope_pos.get_device() == dev
+        a = dex_append_args(q_ptr, k.data_ptr(), v.data_ptr(), out_ptr, q_stride, k_stride, v_stride, out_stride,
+                            self._vector("seq", seq, n, self._i32), self._vector("pos", pos, n, self._i32), rope_ptr, n,
+                            heads, DEX_DT_FP32 if f32 else self.kv.dtype, theta)
         rejected_ptr = None if rejected is None else self._vector("rejected", rejected, 1, self._i32)
-        for t in (k, v, q, q_out, seq, pos, rope_pos, rejected):
-            if t is not None and t.get_device() != self._dev:
-                self._on_device(k=k, v=v, q=q, q_out=q_out, seq=seq, pos=pos, rope_pos=rope_pos, rejected=rejected)
+        if not here or (rejected is not None and rejected.get_device() != dev):
+            self._on_device(k=k, v=v, q=q, q_out=q_out, seq=seq, pos=pos, rope_pos=rope_pos, rejected=rejected)
         self._run(self._lib_append, "dex_paged_append", self._kv_ref, C.byref(a), rejected_ptr)
         return q_out
 

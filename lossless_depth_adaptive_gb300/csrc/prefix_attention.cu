@@ -49,8 +49,10 @@ constexpr int kSms = 152;         // of the sm_103 part: workspace sizes and gri
 constexpr int kTileKeys = 128;    // keys of a tile of tile_kernel
 constexpr int kTileRows = 256;    // its query rows (two tiles of 128)
 // What a segment costs a CTA beside its key tiles, in tiles (queries, start and end of its pipeline, result), and the
-// units (tiles and these) of a CTA, at least.
-constexpr int kRowsSegCost = 1, kTileSegCost = 3;
+// units (tiles and these) of a CTA, at least.  With no cost 64 sequences behind 8192 positions take 60 us instead
+// of 46 (some CTAs get seven segments of one tile), 32 of 32 heads 45.5 instead of 42; with two tiles in
+// rows_kernel the latter 46; with two instead of four in tile_kernel 256 sequences behind 32768 162 instead of 158.
+constexpr int kRowsSegCost = 1, kTileSegCost = 4;
 constexpr int kRowsMinUnits = 3, kTileMinUnits = 5;
 constexpr int kMaxBatch = 1024;
 
@@ -493,6 +495,16 @@ struct PageLoader {
     const int page = page_at(first + i);
     if (i < n) box(which ? v : k, which ? v_bar : k_bar, which, kvh, key0, first + i, page, h);
   }
+  // The same in boxes of 16 rows, n16 of them from row 16 first16 on: what a tile at the end of a segment needs of
+  // its 64 rows (a sixth of the bytes of a batch of short sequences are beyond their ends otherwise).
+  __device__ __forceinline__ void load_kv16(const CUtensorMap* map16, uint8_t* k, uint64_t* k_bar, uint8_t* v, uint64_t* v_bar,
+                                            int kvh, int key0, int first16, int n16) const {
+    const int i = lane / (HD / 32), h = lane % (HD / 64), which = lane / (HD / 64) % 2;
+    const int at = (first16 + i) * 16, page = page_at(at >> kv->page_shift);
+    if (i < n16)
+      tma_load_4d((which ? v : k) + h * TILE * 128 + (at - key0) * 128, map16, which ? v_bar : k_bar, h * 64,
+                  at & ((1 << kv->page_shift) - 1), which * kv->KVH + kvh, page);
+  }
   // The page of a table entry at hand, n_pages (beyond the tensor: the copy fills zeros) for a bad id.
   __device__ __forceinline__ int page_at(int entry) const {
     const int page = __shfl_sync(0xffffffffu, ids, (entry - id0) & 31);
@@ -551,7 +563,7 @@ struct RowsSmem {
 
 template <typename T, int HD, int MT>
 __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
-    rows_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ SegWork w) {
+    rows_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm16, const __grid_constant__ SegWork w) {
   using SM = RowsSmem<HD, MT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -656,11 +668,13 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
         if (++st == SM::kStages) st = 0, phase ^= 1u;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        const bool edge = key0 < wk.k.lo || key0 + kRowsTile > wk.k.hi;
+        const int first16 = max(key0, wk.k.lo) >> 4, n16 = ((min(key0 + kRowsTile, wk.k.hi) + 15) >> 4) - first16;
         if (lane < 2) {
           const int x = lane ? vst : kst;
           if (n > 0) {
             bad_stage[x] = bad;
-            mbar_arrive_expect_tx(&full[x], static_cast<uint32_t>(n * ld.box_rows() * HD * 2));
+            mbar_arrive_expect_tx(&full[x], static_cast<uint32_t>((edge ? n16 * 16 : n * ld.box_rows()) * HD * 2));
           } else {
             bad_stage[x] = 0;
             mbar_arrive(&full[x]);
@@ -668,7 +682,10 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
           if (bad && lane && a.status) atomicOr(a.status, DEX_ATTN_BAD_PAGE);
         }
         __syncwarp();
-        ld.load_kv(smem + kst * SM::kBuf, &full[kst], smem + vst * SM::kBuf, &full[vst], wk.kvh, key0, first, n);
+        if (n > 0 && edge)
+          ld.load_kv16(&tm16, smem + kst * SM::kBuf, &full[kst], smem + vst * SM::kBuf, &full[vst], wk.kvh, key0, first16, n16);
+        else
+          ld.load_kv(smem + kst * SM::kBuf, &full[kst], smem + vst * SM::kBuf, &full[vst], wk.kvh, key0, first, n);
         n_ld += 2;
       }
       g += pc.units;
@@ -1176,8 +1193,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           l *= f;
           return true;
         };
-        if (!any || !__all_sync(0xffffffffu, whole && rv.last >= key0 + kTileKeys - 1)) {
-          // a team's first tile needs its maximum first; masked scores go back to TMEM as -inf
+        if (!__all_sync(0xffffffffu, whole && rv.last >= key0 + kTileKeys - 1)) {
+          // masked scores go back to TMEM as -inf
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             tmem_ld32_nowait(t_s + q * 32, s[0]);
@@ -1212,8 +1229,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
           fence_proxy_async_smem();
         }
-        // P with the m at hand, and the maximum on the way: it rarely asks for another m, and then the
-        // scores are still in TMEM
+        // P with the m at hand, and the maximum on the way: it asks for another m in a segment's first tile and
+        // rarely after, and the scores are still in TMEM then
         uint32_t p[4][16];
         do {
           const float sub = m > -INFINITY ? m : 0.0f;
@@ -1787,15 +1804,15 @@ cudaError_t launch_hd(const PrefixAttnArgs& a, const Plan& p, uint8_t* ws, cudaS
       e = launch(tile_kernel<T, HD>, dim3(static_cast<unsigned>(sms)), kTileThreads, TileSmem<HD>::kTotal, st, true, tm, tile);
   }
   if (e == cudaSuccess && (rows.do_own || rows.do_prefix)) {
-    CUtensorMap tm;
-    if (!page_map(&tm, a.kv, page < kRowsTile ? page : kRowsTile)) return cudaErrorInvalidValue;
+    CUtensorMap tm, tm16;
+    if (!page_map(&tm, a.kv, page < kRowsTile ? page : kRowsTile) || !page_map(&tm16, a.kv, 16)) return cudaErrorInvalidValue;
     const dim3 grid(static_cast<unsigned>(kRowsPerSm * sms));
     if (p.rows_mt == 1) {
       e = set_smem(rows_kernel<T, HD, 1>, RowsSmem<HD, 1>::kTotal, rows1_set, dev);
-      if (e == cudaSuccess) e = launch(rows_kernel<T, HD, 1>, grid, kRowsThreads, RowsSmem<HD, 1>::kTotal, st, true, tm, rows);
+      if (e == cudaSuccess) e = launch(rows_kernel<T, HD, 1>, grid, kRowsThreads, RowsSmem<HD, 1>::kTotal, st, true, tm, tm16, rows);
     } else {
       e = set_smem(rows_kernel<T, HD, 2>, RowsSmem<HD, 2>::kTotal, rows2_set, dev);
-      if (e == cudaSuccess) e = launch(rows_kernel<T, HD, 2>, grid, kRowsThreads, RowsSmem<HD, 2>::kTotal, st, true, tm, rows);
+      if (e == cudaSuccess) e = launch(rows_kernel<T, HD, 2>, grid, kRowsThreads, RowsSmem<HD, 2>::kTotal, st, true, tm, tm16, rows);
     }
   }
   if (e == cudaSuccess) {
@@ -1809,10 +1826,12 @@ cudaError_t launch_hd(const PrefixAttnArgs& a, const Plan& p, uint8_t* ws, cudaS
     while (c.row_bits < 5 && (1 << c.row_bits) < a.n_tokens * a.G) ++c.row_bits;
     const unsigned groups = static_cast<unsigned>((a.n_tokens * a.G + (1 << c.row_bits) - 1) >> c.row_bits);
     const dim3 grid(groups, static_cast<unsigned>(a.kv.KVH));
-    // the fewer blocks there are, the more warps share a row's parts and head dims
+    // The fewer blocks there are, the more warps share a row's parts and head dims.  Whole calls, us: 1 block
+    // of parts per K/V head and 8 K/V heads 85.9 with eight groups, 88.5 with two; 64 blocks 45.6 and 45.2; 160
+    // blocks 43.7, 32.5 and 34.4 with one group; 1752 blocks 215 with two, 208 with one.
     const unsigned blocks = groups * static_cast<unsigned>(a.kv.KVH);
     const dim3 split(groups, static_cast<unsigned>(a.kv.KVH), HD / 32);
-    if (blocks < static_cast<unsigned>(sms)) e = launch(combine_kernel<T, HD, 32, 8>, split, 512, 0, st, true, c);
+    if (blocks < 64) e = launch(combine_kernel<T, HD, 32, 8>, split, 512, 0, st, true, c);
     else if (blocks < 4u * sms) e = launch(combine_kernel<T, HD, 32, 2>, split, 128, 0, st, true, c);
     else e = launch(combine_kernel<T, HD, HD, 1>, grid, HD * 2, 0, st, true, c);
   }
