@@ -318,8 +318,10 @@ int dex_paged_append(const dex_paged_kv* kv, const dex_append_args* a, int32_t* 
  * positions 0..p, or with tree_mask every position before seq_len[b] - n and, of the last n,
  * position seq_len[b] - n + j where bit j of its word is set (n <= 64).  A query that sees
  * nothing gets zeros and lse -inf.  Query head h reads K/V head h / (n_heads / n_kv_heads).
- * prefix_len: every sequence's positions below it hold the same keys and values; they are
- * read through prefix_table (NULL: row 0 of the cache's table), once for the whole batch. */
+ * prefix_len is a promise: the positions below it hold the same keys and values for every
+ * sequence with queries, and every such sequence's table names them (usually the same pages).
+ * Where it pays they are read once for the whole batch, through prefix_table (NULL: row 0 of the
+ * cache's table, which has to name them then even if sequence 0 has no queries). */
 typedef struct dex_attention_args {
   const void* q;               /* device, cache's type, [n_tokens][n_heads][head_dim] */
   void* out;                   /* device, cache's type, [n_tokens][n_heads][head_dim] */

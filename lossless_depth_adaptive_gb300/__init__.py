@@ -515,9 +515,10 @@ class PagedCache:
         The queries of sequence b are tokens q_start[b] .. q_start[b+1]-1 (int32 [batch + 1], at most max_q
         each) and stand at its last positions; seq_len (int32 [batch]) counts them.  Query i of n sees
         positions 0 .. seq_len - n + i, or with tree_mask (int64 [tokens]) everything before the last n and
-        of those the ones whose bit is set.  Positions below prefix_len are read through prefix_table (int32;
-        default: row 0 of the table), once for the batch.  scale defaults to head_dim**-0.5.  lse: fp32
-        [tokens, heads], receives the log of the softmax denominator.  workspace: from
+        of those the ones whose bit is set.  prefix_len promises that the positions below it are the same for
+        every sequence with queries (and named by its table, usually the same pages); where it pays they are
+        read once for the batch, through prefix_table (int32; default: row 0 of the table).  scale defaults to
+        head_dim**-0.5.  lse: fp32 [tokens, heads], receives the log of the softmax denominator.  workspace: from
         attention_workspace(), allocated when not given.  status: int32 [1], receives DEX_ATTN_* bits.
         Rows of out and lse that belong to no sequence are left as they were.
         """

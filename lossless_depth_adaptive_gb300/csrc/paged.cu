@@ -18,7 +18,8 @@ __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ void from_f32(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void from_f32(__half& y, float x) { y = __float2half_rn(x); }
 
-// Eight consecutive elements as loaded (16 bytes of a 16-bit type, 32 of fp32).
+// Eight consecutive elements as loaded (16 bytes of a 16-bit type, 32 of fp32).  Nothing goes through the
+// read-only path: the kernel can be resident before the one that writes its inputs ends.
 template <typename T>
 struct alignas(16) Vec8 {
   T v[8];
@@ -29,7 +30,7 @@ __device__ __forceinline__ Vec8<T> load8(const T* p) {
   const uint4* s = reinterpret_cast<const uint4*>(p);
   uint4* d = reinterpret_cast<uint4*>(&r);
 #pragma unroll
-  for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i) d[i] = __ldg(s + i);
+  for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i) d[i] = __ldcg(s + i);
   return r;
 }
 
@@ -71,11 +72,11 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 8) paged_append_kernel(cons
   const int first = blockIdx.y * rows + lane / kItems;
   if (first < end) load_item(first);
 
-  const int seq = __ldg(a.seq + t), pos = __ldg(a.pos + t), pidx = pos >> a.kv.page_shift;
+  const int seq = a.seq[t], pos = a.pos[t], pidx = pos >> a.kv.page_shift;
   bool ok = seq >= 0 && seq < a.kv.batch && pos >= 0 && pidx < a.kv.table_width;
   int page = -1;
   if (ok) {
-    page = __ldg(a.kv.table + static_cast<int64_t>(seq) * a.kv.table_stride + pidx);
+    page = a.kv.table[static_cast<int64_t>(seq) * a.kv.table_stride + pidx];
     ok = page >= 0 && page < a.kv.n_pages;
   }
   if (!ok) {
@@ -84,7 +85,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 8) paged_append_kernel(cons
   }
   float4 w[4];   // (cos, sin) of the lane's eight pairs
   if (a.rotate) {
-    const int rpos = a.rope_pos ? __ldg(a.rope_pos + t) : pos;
+    const int rpos = a.rope_pos ? a.rope_pos[t] : pos;
     for (int j = lane; j < HD / 2; j += 32) {
       uint64_t turn = a.turn;
 #pragma unroll

@@ -130,11 +130,13 @@ struct SeqRef {
   bool valid;   // has queries, and they are in range
   bool bad;     // length out of range: rows are poisoned
 };
+// Lengths and tables are read by plain loads: a kernel here can be resident before the kernel that writes them
+// ends (programmatic launches), so they are not read-only for its lifetime.
 __device__ __forceinline__ SeqRef seq_ref(const PrefixAttnArgs& a, int b, bool* report = nullptr) {
   SeqRef s;
-  s.q0 = __ldg(a.q_start + b);
-  const int q1 = __ldg(a.q_start + b + 1);
-  s.len = __ldg(a.seq_len + b);
+  s.q0 = a.q_start[b];
+  const int q1 = a.q_start[b + 1];
+  s.len = a.seq_len[b];
   const bool range = s.q0 >= 0 && q1 >= s.q0 && q1 <= a.n_tokens && q1 - s.q0 <= a.max_q;
   s.n = range ? q1 - s.q0 : 0;
   s.valid = s.n > 0;
@@ -292,10 +294,10 @@ struct Walker {
 __device__ __forceinline__ int seq_of_token(const PrefixAttnArgs& a, int t) {
   int lo = 0, hi = a.kv.batch - 1;
   // with one query per sequence it is t itself: two loads instead of a chain of them
-  if (t <= hi && __ldg(a.q_start + t) <= t && (t == hi || __ldg(a.q_start + t + 1) > t)) return t;
+  if (t <= hi && a.q_start[t] <= t && (t == hi || a.q_start[t + 1] > t)) return t;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(a.q_start + mid) <= t) lo = mid;
+    if (a.q_start[mid] <= t) lo = mid;
     else hi = mid - 1;
   }
   return lo;
@@ -312,7 +314,7 @@ __device__ __forceinline__ RowView row_view(const PrefixAttnArgs& a, const SeqRe
   RowView v;
   v.owned = s.valid && t >= s.q0 && t < s.q0 + s.n;
   v.first = s.len - s.n;
-  v.word = a.tree && v.owned ? __ldg(reinterpret_cast<const unsigned long long*>(a.tree) + t) : 0ull;
+  v.word = a.tree && v.owned ? a.tree[t] : 0ull;
   v.last = a.tree ? v.first - 1 : v.first + (t - s.q0);
   if (s.bad) v.last = -1, v.word = 0;
   if (!v.owned) v.last = 0x7fffffff;   // its result is not used: no reason to mask
@@ -473,7 +475,7 @@ struct PageLoader {
   __device__ __forceinline__ void prefetch(int first, int n) {
     if (n > 0 && (first < id0 || first + n > id0 + 32)) {
       id0 = first;
-      ids = first + lane < id_end ? __ldg(tab + first + lane) : -1;
+      ids = first + lane < id_end ? tab[first + lane] : -1;
     }
   }
   // Whether a page of the tile has an id out of range.
@@ -1577,13 +1579,13 @@ __global__ void __launch_bounds__(DIMS * 2 * SPLIT) combine_kernel(const __grid_
   int pre_c0 = 0, n_pre = 0, own_c0 = 0, n_own = 0;
   if (b >= 0) {
     if (w.share) {
-      const int2 info = w.pre.pre_info[rg / w.pre_rt * a.kv.KVH + kvh];
+      const int2 info = __ldcg(w.pre.pre_info + rg / w.pre_rt * a.kv.KVH + kvh);
       pre_c0 = info.x;
       n_pre = info.y - info.x + 1;
     }
     const int nt = w.own_tile == kRowsTile ? own_range<kRowsTile>(w.own, s, r1).nt : own_range<kTileKeys>(w.own, s, r1).nt;
     if (nt > 0) {
-      const int2 info = w.own.own_info[own_info_of(a, w.own_rt, s.q0, b, rt, kvh)];
+      const int2 info = __ldcg(w.own.own_info + own_info_of(a, w.own_rt, s.q0, b, rt, kvh));
       own_c0 = info.x;
       n_own = info.y - info.x + 1;
       if (n_own == 1 && !w.share) n_own = 0;   // written where it was computed
@@ -1612,9 +1614,9 @@ __global__ void __launch_bounds__(DIMS * 2 * SPLIT) combine_kernel(const __grid_
                               ? joined_part<HD>(pre ? sw.pre_o : sw.own_o, pre ? sw.pre_ml : sw.own_ml, kvh, rows_all, rg)
                               : slot_part<HD>(sw.part_o, sw.part_ml, 2 * ((pre ? pre_c0 : own_c0) + i) + (i == 0 ? 1 : 0), rows,
                                               pre ? rg % rows : r - rt * rows);
-        ml[u] = *p.ml;
+        ml[u] = __ldcg(p.ml);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) x[u][q] = *reinterpret_cast<const float4*>(p.o + (warp * 4 + q) * p.step);
+        for (int q = 0; q < 4; ++q) x[u][q] = __ldcg(reinterpret_cast<const float4*>(p.o + (warp * 4 + q) * p.step));
       } else {
 #pragma unroll
         for (int q = 0; q < 4; ++q) x[u][q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);

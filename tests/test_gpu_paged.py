@@ -201,6 +201,140 @@ def test_attention_bad_pages_and_ranges():
     assert bool((out[1:4] == 7.0).all()) and not bool((out[[0, 4, 5]] == 7.0).any())
 
 
+def test_attention_inactive_first_slot():
+    """Sequence 0 is an empty slot without pages: the shared prefix comes from prefix_table."""
+    dexlib = require_gpu()
+    H, kvh, hd, ps, prefix = 32, 8, 128, 32, 200
+    lens, new = [0] + [prefix + n for n in (3, 90, 1, 64, 17)], [0, 1, 1, 1, 1, 1]
+    for h in (H, kvh):   # the prefix on either kernel
+        cache, pages, table = paged(dexlib, kvh, hd, ps, lens, BF, prefix)
+        shared = table[1, :-(-prefix // ps)].clone()
+        cache.table[0] = -1
+        q, start = queries(h, hd, new, BF)
+        seq_len = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        lse = torch.zeros(q.shape[:2], device="cuda")
+        out = cache.attention(q, start.cuda(), seq_len, 1, prefix, prefix_table=shared.cuda(), lse=lse, status=status)
+        assert int(status.item()) == 0
+        compare(out, lse, attention(pages, table, q.cpu(), start, lens, prefix, shared), torch.ones(5, dtype=torch.bool))
+
+
+@pytest.mark.parametrize("prefix", [0, 128])
+def test_attention_large_batch(prefix):
+    """The largest batch, most of it without queries or without positions."""
+    g = torch.Generator().manual_seed(5)
+    new = [int(x) for x in (torch.rand(1024, generator=g) < 0.06)]
+    new[0] = 1
+    lens = [prefix + int(x) if n else 0 for n, x in zip(new, torch.randint(1, 200, (1024,), generator=g))]
+    run_case(8, 2, 64, 64, FP, lens, new, prefix)
+
+
+def test_attention_strides():
+    """Queries that are one expanded row, an output inside a larger tensor, a table inside a wider one, tokens
+    before the first sequence's."""
+    dexlib = require_gpu()
+    H, kvh, hd, ps, prefix = 8, 2, 64, 32, 96
+    lens, new = [prefix + n for n in (5, 70, 33)], [1, 2, 1]
+    for prefix_len in (0, prefix):
+        cache, pages, table = paged(dexlib, kvh, hd, ps, lens, FP, prefix)
+        wide = torch.full((3, table.shape[1] + 5), -7, dtype=torch.int32, device="cuda")
+        wide[:, 2:2 + table.shape[1]] = table.cuda()
+        cache = dexlib.PagedCache(cache.pages, wide[:, 2:2 + table.shape[1]])
+        one = torch.randn((1, H, hd), device="cuda").to(FP)
+        q = one.expand(6, H, hd)
+        big = torch.full((6, H + 3, hd), 7.0, dtype=FP, device="cuda")
+        lse = torch.full((6, H), 7.0, device="cuda")
+        start = torch.tensor([2, 3, 5, 6], dtype=torch.int32)
+        cache.attention(q, start.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), 2, prefix_len,
+                        out=big[:, 1:H + 1], lse=lse)
+        own = torch.tensor([False, False, True, True, True, True])
+        compare(big[:, 1:H + 1], lse, attention(pages, table, q.cpu(), start, lens, prefix_len), own)
+        assert bool((big[:2] == 7.0).all()) and bool((big[:, 0] == 7.0).all()) and bool((big[:, H + 1:] == 7.0).all())
+        assert bool((lse[:2] == 7.0).all())
+
+
+def test_offsets_beyond_32_bits():
+    """Pages whose elements and bytes lie beyond 2^31 and 2^32: append and attention reach them."""
+    dexlib = require_gpu()
+    kvh, hd, ps, H = 8, 128, 64, 32
+    n_pages = (1 << 32) // (2 * kvh * ps * hd) + 40   # 2^32 elements and some
+    pages = torch.empty((n_pages, 2, kvh, ps, hd), dtype=BF, device="cuda")
+    ids = torch.tensor([[n_pages - 1, 3], [n_pages - 30, n_pages - 2]], dtype=torch.int32)
+    cache = dexlib.PagedCache(pages, ids.cuda())
+    gen = torch.Generator().manual_seed(4)
+    lens = [100, 128]
+    n = sum(lens)
+    k, v = (torch.randn((n, kvh, hd), generator=gen).to(BF) for _ in range(2))
+    seq = torch.tensor([0] * 100 + [1] * 128, dtype=torch.int32, device="cuda")
+    pos = torch.cat((torch.arange(100), torch.arange(128))).int().cuda()
+    cache.append(k.cuda(), v.cuda(), seq, pos, theta=0.0)
+    small = torch.zeros((4, 2, kvh, ps, hd), dtype=BF)
+    small_ids = torch.tensor([[0, 1], [2, 3]], dtype=torch.int32)
+    for i in range(4):
+        small[i] = pages[int(ids.view(-1)[i])].cpu()
+    for t in range(n):
+        b, p = int(seq[t]), int(pos[t])
+        assert t % 37 or (torch.equal(small[2 * b + p // ps, 0, :, p % ps], k[t]) and
+                          torch.equal(small[2 * b + p // ps, 1, :, p % ps], v[t]))
+    for new in ([1, 1], [20, 60]):
+        q, start = queries(H, hd, new, BF)
+        lse = torch.zeros(q.shape[:2], device="cuda")
+        out = cache.attention(q, start.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), max(new), lse=lse)
+        compare(out, lse, attention(small, small_ids, q.cpu(), start, lens), torch.ones(len(q), dtype=torch.bool))
+
+
+def test_attention_two_at_once():
+    """Calls on two streams, a workspace each, give what they give alone."""
+    dexlib = require_gpu()
+    H, kvh, hd, ps, prefix = 32, 8, 128, 64, 512
+    lens, new = [prefix + 40 * i + 1 for i in range(20)], [1] * 20
+    cache, pages, table = paged(dexlib, kvh, hd, ps, lens, BF, prefix)
+    seq_len = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    qs = [queries(H, hd, new, BF, seed=s)[0] for s in (1, 2)]
+    start = queries(H, hd, new, BF)[1].cuda()
+    alone = [cache.attention(q, start, seq_len, 1, prefix) for q in qs]
+    outs = [torch.zeros_like(q) for q in qs]
+    spaces = [cache.attention_workspace(q, 1, prefix) for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for q, o, w, st in zip(qs, outs, spaces, streams):
+            with torch.cuda.stream(st):
+                cache.attention(q, start, seq_len, 1, prefix, out=o, workspace=w)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, o) for a, o in zip(alone, outs))
+
+
+def test_calls_follow_each_other_closely():
+    """Steps back to back on one stream, each changing the lengths and the cache the next one reads: what
+    a step sees does not depend on how early its kernels become resident."""
+    dexlib = require_gpu()
+    H, kvh, hd, ps = 8, 2, 128, 16
+    lens = [30, 61, 7]
+    gen = torch.Generator().manual_seed(8)
+    steps = 40
+    cache, pages, table = paged(dexlib, kvh, hd, ps, [n + steps for n in lens], FP, fill=0.0)
+    pages = pages.clone()
+    qkv = torch.randn((steps, 3, H + 2 * kvh, hd), generator=gen).to(FP)
+    dev, seq = qkv.cuda(), torch.arange(3, dtype=torch.int32, device="cuda")
+    pos = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    start = torch.arange(4, dtype=torch.int32, device="cuda")
+    outs, ws = [], cache.attention_workspace(dev[0, :, :H], 1)
+    torch.cuda.synchronize()
+    for i in range(steps):
+        cache.append(dev[i, :, H:H + kvh], dev[i, :, H + kvh:], seq, pos, theta=0.0)
+        pos += 1
+        outs.append(cache.attention(dev[i, :, :H], start, pos, 1, workspace=ws))
+    torch.cuda.synchronize()
+    for i in range(steps):
+        for b in range(3):
+            p = lens[b] + i
+            pages[int(table[b, p // ps]), 0, :, p % ps] = qkv[i, b, H:H + kvh]
+            pages[int(table[b, p // ps]), 1, :, p % ps] = qkv[i, b, H + kvh:]
+        o, _, bo, _ = attention(pages, table, qkv[i, :, :H], start.cpu(), [n + i + 1 for n in lens])
+        assert bool(((outs[i].cpu().double() - o).abs() <= bo).all()), i
+
+
 def test_attention_graph_and_streams():
     """A captured call replayed on other lengths and tables; a call on a side stream."""
     dexlib = require_gpu()
