@@ -1113,8 +1113,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     float* join = reinterpret_cast<float*>(smem + SM::oQ);   // [HD][128] O of team 1
     float2* join_ml = reinterpret_cast<float2*>(smem + SM::oMl);
     uint32_t n_s = 0, n_seg = 0, base = 0;   // score tiles of this team, segments, loads so far
-    auto free_load = [&](uint32_t load, bool both) {   // the stage of a load goes back (both: for the other team too)
-      uint64_t* bar = &empty[load % SM::kStages];
+    auto stage_of = [&](int load) { return &empty[(base + static_cast<uint32_t>(load)) % SM::kStages]; };
+    auto free_stage = [&](uint64_t* bar, bool both) {   // a load's stage goes back (both: for the other team too)
       mbar_arrive(bar);
       if (both) mbar_arrive(bar);
     };
@@ -1161,7 +1161,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (on) rv = wk.prefix ? row_view(a, seq_ref(a, seq_of_token(a, t_row)), t_row) : row_view(a, wk.s, t_row);
       float m = -INFINITY, l = 0.0f;
       bool any = false;   // this team had a tile
-      int last = -1;      // its last one
+      // stages of K of its next tile and V of its last one (thread 0), at hand before they are to be freed: the
+      // loads that wait for them are needed within a tile's time
+      uint64_t *k_stage = stage_of(k_load(alt ? team : 0, cnt, ahead)), *v_stage = nullptr;
       for (int j = alt ? team : 0; j < cnt; j += ahead == 2 ? 2 : 1) {
         if (ok && !pipe_wait(&s_full[team], n_s & 1u)) {
           timed_out();
@@ -1170,6 +1172,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
+        if (r128 == 0) {   // K of this tile and V of the team's tile before it are read
+          free_stage(k_stage, alt);
+          if (any) free_stage(v_stage, alt);
+        }
         const int key0 = (wk.k.t0 + tile + j) * kTileKeys;
         const bool whole = wk.k.lo <= key0 && wk.k.hi >= key0 + kTileKeys;
         uint32_t s[2][32];
@@ -1266,11 +1272,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[team]);
-        if (r128 == 0) {   // K of this tile and V of the team's tile before it are read
-          free_load(base + static_cast<uint32_t>(k_load(j, cnt, ahead)), alt);
-          if (last >= 0) free_load(base + static_cast<uint32_t>(v_load(last, cnt, ahead)), alt);
-          last = j;
-        }
+        v_stage = stage_of(v_load(j, cnt, ahead));
+        k_stage = stage_of(k_load(j + ahead, cnt, ahead));
         ++n_s;
       }
       // ---------------- the segment's result ----------------
@@ -1280,7 +1283,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
-      if (r128 == 0 && last >= 0) free_load(base + static_cast<uint32_t>(v_load(last, cnt, ahead)), alt);
+      if (r128 == 0 && any) free_stage(v_stage, alt);
       if (!ok || seg_bad[0] || seg_bad[1] || (!wk.prefix && wk.s.bad)) l = quiet_nan();
       const bool read = ok && any;   // warp-uniform
       if (alt && team == 1) {
