@@ -276,8 +276,9 @@ typedef enum dex_dtype { DEX_DT_BF16 = 0, DEX_DT_FP16 = 1, DEX_DT_FP32 = 2 } dex
  * (page_stride = n_layers * 2 * n_kv_heads * page_size * head_dim, pages offset to the layer).
  * Several sequences may name the same page (a shared prefix).
  * Constraints (DEX_EINVAL otherwise): head_dim 64 or 128; page_size 16, 32, 64, 128 or 256;
- * dtype DEX_DT_BF16 or DEX_DT_FP16; pages 16-byte aligned; page_stride a multiple of 8 and at
- * least one page; batch <= 1024; table_width * page_size < 2^31; table_stride >= table_width. */
+ * dtype DEX_DT_BF16 or DEX_DT_FP16; pages 16-byte aligned, n_pages >= 1; page_stride a multiple of 8
+ * and at least one page; n_kv_heads and batch 1 .. 1024; table_width >= 1, table_width * page_size <=
+ * 2^31 - 512; table_stride >= table_width.  A call takes at most 2^23 tokens. */
 typedef struct dex_paged_kv {
   void* pages;            /* device, bf16 or fp16 */
   const int32_t* table;   /* device, int32 [batch][table_stride] page ids */
@@ -321,7 +322,8 @@ int dex_paged_append(const dex_paged_kv* kv, const dex_append_args* a, int32_t* 
  * prefix_len is a promise: the positions below it hold the same keys and values for every
  * sequence with queries, and every such sequence's table names them (usually the same pages).
  * Where it pays they are read once for the whole batch, through prefix_table (NULL: row 0 of the
- * cache's table, which has to name them then even if sequence 0 has no queries). */
+ * cache's table, which has to name them then even if sequence 0 has no queries).  A query at a position
+ * below prefix_len still sees no position beyond its own. */
 typedef struct dex_attention_args {
   const void* q;               /* device, cache's type, [n_tokens][n_heads][head_dim] */
   void* out;                   /* device, cache's type, [n_tokens][n_heads][head_dim] */
@@ -350,8 +352,9 @@ int dex_prefix_attention_workspace(const dex_paged_kv* kv, const dex_attention_a
 /* Attention of a ragged batch of queries over a paged cache whose sequences share their first
  * prefix_len positions.  Scores, softmax statistics and sums are fp32; the probabilities enter the
  * second product in the cache's type.  Rows of out and lse that belong to no sequence are
- * left as they were.  Keys and values at positions below seq_len must be finite; what pages hold
- * beyond is never used.  A page id that is out of range is never followed: the rows that need
+ * left as they were; out must not overlap q.  Keys and values at positions below seq_len, and with
+ * prefix_len > 0 below that, must be finite, seen by a query or not; what pages hold beyond is never
+ * used.  The lengths must not change while the call runs.  A page id that is out of range is never followed: the rows that need
  * it become NaN and status gets DEX_ATTN_BAD_PAGE.  A sequence whose seq_len is negative or beyond the
  * table gets NaN rows, one whose queries exceed max_q or n_tokens is skipped, both with DEX_ATTN_BAD_RANGE.
  * workspace: device, 256-byte aligned, at least the bytes dex_prefix_attention_workspace gives

@@ -520,7 +520,8 @@ class PagedCache:
         read once for the batch, through prefix_table (int32; default: row 0 of the table).  scale defaults to
         head_dim**-0.5.  lse: fp32 [tokens, heads], receives the log of the softmax denominator.  workspace: from
         attention_workspace(), allocated when not given.  status: int32 [1], receives DEX_ATTN_* bits.
-        Rows of out and lse that belong to no sequence are left as they were.
+        Rows of out and lse that belong to no sequence are left as they were.  out must not overlap q, and what
+        the cache holds at positions below seq_len and prefix_len must be finite.
         """
         i32, batch = self._i32, self.kv.batch
         n, heads = q.shape[0], q.shape[1]

@@ -168,6 +168,11 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// Positions of a sequence and tokens of a call: a tile beyond the last one still counts in 31 bits, and so do the
+// rows of 128 query heads.
+constexpr int64_t kMaxPositions = (int64_t(1) << 31) - 512;
+constexpr int kMaxTokens = 1 << 23;
+
 // Checks a cache description and fills the kernels' form of it.
 int paged_kv(const dex_paged_kv* kv, dex::PagedKv* out) {
   if (!kv || (kv->head_dim != 64 && kv->head_dim != 128) || kv->n_pages < 1 || kv->n_kv_heads < 1 ||
@@ -177,7 +182,7 @@ int paged_kv(const dex_paged_kv* kv, dex::PagedKv* out) {
   int shift = 4;
   while (shift < 8 && (1 << shift) != kv->page_size) ++shift;
   if ((1 << shift) != kv->page_size) return DEX_EINVAL;
-  if (static_cast<int64_t>(kv->table_width) * kv->page_size >= (int64_t(1) << 31)) return DEX_EINVAL;
+  if (static_cast<int64_t>(kv->table_width) * kv->page_size > kMaxPositions) return DEX_EINVAL;
   const int64_t page_elems = int64_t(2) * kv->n_kv_heads * kv->page_size * kv->head_dim;
   if (kv->page_stride < page_elems || kv->page_stride % 8 || kv->page_stride >= (int64_t(1) << 39)) return DEX_EINVAL;
   out->pages = kv->pages;
@@ -200,7 +205,7 @@ extern "C" int dex_paged_append(const dex_paged_kv* kv, const dex_append_args* a
   dex::AppendArgs d = {};
   const int rc = paged_kv(kv, &d.kv);
   if (rc) return rc;
-  if (!a || a->n_tokens < 0 || !kv->pages || !kv->table || !aligned16(kv->pages)) return DEX_EINVAL;
+  if (!a || a->n_tokens < 0 || a->n_tokens > kMaxTokens || !kv->pages || !kv->table || !aligned16(kv->pages)) return DEX_EINVAL;
   if (a->in_dtype != kv->dtype && a->in_dtype != DEX_DT_FP32) return DEX_EINVAL;
   if (!(a->rope_theta == 0.0f || (a->rope_theta >= 1.0f && a->rope_theta < INFINITY))) return DEX_EINVAL;
   const int64_t vec = a->in_dtype == DEX_DT_FP32 ? 4 : 8;   // elements in 16 bytes
@@ -246,7 +251,7 @@ extern "C" int dex_paged_append(const dex_paged_kv* kv, const dex_append_args* a
 static int attention_args(const dex_paged_kv* kv, const dex_attention_args* a, dex::PrefixAttnArgs* d) {
   const int rc = paged_kv(kv, &d->kv);
   if (rc) return rc;
-  if (!a || a->n_tokens < 0 || a->n_tokens >= (1 << 24) || a->n_heads < 1 || a->n_heads % kv->n_kv_heads ||
+  if (!a || a->n_tokens < 0 || a->n_tokens > kMaxTokens || a->n_heads < 1 || a->n_heads % kv->n_kv_heads ||
       a->n_heads / kv->n_kv_heads > 128 || a->max_q < 1 || a->prefix_len < 0 ||
       a->prefix_len > static_cast<int64_t>(kv->table_width) * kv->page_size)
     return DEX_EINVAL;

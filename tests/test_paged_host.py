@@ -40,7 +40,8 @@ def attn_args(**over):
 BAD_KV = [dict(head_dim=96), dict(head_dim=0), dict(page_size=8), dict(page_size=48), dict(page_size=512), dict(n_pages=0),
           dict(n_kv_heads=0), dict(n_kv_heads=-1), dict(n_kv_heads=2000), dict(batch=0), dict(batch=1025),
           dict(table_width=0), dict(table_stride=3), dict(dtype=2), dict(dtype=-1), dict(page_stride=4095),
-          dict(page_stride=4100), dict(page_stride=-4096), dict(table_width=1 << 28, table_stride=1 << 28)]
+          dict(page_stride=4100), dict(page_stride=-4096), dict(table_width=1 << 28, table_stride=1 << 28),
+          dict(table_width=(1 << 27) - 31, table_stride=1 << 28)]
 
 
 @pytest.mark.parametrize("bad", BAD_KV + [dict(pages=None), dict(table=None), dict(pages=(1 << 20) + 2)])
@@ -58,7 +59,8 @@ def test_bad_cache_is_refused(bad):
     dict(n_heads=0), dict(k=(1 << 23) + 8), dict(v=(1 << 24) + 2), dict(q=(1 << 22) + 4), dict(q_out=(1 << 25) + 8),
     dict(k_stride=132), dict(v_stride=129), dict(q_stride=260), dict(q_out_stride=258), dict(q_out_stride=64),
     dict(in_dtype=1), dict(in_dtype=3), dict(in_dtype=-1), dict(rope_theta=0.5), dict(rope_theta=-1.0),
-    dict(rope_theta=float("nan")), dict(rope_theta=float("inf")), dict(q=1 << 25, in_dtype=2), dict(q=1 << 25, q_stride=512)])
+    dict(rope_theta=float("nan")), dict(rope_theta=float("inf")), dict(q=1 << 25, in_dtype=2), dict(q=1 << 25, q_stride=512),
+    dict(n_tokens=(1 << 23) + 1), dict(n_tokens=2 ** 31 - 1)])
 def test_bad_append_is_refused(bad):
     assert dexlib.lib().dex_paged_append(C.byref(kv()), C.byref(append_args(**bad)), None, None) == EINVAL
 
@@ -75,7 +77,7 @@ def test_null_structs_are_refused():
 
 
 @pytest.mark.parametrize("bad", [
-    dict(n_tokens=-1), dict(n_tokens=1 << 24), dict(n_heads=0), dict(n_heads=5), dict(n_heads=258), dict(max_q=0),
+    dict(n_tokens=-1), dict(n_tokens=1 << 24), dict(n_tokens=(1 << 23) + 1), dict(n_heads=0), dict(n_heads=5), dict(n_heads=258), dict(max_q=0),
     dict(max_q=-3), dict(prefix_len=-1), dict(prefix_len=65), dict(q=None), dict(out=None), dict(q_start=None),
     dict(seq_len=None), dict(q=(1 << 22) + 8), dict(out=(1 << 23) + 4), dict(q_stride=258), dict(out_stride=250),
     dict(out_stride=248), dict(scale=float("nan")), dict(scale=float("inf")), dict(tree_mask=1 << 20, max_q=65)])
@@ -95,6 +97,20 @@ def test_workspace_size():
         assert L.dex_prefix_attention(C.byref(c), C.byref(a), 1 << 20, need - 1, None, None) == ECAP
         assert L.dex_prefix_attention(C.byref(c), C.byref(a), (1 << 20) + 16, need, None, None) == EINVAL
         assert L.dex_prefix_attention(C.byref(c), C.byref(a), None, need, None, None) == EINVAL
+
+
+def test_largest_sizes():
+    """The limits themselves are taken (their workspace can be told); one more is refused."""
+    most = ((1 << 31) - 512) // 16
+    c = kv(batch=1, table_width=most, table_stride=most, n_kv_heads=1)
+    assert dexlib.dex_prefix_attention_workspace(c, attn_args(prefix_len=(1 << 31) - 512)) > 0
+    c = kv(n_kv_heads=1)
+    a = attn_args(n_tokens=1 << 23, n_heads=128, max_q=1 << 23, prefix_len=0)
+    assert 0 < dexlib.dex_prefix_attention_workspace(c, a) < 1 << 40
+    a.prefix_len, a.max_q, a.n_heads = 64, 1, 64   # with a shared prefix: every row's result twice, in fp32
+    assert dexlib.dex_prefix_attention_workspace(c, a) > (1 << 29) * 2 * 64 * 4
+    a.n_tokens += 1
+    assert dexlib.lib().dex_prefix_attention_workspace(C.byref(c), C.byref(a), C.byref(C.c_size_t())) == EINVAL
 
 
 def test_cache_object_refuses_wrong_tensors():
