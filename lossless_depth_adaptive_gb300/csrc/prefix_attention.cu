@@ -155,7 +155,7 @@ __device__ __forceinline__ KeyRange own_range(const SegWork& w, const SeqRef& s,
   KeyRange k;
   k.lo = w.share ? w.a.prefix_len : 0;
   const int last = s.len - s.n + w.by_g.div(r1 - 1);   // position of the last query
-  k.hi = s.bad ? 0 : w.a.tree ? s.len : max(0, last + 1);
+  k.hi = s.bad ? 0 : w.a.tree ? s.len : min(max(0, last + 1), s.len);
   k.t0 = k.lo / TILE;
   k.nt = k.hi > k.lo ? (k.hi + TILE - 1) / TILE - k.t0 : 0;
   if (k.nt == 0) {
@@ -179,7 +179,8 @@ struct Piece {
 };
 
 // The segment that holds a unit, and the walk to the next one.  A segment is COST units followed by its
-// key tiles.
+// key tiles.  Lengths that change under a call (a caller's mistake) make its results wrong, but no loop
+// endless and no index leave its array: each read of a sequence is checked, and the walk ends within the batch.
 template <int RT, int TILE, int COST>
 struct Walker {
   const SegWork& w;
@@ -227,7 +228,7 @@ struct Walker {
     prefix = false;
     r0 = rt * RT;
     rows = min(RT, s.n * w.a.G - r0);
-    k = own_range<TILE>(w, s, r0 + rows);
+    k = own_range<TILE>(w, s, max(r0 + rows, 1));
   }
   // Segment of unit g (cum[b]: own units of all K/V heads before sequence b); returns the unit within it.
   __device__ __forceinline__ int find(uint32_t g, const uint32_t* cum) {
@@ -248,11 +249,12 @@ struct Walker {
     for (rt = 0;; ++rt) {
       set_own();
       const uint32_t cnt = units(k.nt) * static_cast<uint32_t>(w.a.kv.KVH);
-      if (g < cnt) break;
+      if (g < cnt || (rt + 1) * RT >= s.n * w.a.G) break;
       g -= cnt;
     }
-    kvh = static_cast<int>(g / units(k.nt));
-    return static_cast<int>(g % units(k.nt));
+    const uint32_t each = max(units(k.nt), 1u);
+    kvh = min(static_cast<int>(g / each), w.a.kv.KVH - 1);
+    return static_cast<int>(g % each);
   }
   // The next segment that has tiles (the caller knows that there is one).
   __device__ __forceinline__ void next() {
@@ -280,6 +282,7 @@ struct Walker {
         if (k.nt > 0) return;
       }
     }
+    b = w.a.kv.batch - 1;
   }
   // Token and query head of row r of the segment.
   __device__ __forceinline__ void row_of(int r, int& t, int& h) const {
@@ -1582,19 +1585,24 @@ __global__ void __launch_bounds__(DIMS * 2 * SPLIT) combine_kernel(const __grid_
   const SeqRef s = seq_ref(a, max(b, 0));
   const int r = rg - s.q0 * a.G, rt = b >= 0 ? r / w.own_rt : 0, r1 = min((rt + 1) * w.own_rt, s.n * a.G);
   griddep_wait();
-  // this row's parts: prefix parts of CTAs pre_c0 .., then own parts of CTAs own_c0 ..
+  // this row's parts: prefix parts of CTAs pre_c0 .., then own parts of CTAs own_c0 ..  A kernel that gave up
+  // waiting leaves entries that hold anything: none of them is followed.
+  auto parts_of = [](int2 info, int rt) {
+    const int ctas = rt == kTileRows ? kSms : kRowsPerSm * kSms;
+    return info.x >= 0 && info.x <= info.y && info.y < ctas ? info.y - info.x + 1 : 0;
+  };
   int pre_c0 = 0, n_pre = 0, own_c0 = 0, n_own = 0;
   if (b >= 0) {
     if (w.share) {
       const int2 info = __ldcg(w.pre.pre_info + rg / w.pre_rt * a.kv.KVH + kvh);
       pre_c0 = info.x;
-      n_pre = info.y - info.x + 1;
+      n_pre = parts_of(info, w.pre_rt);
     }
     const int nt = w.own_tile == kRowsTile ? own_range<kRowsTile>(w.own, s, r1).nt : own_range<kTileKeys>(w.own, s, r1).nt;
     if (nt > 0) {
       const int2 info = __ldcg(w.own.own_info + own_info_of(a, w.own_rt, s.q0, b, rt, kvh));
       own_c0 = info.x;
-      n_own = info.y - info.x + 1;
+      n_own = parts_of(info, w.own_rt);
       if (n_own == 1 && !w.share) n_own = 0;   // written where it was computed
     }
   }
