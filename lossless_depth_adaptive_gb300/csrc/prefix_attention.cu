@@ -623,6 +623,11 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
       if (pc.cnt == 0) break;   // only at the end of the range
       // the segment's description, row table and query rows
       const int slot = static_cast<int>(n_seg % n_slots), row0 = slot * (SM::kQRows / n_slots);
+      // its first page ids are on their way meanwhile
+      ld.start(wk.prefix ? a.prefix_table : a.kv.table + static_cast<int64_t>(wk.b) * a.kv.table_stride, wk.k.hi);
+      int first0 = 0;
+      const int n0 = ld.boxes((wk.k.t0 + pc.tile) * kRowsTile, wk.k.lo, wk.k.hi, first0);
+      ld.prefetch(first0, n0);
       if (n_seg >= static_cast<uint32_t>(n_slots) &&
           !pipe_wait(&seg_empty[slot], (n_seg / n_slots - 1) & 1u))
         ok = false;
@@ -657,7 +662,6 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
         if (lane < wk.rows)
           bulk_load_1d(smem + SM::oQ + (row0 + lane) * SM::kQRow, static_cast<const T*>(a.q) + t * a.q_stride + h * HD, HD * 2,
                        &seg_full[slot]);
-        ld.start(wk.prefix ? a.prefix_table : a.kv.table + static_cast<int64_t>(wk.b) * a.kv.table_stride, wk.k.hi);
       }
       for (int i = 0; i < pc.cnt && ok; ++i) {
         const int key0 = (wk.k.t0 + pc.tile + i) * kRowsTile;
@@ -1221,6 +1225,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           tmem_wait_st();
           tile_m *= c;
           move_m();
+        } else if (!any) {
+          // the first tile's maximum: a pass of loads, where the exponentials below would be taken twice
+          float mx[2] = {-INFINITY, -INFINITY};
+          tmem_ld32_nowait(t_s, s[0]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            tmem_wait_ld();
+            if (q < 3) tmem_ld32_nowait(t_s + (q + 1) * 32, s[(q + 1) & 1]);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              mx[i & 1] = max3(mx[i & 1], __uint_as_float(s[q & 1][2 * i]), __uint_as_float(s[q & 1][2 * i + 1]));
+          }
+          m = fmaxf(mx[0], mx[1]) * c;
         }
         if (!whole) {
           // rows of V outside the segment hold anything, and P = 0 must meet a finite v
@@ -1240,8 +1257,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
           fence_proxy_async_smem();
         }
-        // P with the m at hand, and the maximum on the way: it asks for another m in a segment's first tile and
-        // rarely after, and the scores are still in TMEM then
+        // P with the m at hand, and the maximum on the way: it rarely asks for another m, and the scores are still
+        // in TMEM then
         uint32_t p[4][16];
         do {
           const float sub = m > -INFINITY ? m : 0.0f;
