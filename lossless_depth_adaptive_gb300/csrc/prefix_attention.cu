@@ -13,10 +13,10 @@
 //  * own segment: rows of one sequence against its positions from prefix_len on (from 0 when
 //    nothing is shared).
 // Key tiles of all segments are laid end to end, each segment behind a few units that stand for what it
-// costs beside its tiles, and cut into equal contiguous ranges, one per CTA of a persistent grid, so
-// lengths need no plan on the host and any mix of lengths balances.
-// A segment that lies in one CTA is finished there; one that is cut leaves a partial (m, l, O) per
-// CTA, and combine_kernel joins the parts of each row in a fixed order (no atomics: the same
+// costs beside its tiles, and cut into equal contiguous ranges, one per CTA of a persistent grid (or two, from a
+// queue), so lengths need no plan on the host and any mix of lengths balances.
+// A segment that lies in one range is finished there; one that is cut leaves a partial (m, l, O) per
+// range, and combine_kernel joins the parts of each row in a fixed order (no atomics: the same
 // lengths give the same bits).
 //
 // Two kernels compute segments:
@@ -54,6 +54,14 @@ constexpr int kTileRows = 256;    // its query rows (two tiles of 128)
 // rows_kernel the latter 46; with two instead of four in tile_kernel 256 sequences behind 32768 162 instead of 158.
 constexpr int kRowsSegCost = 1, kTileSegCost = 4;
 constexpr int kRowsMinUnits = 3, kTileMinUnits = 5;
+// Where tile_kernel computes the prefix and rows_kernel the rest, they run side by side: tile_kernel takes SMs in
+// proportion to the work, a unit of it counted as kTileWeight of rows_kernel's, and rows_kernel's CTAs, those on
+// the other SMs from the start and those that follow on its SMs, take kRowsQueue ranges each on average from a
+// queue.  64 sequences behind 8192 positions and 256 behind 32768: 37.7 and 144.8 us; weight 4 41.5 and 149.7, 6
+// 39.2 and 146.9; with a fixed range per CTA and all SMs for tile_kernel first 44.7 and 151.9; four ranges per CTA
+// 40.9 and 145.3, one 40.6 and 156.
+constexpr float kTileWeight = 5.0f;
+constexpr int kRowsQueue = 2;
 constexpr int kMaxBatch = 1024;
 
 // Division by a number fixed for the call: n / d for 0 <= n < 2^31 (multiply, add, shift).
@@ -79,13 +87,16 @@ struct SegWork {
   int32_t do_own;       // this kernel computes the own segments
   int32_t joined;       // 1: rows have prefix and own parts, so a finished segment is not yet the output
   int32_t slots;        // rows_kernel: segments posted ahead
-  float* part_o;        // parts of cut segments, two per CTA: [2 * CTAs][hd / 4][rows][4]
-  float2* part_ml;      // [2 * CTAs][rows] (m, l)
+  int32_t behind_rt;    // tile_kernel: rows per segment of the rows_kernel behind it (it computes the own segments), or 0
+  uint32_t* queue;      // rows_kernel behind tile_kernel, which sets them: next range to take, CTAs that start beside
+                        // it; or null: CTA i takes range i
+  float* part_o;        // parts of cut segments, two per range: [2 * ranges][hd / 4][rows][4]
+  float2* part_ml;      // [2 * ranges][rows] (m, l)
   float* pre_o;         // finished prefix segments (joined): [KVH][hd / 4][n_tokens * G][4]
   float2* pre_ml;       // [KVH][n_tokens * G]
   float* own_o;         // the same of own segments
   float2* own_ml;
-  int2* pre_info;       // [prefix segments] first and last CTA
+  int2* pre_info;       // [prefix segments] first and last range
   int2* own_info;       // [own segments]
 };
 
@@ -380,8 +391,26 @@ __device__ __forceinline__ uint32_t count_units(const W& wk, uint32_t* cum, uint
   return wk.pre_units() + base;
 }
 
-// Shares of `total` units over at most `grid` CTAs: contiguous, equal within one, none below `least`
-// (but in a call that has no more); CTA c takes [begin(c), begin(c + 1)).
+// Units of the rows_kernel behind a tile_kernel (about: a causal segment may end a tile earlier); the block's threads
+// together.  scratch: a word per warp.
+template <int THREADS>
+__device__ __forceinline__ uint32_t units_behind(const SegWork& w, uint32_t* scratch) {
+  uint32_t n = 0;
+  for (int b = threadIdx.x; b < w.a.kv.batch; b += THREADS) {
+    const SeqRef s = seq_ref(w.a, b);
+    if (s.valid && s.len > w.a.prefix_len)
+      n += static_cast<uint32_t>((s.n * w.a.G + w.behind_rt - 1) / w.behind_rt * ((s.len - w.a.prefix_len + kRowsTile - 1) / kRowsTile + kRowsSegCost));
+  }
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (threadIdx.x % 32 == 0) scratch[threadIdx.x / 32] = n;
+  __syncthreads();
+  n = 0;
+  for (int i = 0; i < THREADS / 32; ++i) n += scratch[i];
+  return n * static_cast<uint32_t>(w.a.kv.KVH);
+}
+
+// Shares of `total` units in at most `grid` ranges (of a CTA each, mostly): contiguous, equal within one, none below
+// `least` (but in a call that has no more); range c is [begin(c), begin(c + 1)).
 struct Share {
   uint32_t ctas, each, more;   // the first `more` CTAs take each + 1 units
   __device__ __forceinline__ Share(uint32_t total, uint32_t grid, uint32_t least) {
@@ -537,7 +566,7 @@ struct PageLoader {
 struct alignas(16) SegDesc {
   int32_t rows, mt, lo, hi;
   int32_t key0, cnt, kvh, flags;            // key0: first tile's first position; flags: kSeg* bits
-  int32_t info, last_cta, pad0, pad1;       // entry of pre_info / own_info, CTA of the last tile (first part only)
+  int32_t info, range, last_range, pad;     // entry of pre_info / own_info, the range, that of the last tile (first part only)
 };
 constexpr int kSegPrefix = 1, kSegStarts = 2, kSegEnds = 4, kSegBad = 8, kSegLast = 16;
 struct alignas(16) RowDesc {
@@ -561,8 +590,8 @@ struct RowsSmem {
   static constexpr uint32_t oSeg = oSum + kRowsWarps * kRows * 4;     // SegDesc [kSlots]
   static constexpr uint32_t oBar = oSeg + kSlots * sizeof(SegDesc);   // full, empty, seg_full, seg_empty
   static constexpr uint32_t oMisc = oBar + (2 * kStages + 2 * kSlots) * 8;   // bad flags, scratch [32], sequence of a token [64]
-  static constexpr uint32_t kTotal = oMisc + (kStages + 32 + 64) * 4 + 1024;
-  static_assert(kStages * kBuf >= kMaxBatch * 4, "the counts use the ring before the first copy");
+  static constexpr uint32_t oCum = oMisc + (kStages + 32 + 64) * 4;   // own units before each sequence
+  static constexpr uint32_t kTotal = oCum + kMaxBatch * 4 + 1024;
   static_assert(kRowsPerSm * (kTotal + 1024) <= 228 * 1024, "resident CTAs");
 };
 
@@ -579,7 +608,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
   volatile int* bad_stage = reinterpret_cast<volatile int*>(smem + SM::oMisc);
   uint32_t* scratch = reinterpret_cast<uint32_t*>(smem + SM::oMisc) + SM::kStages;
   int* token_seq = reinterpret_cast<int*>(scratch + 32);
-  uint32_t* cum = reinterpret_cast<uint32_t*>(smem);
+  uint32_t* cum = reinterpret_cast<uint32_t*>(smem + SM::oCum);
   const PrefixAttnArgs& a = w.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -596,14 +625,23 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
     tma_prefetch(&tm);
   }
   if (tid < 64) token_seq[tid] = -1;
+  // A CTA that starts when tile_kernel's are done leaves if those that started with them have at most one range each
+  // to go: its own start takes longer (64 sequences behind 8192 positions: 39.5 us, 37.7 so).  Those never leave,
+  // so every range is taken whatever the two words say.
+  if (w.queue && tid == 0) {
+    const uint32_t early = __ldcg(w.queue + 1), taken = __ldcg(w.queue);
+    scratch[31] = blockIdx.x >= early && early > 0 ? taken + early : 0;
+  }
   __syncthreads();
   if (w.first) griddep_wait();
+  const uint32_t enough = w.queue ? scratch[31] : 0;   // the counts use the first words
   Walker<SM::kRows, kRowsTile, kRowsSegCost> wk(w);
   const uint32_t total = count_units<kRowsThreads>(wk, cum, scratch, w.do_prefix ? token_seq : nullptr);
-  const Share sh(total, gridDim.x, kRowsMinUnits);
-  const bool work = blockIdx.x < sh.ctas;
-  const uint32_t g0 = work ? sh.begin(blockIdx.x) : 0, g1 = work ? sh.begin(blockIdx.x + 1) : 0;
-  fence_proxy_async_smem();   // the counts in the ring are written before its first copy
+  const Share sh(total, w.queue ? kRowsQueue * gridDim.x : gridDim.x, kRowsMinUnits);
+  if (w.queue && enough >= sh.ctas) {
+    griddep_wait();
+    return;
+  }
   __syncthreads();
   griddep_launch_dependents();
   const int n_slots = w.slots;   // 64 / (rows of the call's largest segment), at most kSlots
@@ -615,12 +653,37 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
     ld.kv = &a.kv;
     ld.lane = lane;
     uint32_t n_ld = 0, n_seg = 0, phase = 0;
-    int st = 0, off = work ? wk.find(g0, cum) : 0;
+    int st = 0;
     bool ok = true;
-    fence_proxy_async_smem();   // the counts in the ring are read before its first copy
-    for (uint32_t g = g0; g < g1 && ok; ++n_seg) {
+    auto claim = [&] {   // the next range
+      uint32_t r = 0;
+      if (lane == 0) r = atomicAdd(w.queue, 1u);
+      return __shfl_sync(0xffffffffu, r, 0);
+    };
+    auto slot_free = [&](int slot) {
+      if (n_seg >= static_cast<uint32_t>(n_slots) && !pipe_wait(&seg_empty[slot], (n_seg / n_slots - 1) & 1u)) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+      return ok;
+    };
+    uint32_t g = 0, g1 = 0, range = 0;
+    int off = 0;
+    auto start_range = [&](uint32_t r) {
+      range = r;
+      if (r >= sh.ctas) return false;
+      g = sh.begin(r);
+      g1 = sh.begin(r + 1);
+      off = wk.find(g, cum);
+      return true;
+    };
+    bool more = start_range(w.queue ? claim() : blockIdx.x);
+    for (; more && ok; ++n_seg) {
       const Piece pc = wk.piece(off, g1 - g);
-      if (pc.cnt == 0) break;   // only at the end of the range
+      if (pc.cnt == 0) {   // only at the end of the range
+        if (!w.queue) break;
+        more = start_range(claim());
+        --n_seg;
+        continue;
+      }
       // the segment's description, row table and query rows
       const int slot = static_cast<int>(n_seg % n_slots), row0 = slot * (SM::kQRows / n_slots);
       // its first page ids are on their way meanwhile
@@ -628,11 +691,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
       int first0 = 0;
       const int n0 = ld.boxes((wk.k.t0 + pc.tile) * kRowsTile, wk.k.lo, wk.k.hi, first0);
       ld.prefetch(first0, n0);
-      if (n_seg >= static_cast<uint32_t>(n_slots) &&
-          !pipe_wait(&seg_empty[slot], (n_seg / n_slots - 1) & 1u))
-        ok = false;
-      ok = __all_sync(0xffffffffu, ok);
-      if (ok) {
+      if (slot_free(slot)) {
         int t = 0, h = 0;   // a row per lane
         if (lane < wk.rows) {
           wk.row_of(lane, t, h);
@@ -653,9 +712,9 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
           d[0] = make_int4(wk.rows, (wk.rows + kRowsUnit - 1) / kRowsUnit, wk.k.lo, wk.k.hi);
           d[1] = make_int4((wk.k.t0 + pc.tile) * kRowsTile, pc.cnt, wk.kvh,
                            (wk.prefix ? kSegPrefix : 0) | (pc.starts ? kSegStarts : 0) | (pc.ends ? kSegEnds : 0) |
-                               (!wk.prefix && wk.s.bad ? kSegBad : 0) | (g1 - g - pc.units <= kRowsSegCost ? kSegLast : 0));
-          d[2] = make_int4(wk.prefix ? wk.seg : wk.own_info_index(),
-                           pc.starts ? sh.owner(g - static_cast<uint32_t>(off) + wk.units(wk.k.nt) - 1) : 0, 0, 0);
+                               (!wk.prefix && wk.s.bad ? kSegBad : 0) | (!w.queue && g1 - g - pc.units <= kRowsSegCost ? kSegLast : 0));
+          d[2] = make_int4(wk.prefix ? wk.seg : wk.own_info_index(), range,
+                           pc.starts ? sh.owner(g - static_cast<uint32_t>(off) + wk.units(wk.k.nt) - 1) : 0, 0);
           mbar_arrive_expect_tx(&seg_full[slot], static_cast<uint32_t>(wk.rows * HD * 2));
         }
         __syncwarp();
@@ -698,8 +757,19 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
         n_ld += 2;
       }
       g += pc.units;
-      if (g < g1) wk.next();
-      off = 0;
+      if (g < g1) {
+        wk.next();
+        off = 0;
+      } else {
+        more = w.queue && start_range(claim());
+      }
+    }
+    if (w.queue && slot_free(static_cast<int>(n_seg % n_slots))) {   // nothing more
+      const int slot = static_cast<int>(n_seg++ % n_slots);
+      if (lane == 0) {
+        reinterpret_cast<SegDesc*>(smem + SM::oSeg)[slot].cnt = 0;
+        mbar_arrive(&seg_full[slot]);
+      }
     }
     if (!ok) {   // let the copies in flight land before the CTA goes
       if (lane == 0 && a.status) atomicOr(a.status, DEX_ATTN_TIMEOUT);
@@ -725,11 +795,12 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
         ok = false;
       }
     };
-    for (bool more = work; more; ++n_seg) {
+    for (bool more = w.queue || blockIdx.x < sh.ctas; more; ++n_seg) {
       const int slot = static_cast<int>(n_seg % n_slots), row0 = slot * (SM::kQRows / n_slots);
       wait(&seg_full[slot], n_seg / n_slots);
       if (!named_bar_and(1, kRowsWarps * 32, ok)) break;   // all four warps or none: they meet at barriers
       const SegDesc d = reinterpret_cast<const SegDesc*>(smem + SM::oSeg)[slot];
+      if (d.cnt == 0) break;
       const RowDesc* rd = reinterpret_cast<const RowDesc*>(smem + SM::oRow) + row0;
       const uint32_t sq = smem_u32(smem + SM::oQ) + row0 * SM::kQRow;
       uint32_t qf[MT == 1 ? HD / 16 : 1][4];   // one row tile's queries stay in registers
@@ -914,7 +985,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
           } else {
             const PartRef p = whole ? joined_part<HD>(prefix ? w.pre_o : w.own_o, prefix ? w.pre_ml : w.own_ml, d.kvh, rows_all,
                                                       t * a.G + hg)
-                                    : slot_part<HD>(w.part_o, w.part_ml, 2 * blockIdx.x + (starts ? 1 : 0), SM::kRows, r);
+                                    : slot_part<HD>(w.part_o, w.part_ml, 2 * d.range + (starts ? 1 : 0), SM::kRows, r);
 #pragma unroll
             for (int n = 0; n < NV; ++n)
               *reinterpret_cast<float2*>(p.o + static_cast<int64_t>((dim + n * 8) >> 2) * p.step + (tq & 1) * 2) =
@@ -923,7 +994,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
           }
         }
       }
-      if (starts && tid == 0) (prefix ? w.pre_info : w.own_info)[d.info] = make_int2(blockIdx.x, d.last_cta);
+      if (starts && tid == 0) (prefix ? w.pre_info : w.own_info)[d.info] = make_int2(d.range, d.last_range);
       more = !(d.flags & kSegLast);
       __syncwarp();
       if (lane == 0) mbar_arrive(&seg_empty[slot]);
@@ -1096,7 +1167,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (w.first) griddep_wait();
   Walker<kTileRows, kTileKeys, kTileSegCost> wk(w);
   const uint32_t total = count_units<kTileThreads>(wk, cum, scratch);
-  const Share sh(total, gridDim.x, kTileMinUnits);
+  uint32_t ctas = gridDim.x;
+  if (w.behind_rt) {   // the other SMs go to rows_kernel at once
+    const float mine = kTileWeight * static_cast<float>(total), other = static_cast<float>(units_behind<kTileThreads>(w, scratch));
+    ctas = max(static_cast<uint32_t>(ceilf(static_cast<float>(ctas) * (mine / (mine + other)))), 1u);
+  }
+  const Share sh(total, ctas, kTileMinUnits);
+  // rows_kernel cannot start before every CTA here has allowed it, which this one does after the fence; it reads
+  // both words from L2
+  if (w.queue && blockIdx.x == 0 && tid == 0) {
+    w.queue[0] = 0;
+    w.queue[1] = kRowsPerSm * (gridDim.x - sh.ctas);
+    __threadfence();
+  }
   const bool work = blockIdx.x < sh.ctas;
   const uint32_t g0 = work ? sh.begin(blockIdx.x) : 0, g1 = work ? sh.begin(blockIdx.x + 1) : 0;
   int off = work ? wk.find(g0, cum) : 0;
@@ -1602,11 +1685,11 @@ __global__ void __launch_bounds__(DIMS * 2 * SPLIT) combine_kernel(const __grid_
   const SeqRef s = seq_ref(a, max(b, 0));
   const int r = rg - s.q0 * a.G, rt = b >= 0 ? r / w.own_rt : 0, r1 = min((rt + 1) * w.own_rt, s.n * a.G);
   griddep_wait();
-  // this row's parts: prefix parts of CTAs pre_c0 .., then own parts of CTAs own_c0 ..  A kernel that gave up
+  // this row's parts: prefix parts of ranges pre_c0 .., then own parts of ranges own_c0 ..  A kernel that gave up
   // waiting leaves entries that hold anything: none of them is followed.
   auto parts_of = [](int2 info, int rt) {
-    const int ctas = rt == kTileRows ? kSms : kRowsPerSm * kSms;
-    return info.x >= 0 && info.x <= info.y && info.y < ctas ? info.y - info.x + 1 : 0;
+    const int ranges = rt == kTileRows ? kSms : kRowsQueue * kRowsPerSm * kSms;
+    return info.x >= 0 && info.x <= info.y && info.y < ranges ? info.y - info.x + 1 : 0;
   };
   int pre_c0 = 0, n_pre = 0, own_c0 = 0, n_own = 0;
   if (b >= 0) {
@@ -1713,7 +1796,9 @@ struct Plan {
   bool share, prefix_tile, own_tile;   // prefix / own segments on tile_kernel
   int rows_mt;                         // row tiles of rows_kernel: 1 or 2 (0: it has nothing to do)
   int slots;
-  size_t o_rows_part, o_rows_ml, o_tile_part, o_tile_ml, o_pre, o_pre_ml, o_own, o_own_ml, o_pre_info, o_own_info, total;
+  bool queue() const { return prefix_tile && !own_tile; }   // rows_kernel behind tile_kernel
+  int rows_ranges() const { return (queue() ? kRowsQueue : 1) * kRowsPerSm * kSms; }
+  size_t o_queue, o_rows_part, o_rows_ml, o_tile_part, o_tile_ml, o_pre, o_pre_ml, o_own, o_own_ml, o_pre_info, o_own_info, total;
   int own_rt() const { return own_tile ? kTileRows : rows_mt * kRowsUnit; }
   int pre_rt() const { return prefix_tile ? kTileRows : rows_mt * kRowsUnit; }
 };
@@ -1742,8 +1827,9 @@ Plan make_plan(const PrefixAttnArgs& a) {
   };
   const size_t hd4 = static_cast<size_t>(a.kv.hd) * 4;
   if (p.rows_mt) {
-    p.o_rows_part = take(size_t(2) * kRowsPerSm * kSms * p.rows_mt * kRowsUnit * hd4);
-    p.o_rows_ml = take(size_t(2) * kRowsPerSm * kSms * p.rows_mt * kRowsUnit * 8);
+    if (p.queue()) p.o_queue = take(2 * sizeof(uint32_t));
+    p.o_rows_part = take(size_t(2) * p.rows_ranges() * p.rows_mt * kRowsUnit * hd4);
+    p.o_rows_ml = take(size_t(2) * p.rows_ranges() * p.rows_mt * kRowsUnit * 8);
   }
   if (p.own_tile || p.prefix_tile) {
     p.o_tile_part = take(size_t(2) * kSms * kTileRows * hd4);
@@ -1815,6 +1901,7 @@ cudaError_t launch_hd(const PrefixAttnArgs& a, const Plan& p, uint8_t* ws, cudaS
   base.own_ml = reinterpret_cast<float2*>(ws + p.o_own_ml);
   base.pre_info = reinterpret_cast<int2*>(ws + p.o_pre_info);
   base.own_info = reinterpret_cast<int2*>(ws + p.o_own_info);
+  if (p.queue()) base.queue = reinterpret_cast<uint32_t*>(ws + p.o_queue);
   SegWork rows = base, tile = base;
   rows.part_o = reinterpret_cast<float*>(ws + p.o_rows_part);
   rows.part_ml = reinterpret_cast<float2*>(ws + p.o_rows_ml);
@@ -1826,6 +1913,7 @@ cudaError_t launch_hd(const PrefixAttnArgs& a, const Plan& p, uint8_t* ws, cudaS
   tile.do_own = p.own_tile;
   tile.do_prefix = p.prefix_tile;
   tile.first = 1;
+  tile.behind_rt = p.queue() ? p.own_rt() : 0;
   rows.first = !(tile.do_own || tile.do_prefix);
   const int page = 1 << a.kv.page_shift;
   const int sms = n_sm < kSms ? n_sm : kSms;

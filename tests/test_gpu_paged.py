@@ -229,6 +229,18 @@ def test_attention_large_batch(prefix):
     run_case(8, 2, 64, 64, FP, lens, new, prefix)
 
 
+@pytest.mark.parametrize("H,kvh,hd,dtype", [(32, 8, 128, BF), (8, 4, 64, FP)])
+@pytest.mark.parametrize("batch,longest", [(20, 30), (60, 700), (200, 90), (77, 1)])
+def test_attention_prefix_beside_tails(H, kvh, hd, dtype, batch, longest):
+    """The prefix of many sequences next to their own ragged positions: few of them, some very long, none but the
+    queries' own."""
+    g = torch.Generator().manual_seed(batch)
+    new = [int(x) for x in torch.randint(0, 3, (batch,), generator=g)]
+    new[0] = 1
+    tails = torch.randint(0, longest, (batch,), generator=g)
+    run_case(H, kvh, hd, 32, dtype, [300 + int(t) + n for t, n in zip(tails, new)], new, prefix=300)
+
+
 def test_attention_strides():
     """Queries that are one expanded row, an output inside a larger tensor, a table inside a wider one, tokens
     before the first sequence's."""
