@@ -57,7 +57,9 @@ constexpr int kRowsMinUnits = 3, kTileMinUnits = 5;
 // Where tile_kernel computes the prefix and rows_kernel the rest, they run side by side: tile_kernel takes SMs in
 // proportion to the work, a unit of it counted as kTileWeight of rows_kernel's, and rows_kernel's CTAs, those on
 // the other SMs from the start and those that follow on its SMs, take kRowsQueue ranges each on average from a
-// queue.  64 sequences behind 8192 positions and 256 behind 32768: 37.7 and 144.8 us; weight 4 41.5 and 149.7, 6
+// queue.  Where rows_kernel computes both, its CTAs take two ranges in turn, so that each has prefix segments, whose
+// tiles cost more, and own ones: 32 sequences of 32 heads behind 4096 positions 40.2 us, with one range 42.2, with
+// three 41.9.  64 sequences behind 8192 positions and 256 behind 32768: 37.7 and 144.8 us; weight 4 41.5 and 149.7, 6
 // 39.2 and 146.9; with a fixed range per CTA and all SMs for tile_kernel first 44.7 and 151.9; four ranges per CTA
 // 40.9 and 145.3, one 40.6 and 156.
 constexpr float kTileWeight = 5.0f;
@@ -87,6 +89,7 @@ struct SegWork {
   int32_t do_own;       // this kernel computes the own segments
   int32_t joined;       // 1: rows have prefix and own parts, so a finished segment is not yet the output
   int32_t slots;        // rows_kernel: segments posted ahead
+  int32_t per_cta;      // rows_kernel: ranges per CTA, at most
   int32_t behind_rt;    // tile_kernel: rows per segment of the rows_kernel behind it (it computes the own segments), or 0
   uint32_t* queue;      // rows_kernel behind tile_kernel, which sets them: next range to take, CTAs that start beside
                         // it; or null: CTA i takes range i
@@ -637,7 +640,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
   const uint32_t enough = w.queue ? scratch[31] : 0;   // the counts use the first words
   Walker<SM::kRows, kRowsTile, kRowsSegCost> wk(w);
   const uint32_t total = count_units<kRowsThreads>(wk, cum, scratch, w.do_prefix ? token_seq : nullptr);
-  const Share sh(total, w.queue ? kRowsQueue * gridDim.x : gridDim.x, kRowsMinUnits);
+  const Share sh(total, static_cast<uint32_t>(w.per_cta) * gridDim.x, kRowsMinUnits);
   if (w.queue && enough >= sh.ctas) {
     griddep_wait();
     return;
@@ -655,7 +658,9 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
     uint32_t n_ld = 0, n_seg = 0, phase = 0;
     int st = 0;
     bool ok = true;
+    uint32_t g = 0, g1 = 0, range = 0;
     auto claim = [&] {   // the next range
+      if (!w.queue) return range + gridDim.x;
       uint32_t r = 0;
       if (lane == 0) r = atomicAdd(w.queue, 1u);
       return __shfl_sync(0xffffffffu, r, 0);
@@ -665,7 +670,6 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
       ok = __all_sync(0xffffffffu, ok);
       return ok;
     };
-    uint32_t g = 0, g1 = 0, range = 0;
     int off = 0;
     auto start_range = [&](uint32_t r) {
       range = r;
@@ -679,7 +683,6 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
     for (; more && ok; ++n_seg) {
       const Piece pc = wk.piece(off, g1 - g);
       if (pc.cnt == 0) {   // only at the end of the range
-        if (!w.queue) break;
         more = start_range(claim());
         --n_seg;
         continue;
@@ -712,7 +715,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
           d[0] = make_int4(wk.rows, (wk.rows + kRowsUnit - 1) / kRowsUnit, wk.k.lo, wk.k.hi);
           d[1] = make_int4((wk.k.t0 + pc.tile) * kRowsTile, pc.cnt, wk.kvh,
                            (wk.prefix ? kSegPrefix : 0) | (pc.starts ? kSegStarts : 0) | (pc.ends ? kSegEnds : 0) |
-                               (!wk.prefix && wk.s.bad ? kSegBad : 0) | (!w.queue && g1 - g - pc.units <= kRowsSegCost ? kSegLast : 0));
+                               (!wk.prefix && wk.s.bad ? kSegBad : 0) | (!w.queue && range + gridDim.x >= sh.ctas && g1 - g - pc.units <= kRowsSegCost ? kSegLast : 0));
           d[2] = make_int4(wk.prefix ? wk.seg : wk.own_info_index(), range,
                            pc.starts ? sh.owner(g - static_cast<uint32_t>(off) + wk.units(wk.k.nt) - 1) : 0, 0);
           mbar_arrive_expect_tx(&seg_full[slot], static_cast<uint32_t>(wk.rows * HD * 2));
@@ -761,7 +764,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
         wk.next();
         off = 0;
       } else {
-        more = w.queue && start_range(claim());
+        more = start_range(claim());
       }
     }
     if (w.queue && slot_free(static_cast<int>(n_seg % n_slots))) {   // nothing more
@@ -1684,6 +1687,10 @@ __global__ void __launch_bounds__(DIMS * 2 * SPLIT) combine_kernel(const __grid_
   const int b = row_seq[li];
   const SeqRef s = seq_ref(a, max(b, 0));
   const int r = rg - s.q0 * a.G, rt = b >= 0 ? r / w.own_rt : 0, r1 = min((rt + 1) * w.own_rt, s.n * a.G);
+  const int pre_r = w.share ? rg % w.pre_rt : 0, own_r = r - rt * w.own_rt;   // row within its segments
+  const int nt = w.own_tile == kRowsTile ? own_range<kRowsTile>(w.own, s, r1).nt : own_range<kTileKeys>(w.own, s, r1).nt;
+  const int2* pre_at = b >= 0 && w.share ? w.pre.pre_info + rg / w.pre_rt * a.kv.KVH + kvh : nullptr;
+  const int2* own_at = b >= 0 && nt > 0 ? w.own.own_info + own_info_of(a, w.own_rt, s.q0, b, rt, kvh) : nullptr;
   griddep_wait();
   // this row's parts: prefix parts of ranges pre_c0 .., then own parts of ranges own_c0 ..  A kernel that gave up
   // waiting leaves entries that hold anything: none of them is followed.
@@ -1691,21 +1698,10 @@ __global__ void __launch_bounds__(DIMS * 2 * SPLIT) combine_kernel(const __grid_
     const int ranges = rt == kTileRows ? kSms : kRowsQueue * kRowsPerSm * kSms;
     return info.x >= 0 && info.x <= info.y && info.y < ranges ? info.y - info.x + 1 : 0;
   };
-  int pre_c0 = 0, n_pre = 0, own_c0 = 0, n_own = 0;
-  if (b >= 0) {
-    if (w.share) {
-      const int2 info = __ldcg(w.pre.pre_info + rg / w.pre_rt * a.kv.KVH + kvh);
-      pre_c0 = info.x;
-      n_pre = parts_of(info, w.pre_rt);
-    }
-    const int nt = w.own_tile == kRowsTile ? own_range<kRowsTile>(w.own, s, r1).nt : own_range<kTileKeys>(w.own, s, r1).nt;
-    if (nt > 0) {
-      const int2 info = __ldcg(w.own.own_info + own_info_of(a, w.own_rt, s.q0, b, rt, kvh));
-      own_c0 = info.x;
-      n_own = parts_of(info, w.own_rt);
-      if (n_own == 1 && !w.share) n_own = 0;   // written where it was computed
-    }
-  }
+  const int2 pre_info = pre_at ? __ldcg(pre_at) : make_int2(0, -1), own_info = own_at ? __ldcg(own_at) : make_int2(0, -1);
+  const int pre_c0 = pre_info.x, n_pre = parts_of(pre_info, w.pre_rt), own_c0 = own_info.x;
+  int n_own = parts_of(own_info, w.own_rt);
+  if (n_own == 1 && !w.share) n_own = 0;   // written where it was computed
   const int n = n_pre + n_own;
   if (__all_sync(0xffffffffu, n <= 0)) return;   // the same in all warps
   float M = -INFINITY, L = 0.0f;
@@ -1728,7 +1724,7 @@ __global__ void __launch_bounds__(DIMS * 2 * SPLIT) combine_kernel(const __grid_
         const PartRef p = (pre ? n_pre : n_own) == 1
                               ? joined_part<HD>(pre ? sw.pre_o : sw.own_o, pre ? sw.pre_ml : sw.own_ml, kvh, rows_all, rg)
                               : slot_part<HD>(sw.part_o, sw.part_ml, 2 * ((pre ? pre_c0 : own_c0) + i) + (i == 0 ? 1 : 0), rows,
-                                              pre ? rg % rows : r - rt * rows);
+                                              pre ? pre_r : own_r);
         ml[u] = __ldcg(p.ml);
 #pragma unroll
         for (int q = 0; q < 4; ++q) x[u][q] = __ldcg(reinterpret_cast<const float4*>(p.o + (warp * 4 + q) * p.step));
@@ -1797,7 +1793,8 @@ struct Plan {
   int rows_mt;                         // row tiles of rows_kernel: 1 or 2 (0: it has nothing to do)
   int slots;
   bool queue() const { return prefix_tile && !own_tile; }   // rows_kernel behind tile_kernel
-  int rows_ranges() const { return (queue() ? kRowsQueue : 1) * kRowsPerSm * kSms; }
+  int rows_per_cta() const { return queue() || (share && !prefix_tile) ? kRowsQueue : 1; }
+  int rows_ranges() const { return rows_per_cta() * kRowsPerSm * kSms; }
   size_t o_queue, o_rows_part, o_rows_ml, o_tile_part, o_tile_ml, o_pre, o_pre_ml, o_own, o_own_ml, o_pre_info, o_own_info, total;
   int own_rt() const { return own_tile ? kTileRows : rows_mt * kRowsUnit; }
   int pre_rt() const { return prefix_tile ? kTileRows : rows_mt * kRowsUnit; }
@@ -1906,6 +1903,7 @@ cudaError_t launch_hd(const PrefixAttnArgs& a, const Plan& p, uint8_t* ws, cudaS
   rows.part_o = reinterpret_cast<float*>(ws + p.o_rows_part);
   rows.part_ml = reinterpret_cast<float2*>(ws + p.o_rows_ml);
   rows.slots = p.slots;
+  rows.per_cta = p.rows_per_cta();
   rows.do_own = !p.own_tile;
   rows.do_prefix = p.share && !p.prefix_tile;
   tile.part_o = reinterpret_cast<float*>(ws + p.o_tile_part);
@@ -1949,11 +1947,13 @@ cudaError_t launch_hd(const PrefixAttnArgs& a, const Plan& p, uint8_t* ws, cudaS
     const unsigned groups = static_cast<unsigned>((a.n_tokens * a.G + (1 << c.row_bits) - 1) >> c.row_bits);
     const dim3 grid(groups, static_cast<unsigned>(a.kv.KVH));
     // The fewer blocks there are, the more warps share a row's parts and head dims.  Whole calls, us: 1 block
-    // of parts per K/V head and 8 K/V heads 85.9 with eight groups, 88.5 with two; 64 blocks 45.6 and 45.2; 160
-    // blocks 43.7, 32.5 and 34.4 with one group; 1752 blocks 215 with two, 208 with one.
+    // of parts per K/V head and 8 K/V heads 85.4 with eight groups, 86.5 with four; 64 blocks 36.9 with four, 38.0
+    // with two; 160 blocks 32.5 with two, 34.4 with one; 256 blocks 146.9 with four, 144.7 with two; 1752 blocks
+    // 215 with two, 208 with one.
     const unsigned blocks = groups * static_cast<unsigned>(a.kv.KVH);
     const dim3 split(groups, static_cast<unsigned>(a.kv.KVH), HD / 32);
     if (blocks < 64) e = launch(combine_kernel<T, HD, 32, 8>, split, 512, 0, st, true, c);
+    else if (blocks < 128) e = launch(combine_kernel<T, HD, 32, 4>, split, 256, 0, st, true, c);
     else if (blocks < 4u * sms) e = launch(combine_kernel<T, HD, 32, 2>, split, 128, 0, st, true, c);
     else e = launch(combine_kernel<T, HD, HD, 1>, grid, HD * 2, 0, st, true, c);
   }
