@@ -48,22 +48,27 @@ constexpr int kRowsPerSm = 2;     // resident CTAs
 constexpr int kSms = 152;         // of the sm_103 part: workspace sizes and grids, whatever device is current
 constexpr int kTileKeys = 128;    // keys of a tile of tile_kernel
 constexpr int kTileRows = 256;    // its query rows (two tiles of 128)
-// What a segment costs a CTA beside its key tiles, in tiles (queries, start and end of its pipeline, result), and the
-// units (tiles and these) of a CTA, at least.  With no cost 64 sequences behind 8192 positions take 60 us instead
-// of 46 (some CTAs get seven segments of one tile), 32 of 32 heads 45.5 instead of 42; with two tiles in
-// rows_kernel the latter 46; with two instead of four in tile_kernel 256 sequences behind 32768 162 instead of 158.
-constexpr int kRowsSegCost = 1, kTileSegCost = 4;
-constexpr int kRowsMinUnits = 3, kTileMinUnits = 5;
+// What a segment costs a CTA beside its key tiles, in tiles (queries, start and end of its pipeline, result);
+// kTileHalfCost where the teams of tile_kernel share its rows.  With no cost 64 sequences behind 8192 positions take
+// 60 us instead of 46 (some CTAs get seven segments of one tile), 32 of 32 heads 45.5 instead of 42; with two tiles
+// in rows_kernel the latter 46; with two instead of four in tile_kernel 256 sequences behind 32768 162 instead of
+// 158; with four for half segments too 16 lattices behind 4096 31.1 instead of 28.6, with one 34.7.
+constexpr int kRowsSegCost = 1, kTileSegCost = 4, kTileHalfCost = 2;
+// Units (tiles and these costs) of a range, at least.  Few long ranges leave SMs idle: 8 tokens behind 2048 positions
+// take 12.9 us with two units, 14.3 with three; 13 sequences behind 777 (tile_kernel) 13.2 with one, 15.0 with
+// three.  Two units of rows_kernel hold a tile.
+constexpr int kRowsMinUnits = kRowsSegCost + 1, kTileMinUnits = 1;
 // Where tile_kernel computes the prefix and rows_kernel the rest, they run side by side: tile_kernel takes SMs in
 // proportion to the work, a unit of it counted as kTileWeight of rows_kernel's, and rows_kernel's CTAs, those on
 // the other SMs from the start and those that follow on its SMs, take kRowsQueue ranges each on average from a
 // queue.  Where rows_kernel computes both, its CTAs take two ranges in turn, so that each has prefix segments, whose
-// tiles cost more, and own ones: 32 sequences of 32 heads behind 4096 positions 40.2 us, with one range 42.2, with
+// tiles cost more, and own ones, if they are kRowsTwo units or more together: 32 sequences of 32 heads behind 4096 positions 40.2 us, with one range 42.2, with
 // three 41.9.  64 sequences behind 8192 positions and 256 behind 32768: 37.7 and 144.8 us; weight 4 41.5 and 149.7, 6
 // 39.2 and 146.9; with a fixed range per CTA and all SMs for tile_kernel first 44.7 and 151.9; four ranges per CTA
 // 40.9 and 145.3, one 40.6 and 156.
 constexpr float kTileWeight = 5.0f;
 constexpr int kRowsQueue = 2;
+constexpr uint32_t kRowsTwo = 8;
 constexpr int kMaxBatch = 1024;
 
 // Division by a number fixed for the call: n / d for 0 <= n < 2^31 (multiply, add, shift).
@@ -198,10 +203,10 @@ struct Piece {
 template <int RT, int TILE, int COST>
 struct Walker {
   const SegWork& w;
-  int n_pre, pre_nt;       // prefix segments of this kernel and their tiles
+  int n_pre, pre_nt, pre_cost;   // prefix segments of this kernel, their tiles and cost
   // current segment
   bool prefix;
-  int seg, b, rt, kvh, rows, r0;   // seg: prefix segment index; r0: first row within the sequence / batch
+  int seg, b, rt, kvh, rows, r0, cost;   // seg: prefix segment index; r0: first row within the sequence / batch
   SeqRef s;
   KeyRange k;
 
@@ -209,22 +214,28 @@ struct Walker {
     const int pre_rows = w.a.n_tokens * w.a.G;
     n_pre = w.do_prefix ? (pre_rows + RT - 1) / RT * w.a.kv.KVH : 0;
     pre_nt = (w.a.prefix_len + TILE - 1) / TILE;
+    pre_cost = cost_of(pre_rows);
   }
-  __device__ __forceinline__ static uint32_t units(int nt) { return nt > 0 ? static_cast<uint32_t>(nt + COST) : 0u; }
-  __device__ __forceinline__ uint32_t pre_units() const { return static_cast<uint32_t>(n_pre) * units(pre_nt); }
+  __device__ __forceinline__ static int cost_of(int rows) { return RT == kTileRows && rows <= kTileRows / 2 ? kTileHalfCost : COST; }
+  __device__ __forceinline__ static uint32_t units(int nt, int cost) { return nt > 0 ? static_cast<uint32_t>(nt + cost) : 0u; }
+  __device__ __forceinline__ uint32_t units() const { return units(k.nt, cost); }
+  __device__ __forceinline__ uint32_t pre_units() const { return static_cast<uint32_t>(n_pre) * units(pre_nt, pre_cost); }
   // units of one K/V head over the row tiles of sequence b
   __device__ __forceinline__ uint32_t seq_units(const SeqRef& q) const {
     if (!q.valid) return 0;
     uint32_t n = 0;
-    for (int r = 0; r < q.n * w.a.G; r += RT) n += units(own_range<TILE>(w, q, min(r + RT, q.n * w.a.G)).nt);
+    for (int r = 0; r < q.n * w.a.G; r += RT) {
+      const int end = min(r + RT, q.n * w.a.G);
+      n += units(own_range<TILE>(w, q, end).nt, cost_of(end - r));
+    }
     return n;
   }
   // The part of the segment from unit `off` on that `left` more units cover.
   __device__ __forceinline__ Piece piece(int off, uint32_t left) const {
     Piece p;
-    p.units = min(units(k.nt) - static_cast<uint32_t>(off), left);
-    p.tile = max(off - COST, 0);
-    p.cnt = max(off + static_cast<int>(p.units) - COST, 0) - p.tile;
+    p.units = min(units() - static_cast<uint32_t>(off), left);
+    p.tile = max(off - cost, 0);
+    p.cnt = max(off + static_cast<int>(p.units) - cost, 0) - p.tile;
     p.starts = p.tile == 0;
     p.ends = p.tile + p.cnt == k.nt;
     return p;
@@ -237,18 +248,20 @@ struct Walker {
     r0 = rt * RT;
     rows = min(RT, w.a.n_tokens * w.a.G - r0);
     k = KeyRange{0, w.a.prefix_len, 0, pre_nt};
+    cost = pre_cost;
   }
   __device__ __forceinline__ void set_own() {
     prefix = false;
     r0 = rt * RT;
     rows = min(RT, s.n * w.a.G - r0);
     k = own_range<TILE>(w, s, max(r0 + rows, 1));
+    cost = cost_of(rows);
   }
   // Segment of unit g (cum[b]: own units of all K/V heads before sequence b); returns the unit within it.
   __device__ __forceinline__ int find(uint32_t g, const uint32_t* cum) {
     if (g < pre_units()) {
-      set_prefix(static_cast<int>(g / units(pre_nt)));
-      return static_cast<int>(g % units(pre_nt));
+      set_prefix(static_cast<int>(g / units(pre_nt, pre_cost)));
+      return static_cast<int>(g % units());
     }
     g -= pre_units();
     int lo = 0, hi = w.a.kv.batch - 1;
@@ -262,11 +275,11 @@ struct Walker {
     s = seq_ref(w.a, b);
     for (rt = 0;; ++rt) {
       set_own();
-      const uint32_t cnt = units(k.nt) * static_cast<uint32_t>(w.a.kv.KVH);
+      const uint32_t cnt = units() * static_cast<uint32_t>(w.a.kv.KVH);
       if (g < cnt || (rt + 1) * RT >= s.n * w.a.G) break;
       g -= cnt;
     }
-    const uint32_t each = max(units(k.nt), 1u);
+    const uint32_t each = max(units(), 1u);
     kvh = min(static_cast<int>(g / each), w.a.kv.KVH - 1);
     return static_cast<int>(g % each);
   }
@@ -640,7 +653,8 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
   const uint32_t enough = w.queue ? scratch[31] : 0;   // the counts use the first words
   Walker<SM::kRows, kRowsTile, kRowsSegCost> wk(w);
   const uint32_t total = count_units<kRowsThreads>(wk, cum, scratch, w.do_prefix ? token_seq : nullptr);
-  const Share sh(total, static_cast<uint32_t>(w.per_cta) * gridDim.x, kRowsMinUnits);
+  const uint32_t per_cta = w.queue || total >= kRowsTwo * gridDim.x ? static_cast<uint32_t>(w.per_cta) : 1u;
+  const Share sh(total, per_cta * gridDim.x, kRowsMinUnits);
   if (w.queue && enough >= sh.ctas) {
     griddep_wait();
     return;
@@ -717,7 +731,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
                            (wk.prefix ? kSegPrefix : 0) | (pc.starts ? kSegStarts : 0) | (pc.ends ? kSegEnds : 0) |
                                (!wk.prefix && wk.s.bad ? kSegBad : 0) | (!w.queue && range + gridDim.x >= sh.ctas && g1 - g - pc.units <= kRowsSegCost ? kSegLast : 0));
           d[2] = make_int4(wk.prefix ? wk.seg : wk.own_info_index(), range,
-                           pc.starts ? sh.owner(g - static_cast<uint32_t>(off) + wk.units(wk.k.nt) - 1) : 0, 0);
+                           pc.starts ? sh.owner(g - static_cast<uint32_t>(off) + wk.units() - 1) : 0, 0);
           mbar_arrive_expect_tx(&seg_full[slot], static_cast<uint32_t>(wk.rows * HD * 2));
         }
         __syncwarp();
@@ -1462,7 +1476,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         if (starts && tid == 0) {
           int2* info = wk.prefix ? w.pre_info + wk.seg : w.own_info + wk.own_info_index();
-          *info = make_int2(blockIdx.x, sh.owner(g - static_cast<uint32_t>(off) + wk.units(wk.k.nt) - 1));
+          *info = make_int2(blockIdx.x, sh.owner(g - static_cast<uint32_t>(off) + wk.units() - 1));
         }
       }
       if (alt) named_bar_sync(2, 256);   // the query tiles may be written again
