@@ -55,7 +55,7 @@ constexpr int kTileRows = 256;    // its query rows (two tiles of 128)
 // 158; with four for half segments too 16 lattices behind 4096 31.1 instead of 28.6, with one 34.7.
 constexpr int kRowsSegCost = 1, kTileSegCost = 4, kTileHalfCost = 2;
 // Units (tiles and these costs) of a range, at least.  Few long ranges leave SMs idle: 8 tokens behind 2048 positions
-// take 12.9 us with two units, 14.3 with three; 13 sequences behind 777 (tile_kernel) 13.2 with one, 15.0 with
+// take 12.9 us with two units, 14.3 with three; 13 sequences behind 777 on tile_kernel 13.2 with one, 15.0 with
 // three.  Two units of rows_kernel hold a tile.
 constexpr int kRowsMinUnits = kRowsSegCost + 1, kTileMinUnits = 1;
 // Where tile_kernel computes the prefix and rows_kernel the rest, they run side by side: tile_kernel takes SMs in
@@ -1814,18 +1814,24 @@ struct Plan {
   int pre_rt() const { return prefix_tile ? kTileRows : rows_mt * kRowsUnit; }
 };
 
-// Which kernel computes what.  Segments of at most 32 rows go to rows_kernel, unless tile_kernel runs
-// for the prefix and there are few of them: a launch less (13 sequences of 4 K/V heads behind 777 positions
-// 20.4 -> 17.9 us).  With 16 rows as the limit, 8 x 8 segments of 32 prefix rows take 23.4 us instead of 14.9,
-// 32 of 32 rows 48.9 instead of 41.8.  The prefix is
-// shared when more than one sequence can have queries (n_tokens > max_q) and it fills a key tile; a
-// sequence whose own rows fill a 128-row tile gains nothing from sharing.
+// Which kernel computes what.  Segments of at most 32 rows go to rows_kernel, unless tile_kernel runs for the prefix
+// and there are few of them: a launch less (14 sequences of 8 K/V heads behind 27032 positions 46.5 -> 41.7 us; for
+// 36 of 8 behind 938 it would be 22.0 -> 28.3).  With 16 rows as the limit, 8 x 8 segments of 32 prefix rows take
+// 23.4 us instead of 14.9, 32 of 32 rows 48.9 instead of 41.8.
+// Sharing costs a join of two parts of every row and mostly a launch, and saves reading the prefix for each sequence.
+// So it is shared when more than one sequence can have queries (n_tokens > max_q) and reading it for all of
+// them would give every CTA of rows_kernel three key tiles: at 624 tiles in all (13 sequences of 4 heads behind 777
+// positions) it takes 13.2 us shared and 12.2 not, at 1188 (9 of 4 behind 2158) 10.4 and 12.6, at 2048 (8 of 8
+// behind 2048) 13.1 and 16.3.  A prefix below two tiles is not (73 positions, 202 sequences of 8 heads: 83 us shared, 70 not), and
+// a sequence whose own rows fill a 128-row tile gains nothing from sharing.
 Plan make_plan(const PrefixAttnArgs& a) {
   Plan p = {};
   const int64_t own_rows = static_cast<int64_t>(a.max_q) * a.G, all_rows = static_cast<int64_t>(a.n_tokens) * a.G;
-  p.share = a.prefix_len >= kRowsTile && a.n_tokens > a.max_q && own_rows < 128;
+  const int64_t readers = a.n_tokens < a.kv.batch ? a.n_tokens : a.kv.batch;
+  p.share = a.prefix_len >= 2 * kRowsTile && a.n_tokens > a.max_q && own_rows < 128 &&
+            readers * a.kv.KVH * (a.prefix_len / kRowsTile) >= 3 * kRowsPerSm * kSms;
   p.prefix_tile = p.share && all_rows > kRowsMax;
-  p.own_tile = own_rows > kRowsMax || (p.prefix_tile && a.kv.batch * a.kv.KVH <= kSms / 2);
+  p.own_tile = own_rows > kRowsMax || (p.prefix_tile && a.kv.batch * a.kv.KVH <= kSms);
   const int64_t most = p.share && !p.prefix_tile ? all_rows : p.own_tile ? 0 : own_rows;   // rows of a rows_kernel segment
   p.rows_mt = most == 0 ? 0 : most <= kRowsUnit ? 1 : kRowsMax / kRowsUnit;
   p.slots = most == 0 ? 1 : static_cast<int>(kRowsSlotRows / ((most + kRowsUnit - 1) / kRowsUnit * kRowsUnit));

@@ -241,6 +241,86 @@ def test_attention_prefix_beside_tails(H, kvh, hd, dtype, batch, longest):
     run_case(H, kvh, hd, 32, dtype, [300 + int(t) + n for t, n in zip(tails, new)], new, prefix=300)
 
 
+# (n_heads, kv_heads, head_dim, page, queries of each sequence, prefix): enough sequences and positions that the prefix
+# is read once for all of them (912 tiles of 64 positions x sequences x K/V heads), by either kernel, next to own
+# positions on either kernel
+SHARED = [(32, 8, 128, 16, [1] * 8, 1000), (4, 4, 64, 64, [2, 1, 0, 1] * 3, 1300), (32, 32, 128, 32, [1] * 5, 450),
+          (32, 8, 128, 64, [1, 3, 0, 2] * 4, 640), (6, 2, 64, 16, [1, 2] * 20, 777), (8, 1, 128, 256, [1, 5, 1] * 15, 1500),
+          (16, 16, 64, 128, [7, 0, 30, 1] * 3, 500), (12, 4, 128, 32, [1] * 70, 260), (30, 2, 128, 16, [2] * 40, 800)]
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("H,kvh,hd,ps,new,prefix", SHARED)
+def test_attention_shared(H, kvh, hd, ps, new, prefix, dtype):
+    g = torch.Generator().manual_seed(prefix)
+    past = torch.randint(0, 150, (len(new),), generator=g)
+    past[1], past[-1] = 0, 400
+    run_case(H, kvh, hd, ps, dtype, [prefix + int(p) + n for p, n in zip(past, new)], new, prefix, pad=2, strided=True)
+
+
+@pytest.mark.parametrize("H,kvh,hd,ps,new,prefix", SHARED)
+def test_attention_shared_tree(H, kvh, hd, ps, new, prefix):
+    g = torch.Generator().manual_seed(prefix + 1)
+    words = []
+    for n in new:
+        word = []
+        for i in range(n):   # ancestors of a random tree; a root that does not see itself now and then
+            parent = int(torch.randint(-1, i, (1,), generator=g)) if i else -1
+            word.append((word[parent] if parent >= 0 else 0) | (1 << i if int(torch.randint(0, 9, (1,), generator=g)) else 0))
+        words += word
+    run_case(H, kvh, hd, ps, FP, [prefix + n + 40 * (n % 2) for n in new], new, prefix,
+             torch.tensor(words, dtype=torch.int64))
+
+
+@pytest.mark.parametrize("H,kvh,hd,ps,new,prefix", SHARED)
+def test_attention_shared_edges(H, kvh, hd, ps, new, prefix):
+    """Sequences that end inside the prefix or before their queries, empty ones, a scale below zero, the prefix by a
+    table of its own."""
+    lens = [prefix + n for n in new]
+    lens[1] = prefix // 2
+    lens[2] = 0
+    lens[-1] = 1
+    run_case(H, kvh, hd, ps, BF, lens, new, prefix, scale=-0.25, prefix_table=True)
+
+
+@pytest.mark.parametrize("H,kvh,hd,ps,new,prefix", SHARED)
+def test_attention_shared_bad_pages(H, kvh, hd, ps, new, prefix):
+    """A bad page of a sequence's own poisons it, one of the prefix everyone, a bad length its sequence."""
+    dexlib = require_gpu()
+    lens = [prefix + 30 * (b % 3) + n for b, n in enumerate(new)]
+    cache, pages, table = paged(dexlib, kvh, hd, ps, lens, BF, prefix)
+    q, start = queries(H, hd, new, BF)
+    ref = attention(pages, table, q.cpu(), start, lens, prefix)
+    seq_len = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    owner = torch.repeat_interleave(torch.arange(len(new)), torch.tensor(new))
+    victim = max(b for b, n in enumerate(new) if n and (lens[b] - 1) // ps >= -(-prefix // ps))
+
+    def call(length=seq_len):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        lse = torch.zeros(q.shape[:2], device="cuda")
+        out = cache.attention(q, start.cuda(), length, max(new), prefix, lse=lse, status=status)
+        return out, lse, int(status.item())
+
+    bad = table.clone()
+    bad[victim, (lens[victim] - 1) // ps] = len(pages)
+    cache.table.copy_(bad)
+    out, lse, status = call()
+    assert status == dexlib.DEX_ATTN_BAD_PAGE
+    assert bool(torch.isnan(out[owner == victim]).all()) and bool(torch.isnan(lse[owner == victim]).all())
+    compare(out, lse, ref, owner != victim)
+    bad = table.clone()
+    bad[:, prefix // ps // 2] = -5
+    cache.table.copy_(bad)
+    out, lse, status = call()
+    assert status == dexlib.DEX_ATTN_BAD_PAGE and bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all())
+    cache.table.copy_(table)
+    length = seq_len.clone()
+    length[victim] = -1
+    out, lse, status = call(length)
+    assert status == dexlib.DEX_ATTN_BAD_RANGE and bool(torch.isnan(out[owner == victim]).all())
+    compare(out, lse, ref, owner != victim)
+
+
 def test_attention_strides():
     """Queries that are one expanded row, an output inside a larger tensor, a table inside a wider one, tokens
     before the first sequence's."""
