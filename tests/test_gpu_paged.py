@@ -397,6 +397,64 @@ def test_attention_two_at_once():
     assert all(torch.equal(a, o) for a, o in zip(alone, outs))
 
 
+@pytest.mark.parametrize("batch,kvh,G,hd,prefix", [(24, 8, 4, 128, 400), (14, 8, 2, 64, 600), (7, 32, 1, 128, 300)])
+def test_shared_steps_in_a_graph(batch, kvh, G, hd, prefix):
+    """A captured step (append, then attention) replayed while the sequences grow, one of them runs ahead and some
+    have no token: the prefix is read once, by either kernel, with the rest beside it or in the same one."""
+    dexlib = require_gpu()
+    H, ps, steps = kvh * G, 32, 12
+    gen = torch.Generator().manual_seed(batch)
+    lens = [prefix + int(x) for x in torch.randint(0, 60, (batch,), generator=gen)]
+    lens[1] = prefix + 900
+    cache, pages, table = paged(dexlib, kvh, hd, ps, [n + steps for n in lens], BF, prefix, fill=0.0)
+    pages = pages.clone()
+    rows = torch.randn((steps, batch, H + 2 * kvh, hd), generator=gen).to(BF)
+    live = torch.rand((steps, batch), generator=gen) < 0.8
+    live[0], live[:, 0], live[5] = True, True, False
+    step = torch.zeros((batch, H + 2 * kvh, hd), dtype=BF, device="cuda")
+    seq, pos, seq_len = (torch.zeros(batch, dtype=torch.int32, device="cuda") for _ in range(3))
+    start = torch.zeros(batch + 1, dtype=torch.int32, device="cuda")
+    out = torch.zeros((batch, H, hd), dtype=BF, device="cuda")
+    lse = torch.zeros((batch, H), device="cuda")
+    q = torch.zeros((batch, H, hd), dtype=BF, device="cuda")
+    ws = cache.attention_workspace(q, 1, prefix)
+
+    def call():
+        cache.append(step[:, H:H + kvh], step[:, H + kvh:], seq, pos, q=step[:, :H], q_out=q, theta=0.0)
+        cache.attention(q, start, seq_len, 1, prefix, out=out, lse=lse, workspace=ws)
+
+    seq.fill_(-1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    now = list(lens)
+    for i in range(steps):
+        who = [b for b in range(batch) if live[i, b]]
+        n = len(who)
+        step[:n] = rows[i, who].cuda()
+        seq.copy_(torch.tensor(who + [-1] * (batch - n), dtype=torch.int32))
+        pos.copy_(torch.tensor([now[b] for b in who] + [0] * (batch - n), dtype=torch.int32))
+        for t, b in enumerate(who):
+            page, row = int(table[b, now[b] // ps]), now[b] % ps
+            pages[page, 0, :, row], pages[page, 1, :, row] = rows[i, b, H:H + kvh], rows[i, b, H + kvh:]
+            now[b] += 1
+        first = torch.tensor([0] + [int(x) for x in live[i]]).cumsum(0).int()
+        start.copy_(first)
+        seq_len.copy_(torch.tensor(now, dtype=torch.int32))
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        own = torch.arange(batch) < n
+        compare(out, lse, attention(pages, table, rows[i, who + [0] * (batch - n), :H], first, now, prefix), own)
+        assert bool((out[n:] == 7.0).all()) and bool((lse[n:] == 7.0).all())
+
+
 def test_calls_follow_each_other_closely():
     """Steps back to back on one stream, each changing the lengths and the cache the next one reads: what
     a step sees does not depend on how early its kernels become resident."""
