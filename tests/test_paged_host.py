@@ -107,7 +107,10 @@ def test_largest_sizes():
     c = kv(n_kv_heads=1)
     a = attn_args(n_tokens=1 << 23, n_heads=128, max_q=1 << 23, prefix_len=0)
     assert 0 < dexlib.dex_prefix_attention_workspace(c, a) < 1 << 40
-    a.prefix_len, a.max_q, a.n_heads = 64, 1, 64   # with a shared prefix: every row's result twice, in fp32
+    a.prefix_len, a.max_q, a.n_heads = 64, 1, 64   # a prefix of one tile is read by every sequence
+    assert 0 < dexlib.dex_prefix_attention_workspace(c, a) < 1 << 40
+    c = kv(n_kv_heads=1, table_width=2000, table_stride=2000)
+    a.prefix_len = 32000   # shared: every row's result twice, in fp32
     assert dexlib.dex_prefix_attention_workspace(c, a) > (1 << 29) * 2 * 64 * 4
     a.n_tokens += 1
     assert dexlib.lib().dex_prefix_attention_workspace(C.byref(c), C.byref(a), C.byref(C.c_size_t())) == EINVAL
