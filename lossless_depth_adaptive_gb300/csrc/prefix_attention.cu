@@ -61,11 +61,13 @@ constexpr int kRowsMinUnits = kRowsSegCost + 1, kTileMinUnits = 1;
 // Where tile_kernel computes the prefix and rows_kernel the rest, they run side by side: tile_kernel takes SMs in
 // proportion to the work, a unit of it counted as kTileWeight of rows_kernel's, and rows_kernel's CTAs, those on
 // the other SMs from the start and those that follow on its SMs, take kRowsQueue ranges each on average from a
-// queue.  Where rows_kernel computes both, its CTAs take two ranges in turn, so that each has prefix segments, whose
-// tiles cost more, and own ones, if they are kRowsTwo units or more together: 32 sequences of 32 heads behind 4096 positions 40.2 us, with one range 42.2, with
-// three 41.9.  64 sequences behind 8192 positions and 256 behind 32768: 37.7 and 144.8 us; weight 4 41.5 and 149.7, 6
+// queue.  64 sequences behind 8192 positions and 256 behind 32768: 37.7 and 144.8 us; weight 4 41.5 and 149.7, 6
 // 39.2 and 146.9; with a fixed range per CTA and all SMs for tile_kernel first 44.7 and 151.9; four ranges per CTA
-// 40.9 and 145.3, one 40.6 and 156.
+// 40.9 and 145.3, one (at weight 6) 40.6 and 156.
+// Where rows_kernel computes both, its CTAs take two ranges in turn, so that each has prefix segments, whose tiles
+// cost more, and own ones: 32 sequences of 32 heads behind 4096 positions 40.2 us, with one range 42.2, with three
+// 41.9.  Below kRowsTwo units per CTA it is one range (3 sequences of 4 heads behind 12815, three units per CTA:
+// 10.9 us, with two 12.5).
 constexpr float kTileWeight = 5.0f;
 constexpr int kRowsQueue = 2;
 constexpr uint32_t kRowsTwo = 8;
@@ -197,9 +199,10 @@ struct Piece {
   bool starts, ends;  // it holds the segment's first, last tile
 };
 
-// The segment that holds a unit, and the walk to the next one.  A segment is COST units followed by its
-// key tiles.  Lengths that change under a call (a caller's mistake) make its results wrong, but no loop
-// endless and no index leave its array: each read of a sequence is checked, and the walk ends within the batch.
+// The segment that holds a unit, and the walk to the next one.  A segment is its cost (COST units, fewer where its rows
+// are half a tile_kernel's) followed by its key tiles.  Lengths that change under a call (a caller's mistake) make
+// its results wrong, but no loop endless and no index leave its array: each read of a sequence is checked, and the
+// walk ends within the batch.
 template <int RT, int TILE, int COST>
 struct Walker {
   const SegWork& w;
@@ -415,7 +418,8 @@ __device__ __forceinline__ uint32_t units_behind(const SegWork& w, uint32_t* scr
   for (int b = threadIdx.x; b < w.a.kv.batch; b += THREADS) {
     const SeqRef s = seq_ref(w.a, b);
     if (s.valid && s.len > w.a.prefix_len)
-      n += static_cast<uint32_t>((s.n * w.a.G + w.behind_rt - 1) / w.behind_rt * ((s.len - w.a.prefix_len + kRowsTile - 1) / kRowsTile + kRowsSegCost));
+      n += static_cast<uint32_t>((s.n * w.a.G + w.behind_rt - 1) / w.behind_rt *
+                                 ((s.len - w.a.prefix_len + kRowsTile - 1) / kRowsTile + kRowsSegCost));
   }
   n = __reduce_add_sync(0xffffffffu, n);
   if (threadIdx.x % 32 == 0) scratch[threadIdx.x / 32] = n;
@@ -729,7 +733,8 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
           d[0] = make_int4(wk.rows, (wk.rows + kRowsUnit - 1) / kRowsUnit, wk.k.lo, wk.k.hi);
           d[1] = make_int4((wk.k.t0 + pc.tile) * kRowsTile, pc.cnt, wk.kvh,
                            (wk.prefix ? kSegPrefix : 0) | (pc.starts ? kSegStarts : 0) | (pc.ends ? kSegEnds : 0) |
-                               (!wk.prefix && wk.s.bad ? kSegBad : 0) | (!w.queue && range + gridDim.x >= sh.ctas && g1 - g - pc.units <= kRowsSegCost ? kSegLast : 0));
+                               (!wk.prefix && wk.s.bad ? kSegBad : 0) |
+                               (!w.queue && range + gridDim.x >= sh.ctas && g1 - g - pc.units <= kRowsSegCost ? kSegLast : 0));
           d[2] = make_int4(wk.prefix ? wk.seg : wk.own_info_index(), range,
                            pc.starts ? sh.owner(g - static_cast<uint32_t>(off) + wk.units() - 1) : 0, 0);
           mbar_arrive_expect_tx(&seg_full[slot], static_cast<uint32_t>(wk.rows * HD * 2));
@@ -1186,7 +1191,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const uint32_t total = count_units<kTileThreads>(wk, cum, scratch);
   uint32_t ctas = gridDim.x;
   if (w.behind_rt) {   // the other SMs go to rows_kernel at once
-    const float mine = kTileWeight * static_cast<float>(total), other = static_cast<float>(units_behind<kTileThreads>(w, scratch));
+    const float mine = kTileWeight * static_cast<float>(total);
+    const float other = static_cast<float>(units_behind<kTileThreads>(w, scratch));
     ctas = max(static_cast<uint32_t>(ceilf(static_cast<float>(ctas) * (mine / (mine + other)))), 1u);
   }
   const Share sh(total, ctas, kTileMinUnits);
@@ -1681,7 +1687,8 @@ __global__ void __launch_bounds__(DIMS * 2 * SPLIT) combine_kernel(const __grid_
   __shared__ int row_seq[32];
   __shared__ float join[SPLIT > 1 ? SPLIT / 2 : 1][SPLIT > 1 ? 18 : 1][DIMS * 2];
   const PrefixAttnArgs& a = w.own.a;
-  const int tid = threadIdx.x, group = tid / (DIMS * 2), warp = blockIdx.z * (DIMS / 16) + (tid >> 5) % (DIMS / 16), lane = tid & 31, kvh = blockIdx.y;
+  const int tid = threadIdx.x, lane = tid & 31, group = tid / (DIMS * 2), kvh = blockIdx.y;
+  const int warp = blockIdx.z * (DIMS / 16) + (tid >> 5) % (DIMS / 16);   // 16 head dims
   const int n_rows = 1 << w.row_bits, li = lane & (n_rows - 1), slot = lane >> w.row_bits, n_slots = 32 >> w.row_bits;
   const int rows_all = a.n_tokens * a.G, rg0 = blockIdx.x << w.row_bits;
   const int rg = rg0 + li;   // row: token * G + head within the K/V head
@@ -1822,8 +1829,8 @@ struct Plan {
 // So it is shared when more than one sequence can have queries (n_tokens > max_q) and reading it for all of
 // them would give every CTA of rows_kernel three key tiles: at 624 tiles in all (13 sequences of 4 heads behind 777
 // positions) it takes 13.2 us shared and 12.2 not, at 1188 (9 of 4 behind 2158) 10.4 and 12.6, at 2048 (8 of 8
-// behind 2048) 13.1 and 16.3.  A prefix below two tiles is not (73 positions, 202 sequences of 8 heads: 83 us shared, 70 not), and
-// a sequence whose own rows fill a 128-row tile gains nothing from sharing.
+// behind 2048) 13.1 and 16.3.  A prefix below two tiles is not shared (73 positions, 202 sequences of 8 heads: 83 us
+// shared, 70 not), and a sequence whose own rows fill a 128-row tile gains nothing from sharing.
 Plan make_plan(const PrefixAttnArgs& a) {
   Plan p = {};
   const int64_t own_rows = static_cast<int64_t>(a.max_q) * a.G, all_rows = static_cast<int64_t>(a.n_tokens) * a.G;
