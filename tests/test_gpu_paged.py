@@ -219,6 +219,24 @@ def test_attention_inactive_first_slot():
         compare(out, lse, attention(pages, table, q.cpu(), start, lens, prefix, shared), torch.ones(5, dtype=torch.bool))
 
 
+@pytest.mark.parametrize("H,new", [(32, [0, 1, 2, 1, 1, 2]), (8, [0, 1, 1, 1, 1, 1])])
+def test_shared_prefix_without_row_zero(H, new):
+    """A prefix long enough to be read once, by either kernel, whose pages row 0 of the table does not name."""
+    dexlib = require_gpu()
+    kvh, hd, ps, prefix = 8, 128, 32, 1600
+    lens = [0] + [prefix + n for n in (3, 90, 2, 64, 17)]
+    cache, pages, table = paged(dexlib, kvh, hd, ps, lens, BF, prefix)
+    shared = table[1, :prefix // ps].clone()
+    cache.table[0] = -1
+    q, start = queries(H, hd, new, BF)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lse = torch.zeros(q.shape[:2], device="cuda")
+    out = cache.attention(q, start.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), max(new), prefix,
+                          prefix_table=shared.cuda(), lse=lse, status=status)
+    assert int(status.item()) == 0
+    compare(out, lse, attention(pages, table, q.cpu(), start, lens, prefix, shared), torch.ones(len(q), dtype=torch.bool))
+
+
 @pytest.mark.parametrize("prefix", [0, 128])
 def test_attention_large_batch(prefix):
     """The largest batch, most of it without queries or without positions."""
