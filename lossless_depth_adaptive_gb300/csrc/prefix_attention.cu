@@ -1043,8 +1043,8 @@ struct TileSmem {
   static constexpr uint32_t oMl = oRing + kStages * kBuf;            // float2 [128]
   static constexpr uint32_t oBar = oMl + 128 * 8;
   static constexpr uint32_t kBars = 2 * kStages + 9;
-  static constexpr uint32_t oMisc = oBar + kBars * 8;                // bad flags [stages], scratch [12], TMEM address, segment flag
-  static constexpr uint32_t kTotal = oMisc + (kStages + 15) * 4 + 1024;
+  static constexpr uint32_t oMisc = oBar + kBars * 8;                // bad flags [stages], scratch [12], TMEM address, segment flags [4]
+  static constexpr uint32_t kTotal = oMisc + (kStages + 17) * 4 + 1024;
   static_assert(kStages * kBuf >= kMaxBatch * 4, "the counts use the ring before the first copy");
 };
 static_assert(TileSmem<128>::kTotal <= 227 * 1024, "tile_kernel shared memory");
@@ -1154,7 +1154,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   volatile int* bad_stage = reinterpret_cast<volatile int*>(smem + SM::oMisc);
   uint32_t* scratch = reinterpret_cast<uint32_t*>(smem + SM::oMisc) + SM::kStages;
   uint32_t* tmem_slot = scratch + 12;
-  volatile int* seg_bad = reinterpret_cast<volatile int*>(tmem_slot + 1);   // [2] the segment met a bad page (before o_full)
+  volatile int* seg_bad = reinterpret_cast<volatile int*>(tmem_slot + 1);   // [2 segments][2 teams] it met a bad page (before o_full)
   uint32_t* cum = reinterpret_cast<uint32_t*>(smem + SM::oRing);
   const PrefixAttnArgs& a = w.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1171,7 +1171,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(&p_full[i], 4);
       mbar_init(&turn[i], 1);
     }
-    mbar_init(o_full, 4);   // both issuers: their MMAs and their word on the segment's pages
+    // both issuers, their MMAs and their word on the segment's pages; and the warps of the teams as they enter the
+    // segment: one team's issuer may need nothing of the other team, which has to have seen the phase before
+    mbar_init(o_full, 4 + 8);
     fence_mbar_init();
     tma_prefetch(&tm);
   }
@@ -1229,6 +1231,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const Piece pc = wk.piece(off, g1 - g);
       const int tile = pc.tile, cnt = pc.cnt;
       if (cnt == 0) break;   // only at the end of the range
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_full);   // this warp has read the segment before
       const bool alt = wk.rows <= 128;   // the teams share the rows and take alternate key tiles
       const int ahead = alt ? 2 : 1;
       const int r = alt ? r128 : team * 128 + r128;
@@ -1403,7 +1407,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
       if (r128 == 0 && any) free_stage(v_stage, alt);
-      if (!ok || seg_bad[0] || seg_bad[1] || (!wk.prefix && wk.s.bad)) l = quiet_nan();
+      const volatile int* met = seg_bad + 2 * (n_seg & 1u);
+      if (!ok || met[0] || met[1] || (!wk.prefix && wk.s.bad)) l = quiet_nan();
       const bool read = ok && any;   // warp-uniform
       if (alt && team == 1) {
         join_ml[r128] = make_float2(m, l);
@@ -1629,7 +1634,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (more) qk(q, k, !alt);
           else if (!alt) mbar_arrive(&turn[team ^ 1]);
         }
-        seg_bad[team] = bad || !ok;   // the teams read it after o_full
+        // The teams read it after o_full.  The word was last that of the segment before the last one, which every
+        // warp had read before it let o_full of the last one complete, and q_full came after that.
+        seg_bad[2 * (n_seg & 1u) + team] = bad || !ok;
         umma_commit(o_full);
         mbar_arrive(o_full);
         g += pc.units;

@@ -150,6 +150,37 @@ def test_attention_nothing_visible(dtype):
     run_case(8, 2, 128, 16, dtype, [2, 2], [2, 2], tree=tree)                            # all words empty, nothing cached
 
 
+@pytest.mark.parametrize("dtype,hd", [(BF, 128), (FP, 64)])
+def test_attention_short_segments_in_turn(dtype, hd):
+    """Many one-tile segments per thread block, of more than 128 rows and of fewer in turn (the two halves of a block
+    take a row tile each, or share the rows), some of them with a bad page: results and poison stay with their own."""
+    dexlib = require_gpu()
+    kvh, G, ps = 4, 4, 32
+    new = [n for _ in range(70) for n in (75, 10, 1, 40)]
+    lens = [n + 13 * (b % 3) for b, n in enumerate(new)]
+    cache, pages, table = paged(dexlib, kvh, hd, ps, lens, dtype)
+    q, start = queries(kvh * G, hd, new, dtype)
+    owner = torch.repeat_interleave(torch.arange(len(new)), torch.tensor(new))
+    at = torch.tensor(lens)[owner] - torch.tensor(new)[owner] + torch.arange(len(q)) - start[:-1].long()[owner]   # positions
+    ref = attention(pages, table, q.cpu(), start, lens)
+    seq_len = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    victims = torch.tensor([b % 5 == 2 and n > 40 for b, n in enumerate(lens)])
+    for entry in (None, 0, 1):
+        bad = table.clone()
+        if entry is not None:
+            bad[victims, entry] = -1
+        cache.table.copy_(bad)
+        for _ in range(5):
+            status = torch.zeros(1, dtype=torch.int32, device="cuda")
+            lse = torch.zeros(q.shape[:2], device="cuda")
+            out = cache.attention(q, start.cuda(), seq_len, max(new), lse=lse, status=status)
+            assert int(status.item()) == (0 if entry is None else dexlib.DEX_ATTN_BAD_PAGE)
+            hit = victims[owner] if entry is not None else torch.zeros(len(q), dtype=torch.bool)
+            compare(out, lse, ref, ~hit)
+            if entry is not None:
+                assert bool(torch.isnan(out[hit & (at >= entry * ps)]).all())
+
+
 def test_attention_long_and_layers():
     """A long context split over the whole GPU, pages strided over the layers of a model."""
     run_case(8, 2, 128, 16, BF, [20011], [1], layers=3)
