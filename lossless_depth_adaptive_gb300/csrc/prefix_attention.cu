@@ -65,6 +65,7 @@ constexpr int kRowsMinUnits = kRowsSegCost + 1, kTileMinUnits = 1;
 constexpr float kTileWeight = 5.0f;
 constexpr uint32_t kRowsTwo = 8;
 constexpr int kMaxBatch = 1024;
+static_assert(kRowsPerSm * kSms <= 0x3ff, "CTAs in the gate of a queue");
 
 // Division by a number fixed for the call: n / d for 0 <= n < 2^31 (multiply, add, shift).
 struct FastDiv {
@@ -79,6 +80,26 @@ struct FastDiv {
   }
 };
 
+// Ranges of a rows_kernel behind tile_kernel, which opens the queue for it.
+struct RangeQueue {
+  uint32_t next;   // next range to take
+  uint32_t pad;
+  uint64_t gate;   // kGate + CTAs of rows_kernel that start beside tile_kernel; anything else: not open (yet)
+};
+static_assert(sizeof(RangeQueue) == kQueueBytes, "workspace of the queue");
+// rows_kernel can run before tile_kernel ends, so no kernel boundary makes `next` visible to it.  It takes the gate's
+// word by an acquiring load, tile_kernel stores it by a releasing one, and the join, which runs when both have ended,
+// takes it back for the next call.  A workspace's first bytes before its first call hold it once in 2^54.
+constexpr uint64_t kGate = 0x5bd1e9a74c36f800ull, kGateCtas = 0x3ffull;
+__device__ __forceinline__ uint64_t load_acquire(const uint64_t* p) {
+  uint64_t v;
+  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_release(uint64_t* p, uint64_t v) {
+  asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+
 // What one of the two kernels has to do in a call.
 struct SegWork {
   PrefixAttnArgs a;
@@ -91,8 +112,7 @@ struct SegWork {
   int32_t slots;        // rows_kernel: segments posted ahead
   int32_t per_cta;      // rows_kernel: ranges per CTA, at most
   int32_t behind_rt;    // tile_kernel: rows per segment of the rows_kernel behind it (it computes the own segments), or 0
-  uint32_t* queue;      // rows_kernel behind tile_kernel, which sets them: next range to take, CTAs that start beside
-                        // it; or null: CTA i takes range i
+  RangeQueue* queue;    // rows_kernel behind tile_kernel, or null: CTA i takes range i
   float* part_o;        // parts of cut segments, two per range: [2 * ranges][hd / 4][rows][4]
   float2* part_ml;      // [2 * ranges][rows] (m, l)
   float* pre_o;         // finished prefix segments (joined): [KVH][hd / 4][n_tokens * G][4]
@@ -640,12 +660,27 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
   if (tid < 64) token_seq[tid] = -1;
   // A CTA that starts when tile_kernel's are done leaves if those that started with them have at most one range each
   // to go: its own start takes longer (64 sequences behind 8192 positions: 39.5 us, 37.7 so).  Those never leave,
-  // so every range is taken whatever the two words say.
+  // so every range is taken whatever `taken`, which is read ahead of the gate, says.
   if (w.queue && tid == 0) {
-    const uint32_t early = __ldcg(w.queue + 1), taken = __ldcg(w.queue);
+    const uint32_t taken = __ldcg(&w.queue->next);
+    uint64_t gate = load_acquire(&w.queue->gate), t0 = 0;
+    while ((gate & ~kGateCtas) != kGate) {   // stored before this kernel could start: a matter of its becoming visible
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      else if (now - t0 > kWaitLimitNs) break;
+      gate = load_acquire(&w.queue->gate);
+    }
+    const bool open = (gate & ~kGateCtas) == kGate;
+    if (!open && a.status) atomicOr(a.status, DEX_ATTN_TIMEOUT);
+    const uint32_t early = static_cast<uint32_t>(gate & kGateCtas);
+    scratch[30] = open;
     scratch[31] = blockIdx.x >= early && early > 0 ? taken + early : 0;
   }
   __syncthreads();
+  if (w.queue && !scratch[30]) {
+    griddep_wait();
+    return;
+  }
   if (w.first) griddep_wait();
   const uint32_t enough = w.queue ? scratch[31] : 0;   // the counts use the first words
   Walker<SM::kRows, kRowsTile, kRowsSegCost> wk(w);
@@ -673,7 +708,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
     auto claim = [&] {   // the next range
       if (!w.queue) return range + gridDim.x;
       uint32_t r = 0;
-      if (lane == 0) r = atomicAdd(w.queue, 1u);
+      if (lane == 0) r = atomicAdd(&w.queue->next, 1u);
       return __shfl_sync(0xffffffffu, r, 0);
     };
     auto slot_free = [&](int slot) {
@@ -1191,12 +1226,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     ctas = max(static_cast<uint32_t>(ceilf(static_cast<float>(ctas) * (mine / (mine + other)))), 1u);
   }
   const Share sh(total, ctas, kTileMinUnits);
-  // rows_kernel cannot start before every CTA here has allowed it, which this one does after the fence; it reads
-  // both words from L2
+  // rows_kernel starts when every CTA here has allowed it, which this one does after it has opened the queue
   if (w.queue && blockIdx.x == 0 && tid == 0) {
-    w.queue[0] = 0;
-    w.queue[1] = kRowsPerSm * (gridDim.x - sh.ctas);
-    __threadfence();
+    w.queue->next = 0;
+    store_release(&w.queue->gate, kGate + kRowsPerSm * (gridDim.x - sh.ctas));
   }
   const bool work = blockIdx.x < sh.ctas;
   const uint32_t g0 = work ? sh.begin(blockIdx.x) : 0, g1 = work ? sh.begin(blockIdx.x + 1) : 0;
@@ -1714,6 +1747,7 @@ __global__ void __launch_bounds__(DIMS * 2 * SPLIT) combine_kernel(const __grid_
   const int2* pre_at = b >= 0 && w.share ? w.pre.pre_info + rg / w.pre_rt * a.kv.KVH + kvh : nullptr;
   const int2* own_at = b >= 0 && nt > 0 ? w.own.own_info + own_info_of(a, w.own_rt, s.q0, b, rt, kvh) : nullptr;
   griddep_wait();
+  if (w.own.queue && tid == 0 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) w.own.queue->gate = 0;
   // this row's parts: prefix parts of ranges pre_c0 .., then own parts of ranges own_c0 ..  A kernel that gave up
   // waiting leaves entries that hold anything: none of them is followed.
   const int2 pre_info = pre_at ? __ldcg(pre_at) : make_int2(0, -1), own_info = own_at ? __ldcg(own_at) : make_int2(0, -1);
@@ -1859,7 +1893,7 @@ cudaError_t launch_hd(const PrefixAttnArgs& a, const Plan& p, uint8_t* ws, cudaS
   base.own_ml = reinterpret_cast<float2*>(ws + p.o_own_ml);
   base.pre_info = reinterpret_cast<int2*>(ws + p.o_pre_info);
   base.own_info = reinterpret_cast<int2*>(ws + p.o_own_info);
-  if (p.queue()) base.queue = reinterpret_cast<uint32_t*>(ws + p.o_queue);
+  if (p.queue()) base.queue = reinterpret_cast<RangeQueue*>(ws + p.o_queue);
   SegWork rows = base, tile = base;
   rows.part_o = reinterpret_cast<float*>(ws + p.o_rows_part);
   rows.part_ml = reinterpret_cast<float2*>(ws + p.o_rows_ml);

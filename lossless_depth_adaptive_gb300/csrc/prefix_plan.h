@@ -22,6 +22,7 @@ constexpr int kRowsSlotRows = 64; // rows of the segments posted ahead
 constexpr int kRowsPerSm = 2;     // resident CTAs
 constexpr int kSms = 152;         // of the sm_103 part: workspace sizes and grids, whatever device is current
 constexpr int kTileRows = 256;    // query rows of a segment of tile_kernel (two tiles of 128)
+constexpr int kQueueBytes = 16;   // state of a queue of ranges
 constexpr int kRowsQueue = 2;     // ranges per CTA of rows_kernel where it takes several
 
 // Parts of a row that a segment's entry (first and last range) stands for, none where it is not one that the kernel
@@ -75,7 +76,7 @@ inline Plan make_plan(const PrefixAttnArgs& a) {
   };
   const size_t hd4 = static_cast<size_t>(a.kv.hd) * 4;
   if (p.rows_mt) {
-    if (p.queue()) p.o_queue = take(2 * sizeof(uint32_t));
+    if (p.queue()) p.o_queue = take(kQueueBytes);
     p.o_rows_part = take(size_t(2) * p.rows_ranges() * p.rows_mt * kRowsUnit * hd4);
     p.o_rows_ml = take(size_t(2) * p.rows_ranges() * p.rows_mt * kRowsUnit * 8);
   }

@@ -446,6 +446,35 @@ def test_attention_two_at_once():
     assert all(torch.equal(a, o) for a, o in zip(alone, outs))
 
 
+def test_workspace_in_any_state():
+    """A workspace holds anything before a call: the same bits from a fresh one, from one filled with any byte, and
+    from one that calls of other plans (either kernel alone, both side by side) have used in between."""
+    dexlib = require_gpu()
+    H, kvh, hd, ps, prefix = 32, 8, 128, 32, 400
+    lens, new = [prefix + 37 * i + 1 for i in range(24)], [1] * 24
+    cache, pages, table = paged(dexlib, kvh, hd, ps, lens, BF, prefix)
+    seq_len = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q, start = queries(H, hd, new, BF)
+    start = start.cuda()
+    runs = torch.tensor([0] + [24] * 24, dtype=torch.int32, device="cuda")   # all tokens of sequence 0
+    # both kernels, rows_kernel, tile_kernel, rows_kernel with the prefix
+    calls = [(q, start, 1, prefix), (q, start, 1, 0), (q, runs, 24, 0), (q[:, :kvh], start, 1, prefix)]
+    calls = [(x.contiguous(), *rest) for x, *rest in calls]
+    size = max(cache.attention_workspace(x, m, p).numel() for x, _, m, p in calls)
+    want = [cache.attention(x, st, seq_len, m, p) for x, st, m, p in calls]
+    out, _, bound, _ = attention(pages, table, q.cpu(), start.cpu(), lens, prefix)
+    assert bool(((want[0].cpu().double() - out).abs() <= bound).all())
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    for fill in (0, 1, 0x7f, 0xff, None):
+        if fill is not None:
+            ws.fill_(fill)
+        for _ in range(3):
+            for (x, st, m, p), w in zip(calls, want):
+                status = torch.zeros(1, dtype=torch.int32, device="cuda")
+                assert torch.equal(cache.attention(x, st, seq_len, m, p, workspace=ws, status=status), w)
+                assert int(status.item()) == 0
+
+
 @pytest.mark.parametrize("batch,kvh,G,hd,prefix", [(24, 8, 4, 128, 400), (14, 8, 2, 64, 600), (7, 32, 1, 128, 300)])
 def test_shared_steps_in_a_graph(batch, kvh, G, hd, prefix):
     """A captured step (append, then attention) replayed while the sequences grow, one of them runs ahead and some
