@@ -49,14 +49,9 @@ int get_encoder() {
 int encode_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows,
               CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
   if ((reinterpret_cast<uintptr_t>(base) & 15) || (cols * 2) % 16) return DEX_EINVAL;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols * 2};
-  cuuint32_t box[2] = {64, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = g_encode(map, dtype, 2, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? DEX_OK : DEX_EINVAL;
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols * 2};
+  const cuuint32_t box[2] = {64, box_rows};
+  return dex::encode_tensor_map(map, dtype, 2, base, dims, strides, box) ? DEX_OK : DEX_EINVAL;
 }
 
 int pow2_at_least(int x) {
@@ -67,7 +62,20 @@ int pow2_at_least(int x) {
 
 }  // namespace
 
-PFN_cuTensorMapEncodeTiled_v12000 dex::tensor_map_encoder() { return get_encoder() == DEX_OK ? g_encode : nullptr; }
+bool dex::encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t rank, const void* base, const cuuint64_t* dims,
+                            const cuuint64_t* strides, const cuuint32_t* box) {
+  if (get_encoder()) return false;
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  auto encode = [&] {
+    return g_encode(map, dtype, rank, const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (encode()) return true;
+  // A thread has no current context until its first runtime call that needs one, and none of those comes before this
+  // on every path: setting the device that is current makes its context current too.
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode();
+}
 
 constexpr int kPrefillRowsMax = 512;   // most prompt positions per prefill pass (rows of the scratch planes)
 

@@ -3,7 +3,6 @@
 #pragma once
 
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -273,8 +272,9 @@ cudaError_t launch_decode_best(const unsigned long long* best, int n, const int3
 // the kernels' DevNode rows.
 cudaError_t launch_exit_nodes(const void* exit_nodes, int n, DevNode* out, cudaStream_t st);
 
-// The driver's tensor-map encoder, or null when it cannot be had.
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+// Tensor map of 128-byte swizzled boxes, zero fill out of bounds (strides in bytes, from the second dimension on).
+bool encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t rank, const void* base, const cuuint64_t* dims,
+                       const cuuint64_t* strides, const cuuint32_t* box);
 
 // ---- paged cache --------------------------------------------------------------------------
 // One layer of a paged K/V cache as the kernels see it: pages of [2][KVH][page][hd] elements,

@@ -24,7 +24,6 @@
 //    stream of K and V through a TMA ring into m16n8k16 MMAs on register fragments;
 //  * tile_kernel (up to 256 rows): 5th-generation tensor cores, two 128-row tiles per CTA that
 //    share every K and V tile.
-#include <cudaTypedefs.h>
 #include <math.h>
 
 #include <atomic>
@@ -1852,15 +1851,12 @@ cudaError_t set_smem(F* func, uint32_t bytes, std::atomic<uint64_t>& done, int d
 // 4-D map of the pages: head_dim, position in the page, (K|V) x K/V head, page; boxes of 64 dims x
 // `rows` positions, 128-byte swizzle.
 bool page_map(CUtensorMap* map, const PagedKv& kv, int rows) {
-  auto encode = tensor_map_encoder();
-  if (!encode) return false;
   const uint64_t page = uint64_t(1) << kv.page_shift;
-  cuuint64_t dims[4] = {static_cast<cuuint64_t>(kv.hd), page, static_cast<cuuint64_t>(2) * kv.KVH, static_cast<cuuint64_t>(kv.n_pages)};
-  cuuint64_t strides[3] = {static_cast<cuuint64_t>(kv.hd) * 2, page * kv.hd * 2, static_cast<cuuint64_t>(kv.page_stride) * 2};
-  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1}, estr[4] = {1, 1, 1, 1};
-  return encode(map, kv.fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, kv.pages, dims, strides,
-                box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(kv.hd), page, static_cast<cuuint64_t>(2) * kv.KVH, static_cast<cuuint64_t>(kv.n_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(kv.hd) * 2, page * kv.hd * 2, static_cast<cuuint64_t>(kv.page_stride) * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1};
+  return encode_tensor_map(map, kv.fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, kv.pages, dims,
+                           strides, box);
 }
 
 template <typename K, typename... A>

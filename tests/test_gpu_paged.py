@@ -1,6 +1,7 @@
 """GPU parity of the paged-cache operators (append with rotation, shared-prefix attention) against
 plain 64-bit forms, element by element within bounds derived from the arithmetic."""
 import math
+import threading
 
 import pytest
 import torch
@@ -422,6 +423,35 @@ def test_offsets_beyond_32_bits():
         lse = torch.zeros(q.shape[:2], device="cuda")
         out = cache.attention(q, start.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), max(new), lse=lse)
         compare(out, lse, attention(small, small_ids, q.cpu(), start, lens), torch.ones(len(q), dtype=torch.bool))
+
+
+def test_calls_from_a_new_thread():
+    """A thread whose first CUDA work is an attention call (or an append): it has no context of its own yet."""
+    dexlib = require_gpu()
+    H, kvh, hd, ps = 8, 2, 64, 16
+    lens, new = [50, 20], [1, 2]
+    cache, pages, table = paged(dexlib, kvh, hd, ps, lens, BF)
+    q, start = queries(H, hd, new, BF)
+    start, seq_len = start.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = cache.attention_workspace(q, 2)
+    want = cache.attention(q, start, seq_len, 2, workspace=ws)
+    k, idx = pages[:2, 0, :, 0].cuda(), torch.full((2,), -1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    for calls in (lambda out: cache.attention(q, start, seq_len, 2, out=out, workspace=ws),
+                  lambda out: (cache.append(k, k, idx, idx), cache.attention(q, start, seq_len, 2, out=out, workspace=ws))):
+        out, errors = torch.zeros_like(q), []
+
+        def run():
+            try:
+                calls(out)
+            except Exception as e:
+                errors.append(e)
+
+        t = threading.Thread(target=run)
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert not errors and torch.equal(out, want), errors
 
 
 def test_attention_two_at_once():

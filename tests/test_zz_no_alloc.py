@@ -113,3 +113,31 @@ def test_noalloc_refuses_oversized_calls():
     rc, tok, _ = _call("dex_exit_head_decs_noalloc", h, w, nodes_t, priors_t, n, d, V, False)
     assert rc == dexlib.DEX_ECAPACITY
     assert (tok == -1).all()          # nothing ran
+
+
+def test_noalloc_from_a_new_thread():
+    """A thread whose first CUDA work is this call (no context of its own yet), after the scratch is known."""
+    import threading
+    dexlib = require_gpu()
+    d, V = 256, 1000
+    h, w, _, _, _, nodes_t, priors_t, n = _inputs(3, 4, d, V, 0.2)
+    _, want, _ = _call("dex_exit_head_decs_noalloc", h, w, nodes_t, priors_t, n, d, V, False)
+    g = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    tokens = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    result = []
+
+    def run():
+        try:
+            result.append(dexlib.dex_exit_head_decs_noalloc(h.data_ptr(), n, d, g.data_ptr(), 1e-5, w.data_ptr(), V,
+                                                            nodes_t.data_ptr(), priors_t.data_ptr(), False, 0.7, 77,
+                                                            tokens.data_ptr()))
+        except Exception as e:
+            result.append(e)
+
+    t = threading.Thread(target=run)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert result == [dexlib.DEX_OK]
+    assert tokens.tolist() == want.tolist()
