@@ -1,6 +1,9 @@
 """GPU parity of the paged-cache operators (append with rotation, shared-prefix attention) against
 plain 64-bit forms, element by element within bounds derived from the arithmetic."""
 import math
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -452,6 +455,43 @@ def test_calls_from_a_new_thread():
         t.join()
         torch.cuda.synchronize()
         assert not errors and torch.equal(out, want), errors
+
+
+FIRST_CALLS = """
+import threading, torch
+import lossless_depth_adaptive_gb300 as dexlib
+pages = torch.randn((40, 2, 2, 16, 64), device="cuda").half()
+table = torch.randperm(40, device="cuda")[:32].int().view(4, 8)
+cache = dexlib.PagedCache(pages, table)
+q = torch.randn((8, 8, 64), device="cuda").half()
+start = torch.arange(0, 10, 2, dtype=torch.int32, device="cuda")
+lens = torch.tensor([100, 17, 64, 128], dtype=torch.int32, device="cuda")
+outs = [torch.zeros_like(q) for _ in range(8)]
+spaces = [cache.attention_workspace(q, 2) for _ in outs]
+streams = [torch.cuda.Stream() for _ in outs]
+torch.cuda.synchronize()
+gate, errors = threading.Barrier(len(outs)), []
+def first(i):
+    try:
+        gate.wait()
+        with torch.cuda.stream(streams[i]):
+            cache.attention(q, start, lens, 2, out=outs[i], workspace=spaces[i])
+    except Exception as e:
+        errors.append(e)
+threads = [threading.Thread(target=first, args=(i,)) for i in range(len(outs))]
+[t.start() for t in threads], [t.join() for t in threads]
+torch.cuda.synchronize()
+assert not errors, errors
+assert all(torch.equal(o, outs[0]) for o in outs) and bool(outs[0].any())
+"""
+
+
+def test_first_calls_on_several_threads():
+    """A process whose first attention calls are made by several threads at once, a stream and a workspace each."""
+    require_gpu()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-3000:]
 
 
 def test_attention_two_at_once():
