@@ -359,7 +359,9 @@ __device__ __forceinline__ RowView row_view(const PrefixAttnArgs& a, const SeqRe
   RowView v;
   v.owned = s.valid && t >= s.q0 && t < s.q0 + s.n;
   v.first = s.len - s.n;
-  v.word = a.tree && v.owned ? a.tree[t] : 0ull;
+  // bits from the sequence's number of queries on name nothing: in a prefix segment, which ends behind a shorter
+  // sequence, they would be positions that it does not have
+  v.word = a.tree && v.owned ? a.tree[t] & (~0ull >> (64 - min(s.n, 64))) : 0ull;
   v.last = a.tree ? v.first - 1 : v.first + (t - s.q0);
   if (s.bad) v.last = -1, v.word = 0;
   if (!v.owned) v.last = 0x7fffffff;   // its result is not used: no reason to mask
