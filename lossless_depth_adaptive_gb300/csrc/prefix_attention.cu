@@ -1065,7 +1065,9 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
 // while the tensor cores work for the other.
 // The running maximum of a row moves only when a score exceeds it by more than 2^8 (P then stays
 // within 2^8, which both 16-bit types hold), so O is rescaled rarely: a rescale reads and writes
-// all of it through registers between two MMAs.
+// all of it through registers between two MMAs.  It is carried without the scale and subtracted before
+// that is multiplied: the other way round the two are one FMA, and the rounded product of maximum and scale is off by
+// up to half the distance of fp32 neighbours from it -- from 2^27 on an exponent that 16 bits cannot hold.
 // ============================================================================================
 constexpr int kTileThreads = 384;   // two softmax teams; producer, an MMA issuer for each team, an idle warp
 constexpr float kRescale = 8.0f;
@@ -1147,9 +1149,9 @@ __device__ __forceinline__ uint64_t u32x2(uint32_t lo, uint32_t hi) {
   return r;
 }
 __device__ __forceinline__ uint64_t f32x2(float lo, float hi) { return u32x2(__float_as_uint(lo), __float_as_uint(hi)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
@@ -1303,8 +1305,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (on) wk.row_of(r, t_row, h_row);
       RowView rv{0x7fffffff, 0, 0, false};
       if (on) rv = wk.prefix ? row_view(a, seq_ref(a, seq_of_token(a, t_row)), t_row) : row_view(a, wk.s, t_row);
-      float m = -INFINITY, l = 0.0f;
-      bool any = false;   // this team had a tile
+      float m = -INFINITY, l = 0.0f;   // m: before the scale, until the segment's end
+      bool any = false;                // this team had a tile
       // stages of K of its next tile and V of its last one (thread 0), at hand before they are to be freed: the
       // loads that wait for them are needed within a tile's time
       uint64_t *k_stage = stage_of(k_load(alt ? team : 0, cnt, ahead)), *v_stage = nullptr;
@@ -1326,9 +1328,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         float tile_l, tile_m = -INFINITY;   // sum and maximum of this tile
         // Moves the row's m to the tile's maximum where that is larger by more than kRescale (or the first).
         auto move_m = [&] {
-          const bool move = tile_m > m + kRescale || (m == -INFINITY && tile_m > -INFINITY);
+          const bool move = (tile_m - m) * c > kRescale;   // at m = -inf too, unless tile_m is -inf as well
           if (!__any_sync(0xffffffffu, move)) return false;
-          const float f = move ? ex2(m - tile_m) : 1.0f;
+          const float f = move ? ex2((m - tile_m) * c) : 1.0f;
           if (any) {   // the PV before is complete: its issuer committed the scores after it
 #pragma unroll 1
             for (int q = 0; q < HD / 32; ++q) {
@@ -1360,7 +1362,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             tmem_st32(t_s + q * 32, s[0]);
           }
           tmem_wait_st();
-          tile_m *= c;
           move_m();
         } else if (!any) {
           // the first tile's maximum: a pass of loads, where the exponentials below would be taken twice
@@ -1374,7 +1375,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int i = 0; i < 16; ++i)
               mx[i & 1] = max3(mx[i & 1], __uint_as_float(s[q & 1][2 * i]), __uint_as_float(s[q & 1][2 * i + 1]));
           }
-          m = fmaxf(mx[0], mx[1]) * c;
+          m = fmaxf(mx[0], mx[1]);
         }
         if (!whole) {
           // rows of V outside the segment hold anything, and P = 0 must meet a finite v
@@ -1411,7 +1412,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int i = 0; i < 16; ++i) {
               const uint32_t s0 = s[q & 1][2 * i], s1 = s[q & 1][2 * i + 1];
               mx[i & 1] = max3(mx[i & 1], __uint_as_float(s0), __uint_as_float(s1));
-              const uint64_t x = fma2(u32x2(s0, s1), c2, sub2);
+              const uint64_t x = mul2(add2(u32x2(s0, s1), sub2), c2);
               const float p0 = ex2(__uint_as_float(static_cast<uint32_t>(x))), p1 = ex2(__uint_as_float(static_cast<uint32_t>(x >> 32)));
               l2[i & 1] = add2(l2[i & 1], f32x2(p0, p1));
               p[q][i] = pack2<T>(p0, p1);
@@ -1419,7 +1420,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
           const uint64_t t2 = add2(l2[0], l2[1]);
           tile_l = __uint_as_float(static_cast<uint32_t>(t2)) + __uint_as_float(static_cast<uint32_t>(t2 >> 32));
-          tile_m = fmaxf(mx[0], mx[1]) * c;
+          tile_m = fmaxf(mx[0], mx[1]);
         } while (move_m());
         l += tile_l;
         any = true;
@@ -1444,6 +1445,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const volatile int* met = seg_bad + 2 * (n_seg & 1u);
       if (!ok || met[0] || met[1] || (!wk.prefix && wk.s.bad)) l = quiet_nan();
       const bool read = ok && any;   // warp-uniform
+      // l and O are sums of exp2(s c - m c): what the product loses when it is rounded for the join they take on
+      const float m_c = m * c;
+      const float fix = fabsf(m_c) < INFINITY ? ex2(fminf(fmaxf(fmaf(m, c, -m_c), -60.0f), 60.0f)) : 1.0f;
+      m = m_c;
+      l *= fix;
       if (alt && team == 1) {
         join_ml[r128] = make_float2(m, l);
         if (read) {
@@ -1453,20 +1459,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             tmem_ld32_nowait(t_o + q * 32, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) join[(q * 32 + i) * 128 + r128] = __uint_as_float(o[i]);
+            for (int i = 0; i < 32; ++i) join[(q * 32 + i) * 128 + r128] = __uint_as_float(o[i]) * fix;
           }
         }
       }
       if (alt) named_bar_sync(1, 256);
       if (!alt || team == 0) {
-        float f0 = 1.0f, f1 = 0.0f;
+        float f0 = fix, f1 = 0.0f;
         const bool both = alt && cnt > 1;
         if (both) {
           const float2 other = join_ml[r128];
           const float M = fmaxf(m, other.x), sub = M > -INFINITY ? M : 0.0f;
-          f0 = ex2(m - sub);
+          const float f = ex2(m - sub);
+          f0 = fix * f;
           f1 = ex2(other.x - sub);
-          l = l * f0 + other.y * f1;
+          l = l * f + other.y * f1;
           m = M;
         }
         const bool starts = pc.starts, ends = pc.ends;
@@ -1490,10 +1497,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
           float x[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]);
+          for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]) * f0;
           if (both) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = x[i] * f0 + join[(q * 32 + i) * 128 + r128] * f1;
+            for (int i = 0; i < 32; ++i) x[i] += join[(q * 32 + i) * 128 + r128] * f1;
           }
           if (on && direct) {
 #pragma unroll
