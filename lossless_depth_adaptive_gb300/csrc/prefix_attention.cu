@@ -3,8 +3,11 @@
 //   o_i = sum_j softmax_j(scale q_i . k_j) v_j        over the keys j that query i sees
 //
 // The softmax over a set of keys is carried as (m, l, O): the largest score, the sum of
-// exp2(s - m) and the sum of exp2(s - m) v.  Two disjoint key sets join as m = max(m1, m2),
-// x = x1 2^(m1-m) + x2 2^(m2-m), so any split of a query's keys over CTAs gives the same result.
+// exp2(c (s - m)) and the sum of exp2(c (s - m)) v, with scores s before the scale and c = scale log2(e), taken
+// positive (a negative scale turns the scores' sign).  Two disjoint key sets join as m = max(m1, m2),
+// x = x1 2^(c (m1-m)) + x2 2^(c (m2-m)), so any split of a query's keys over CTAs gives the same result.  The
+// scale comes after the difference because the difference of near scores is exact, whatever their size; rounded
+// products s c are off by half the distance of fp32 neighbours, from 2^27 on by powers of 2^8.
 //
 // A *segment* is a set of query rows of one K/V head that reads the same keys:
 //  * prefix segment: rows of all sequences (token-major, the G query heads of the K/V head
@@ -137,6 +140,10 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// c of the scores; a zero scale zeroes them instead.
+__device__ __forceinline__ float score_scale(const PrefixAttnArgs& a) {
+  return a.scale_log2 == 0.0f ? 1.0f : fabsf(a.scale_log2);
 }
 __device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fffffff); }
 
@@ -836,7 +843,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
     float* smax = reinterpret_cast<float*>(smem + SM::oMax);
     float* ssum = reinterpret_cast<float*>(smem + SM::oSum);
     const uint32_t sp = smem_u32(smem + SM::oP);
-    const float c = a.scale_log2;
+    const float c = score_scale(a), sign = a.scale_log2 > 0.0f ? 1.0f : a.scale_log2 < 0.0f ? -1.0f : 0.0f;
     uint32_t phase = 0, n_seg = 0;
     int st = 0;
     bool ok = true;
@@ -911,7 +918,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
             for (int h = 0; h < 2; ++h) {
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                x[u][h][e] = (s[0][e >> 1][2 * h + (e & 1)] + s[1][e >> 1][2 * h + (e & 1)]) * c;
+                x[u][h][e] = (s[0][e >> 1][2 * h + (e & 1)] + s[1][e >> 1][2 * h + (e & 1)]) * sign;
               if (masked) {
                 const int r = u * 16 + gr + 8 * h;
                 RowView v{0x7fffffff, 0, 0, false};
@@ -953,10 +960,10 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
 #pragma unroll
             for (int k = 0; k < kRowsWarps; ++k) mx = fmaxf(mx, smax[k * SM::kRows + r]);
             const float base = mx > -INFINITY ? mx : 0.0f;
-            const float f = ex2(m[u][h] - base);
+            const float f = ex2((m[u][h] - base) * c);
             m[u][h] = mx;
-            const float p0 = ex2(x[u][h][0] - base), p1 = ex2(x[u][h][1] - base);
-            const float p2 = ex2(x[u][h][2] - base), p3 = ex2(x[u][h][3] - base);
+            const float p0 = ex2((x[u][h][0] - base) * c), p1 = ex2((x[u][h][1] - base) * c);
+            const float p2 = ex2((x[u][h][2] - base) * c), p3 = ex2((x[u][h][3] - base) * c);
             l[u][h] = l[u][h] * f + ((p0 + p1) + (p2 + p3));
 #pragma unroll
             for (int n = 0; n < NV; ++n) {
@@ -1032,7 +1039,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
               *reinterpret_cast<uint32_t*>(dst + n * 8) = pack2<T>(o[u][n][2 * h] * inv, o[u][n][2 * h + 1] * inv);
             if (a.lse && warp == 0 && tq == 0)
               a.lse[static_cast<int64_t>(t) * a.H + head] =
-                  isnan(L) ? L : L > 0.0f ? (m[u][h] + log2f(L)) * 0.6931471805599453f : -INFINITY;
+                  isnan(L) ? L : L > 0.0f ? (m[u][h] * c + log2f(L)) * 0.6931471805599453f : -INFINITY;
           } else {
             const PartRef p = whole ? joined_part<HD>(prefix ? w.pre_o : w.own_o, prefix ? w.pre_ml : w.own_ml, d.kvh, rows_all,
                                                       t * a.G + hg)
@@ -1065,12 +1072,14 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
 // while the tensor cores work for the other.
 // The running maximum of a row moves only when a score exceeds it by more than 2^8 (P then stays
 // within 2^8, which both 16-bit types hold), so O is rescaled rarely: a rescale reads and writes
-// all of it through registers between two MMAs.  It is carried without the scale and subtracted before
-// that is multiplied: the other way round the two are one FMA, and the rounded product of maximum and scale is off by
-// up to half the distance of fp32 neighbours from it -- from 2^27 on an exponent that 16 bits cannot hold.
+// all of it through registers between two MMAs.  c s - c m is one FMA with the rounded product c m, which is good
+// while that is off by far less than one; of rows with larger products (kFar) the scores in TMEM are replaced by
+// s - m first.  Difference and product apart for every score: 3.5 us more of 203 for 1752 prompt tokens behind
+// 8192 positions.
 // ============================================================================================
 constexpr int kTileThreads = 384;   // two softmax teams; producer, an MMA issuer for each team, an idle warp
 constexpr float kRescale = 8.0f;
+constexpr float kFar = 1048576.0f;   // 2^20, where fp32 neighbours are 2^-3 apart
 
 
 template <int HD>
@@ -1149,9 +1158,9 @@ __device__ __forceinline__ uint64_t u32x2(uint32_t lo, uint32_t hi) {
   return r;
 }
 __device__ __forceinline__ uint64_t f32x2(float lo, float hi) { return u32x2(__float_as_uint(lo), __float_as_uint(hi)); }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
@@ -1253,7 +1262,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + static_cast<uint32_t>(team) * 128 + t_lane;
     const uint32_t t_o = tmem + 256 + static_cast<uint32_t>(team) * 128 + t_lane;
-    const float c = a.scale_log2 == 0.0f ? 1.0f : fabsf(a.scale_log2);
+    const float c = score_scale(a);
     float* join = reinterpret_cast<float*>(smem + SM::oQ);   // [HD][128] O of team 1
     float2* join_ml = reinterpret_cast<float2*>(smem + SM::oMl);
     uint32_t n_s = 0, n_seg = 0, base = 0;   // score tiles of this team, segments, loads so far
@@ -1305,8 +1314,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (on) wk.row_of(r, t_row, h_row);
       RowView rv{0x7fffffff, 0, 0, false};
       if (on) rv = wk.prefix ? row_view(a, seq_ref(a, seq_of_token(a, t_row)), t_row) : row_view(a, wk.s, t_row);
-      float m = -INFINITY, l = 0.0f;   // m: before the scale, until the segment's end
-      bool any = false;                // this team had a tile
+      float m = -INFINITY, l = 0.0f;
+      bool any = false;   // this team had a tile
       // stages of K of its next tile and V of its last one (thread 0), at hand before they are to be freed: the
       // loads that wait for them are needed within a tile's time
       uint64_t *k_stage = stage_of(k_load(alt ? team : 0, cnt, ahead)), *v_stage = nullptr;
@@ -1326,28 +1335,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const bool whole = wk.k.lo <= key0 && wk.k.hi >= key0 + kTileKeys;
         uint32_t s[2][32];
         float tile_l, tile_m = -INFINITY;   // sum and maximum of this tile
-        // Moves the row's m to the tile's maximum where that is larger by more than kRescale (or the first).
-        auto move_m = [&] {
-          const bool move = (tile_m - m) * c > kRescale;   // at m = -inf too, unless tile_m is -inf as well
-          if (!__any_sync(0xffffffffu, move)) return false;
-          const float f = move ? ex2((m - tile_m) * c) : 1.0f;
-          if (any) {   // the PV before is complete: its issuer committed the scores after it
-#pragma unroll 1
-            for (int q = 0; q < HD / 32; ++q) {
-              uint32_t(&o)[32] = s[0];
-              tmem_ld32_nowait(t_o + q * 32, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st32(t_o + q * 32, o);
-            }
-            tmem_wait_st();
-          }
-          if (move) m = tile_m;
-          l *= f;
-          return true;
-        };
-        if (!__all_sync(0xffffffffu, whole && rv.last >= key0 + kTileKeys - 1)) {
+        float c_off = c;                    // 0 when the scores in TMEM are s - m
+        auto far = [&] { return m > -INFINITY && fabsf(m) * c >= kFar; };
+        // m and the scores have to be looked at before P: masked scores, or such a row
+        bool settle = !__all_sync(0xffffffffu, whole && rv.last >= key0 + kTileKeys - 1 && !far());
+        if (settle) {
           // masked scores go back to TMEM as -inf
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
@@ -1362,7 +1354,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             tmem_st32(t_s + q * 32, s[0]);
           }
           tmem_wait_st();
-          move_m();
         } else if (!any) {
           // the first tile's maximum: a pass of loads, where the exponentials below would be taken twice
           float mx[2] = {-INFINITY, -INFINITY};
@@ -1375,7 +1366,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int i = 0; i < 16; ++i)
               mx[i & 1] = max3(mx[i & 1], __uint_as_float(s[q & 1][2 * i]), __uint_as_float(s[q & 1][2 * i + 1]));
           }
-          m = fmaxf(mx[0], mx[1]);
+          tile_m = m = fmaxf(mx[0], mx[1]);
+          settle = __any_sync(0xffffffffu, far());
         }
         if (!whole) {
           // rows of V outside the segment hold anything, and P = 0 must meet a finite v
@@ -1398,8 +1390,43 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // P with the m at hand, and the maximum on the way: it rarely asks for another m, and the scores are still
         // in TMEM then
         uint32_t p[4][16];
-        do {
-          const float sub = m > -INFINITY ? m : 0.0f;
+        for (;;) {
+          if (settle) {
+            // the row's m moves to the tile's maximum where that is larger by more than kRescale (or the first)
+            const bool move = (tile_m - m) * c > kRescale;   // at m = -inf too, unless tile_m is -inf as well
+            if (__any_sync(0xffffffffu, move)) {
+              // by the products that the probabilities are relative to, or by the exact difference where those are
+              const float f = !move ? 1.0f : ex2(far() ? (m - tile_m) * c : __fmul_rn(m, c) - __fmul_rn(tile_m, c));
+              if (any) {   // the PV before is complete: its issuer committed the scores after it
+#pragma unroll 1
+                for (int q = 0; q < HD / 32; ++q) {
+                  uint32_t(&o)[32] = s[0];
+                  tmem_ld32_nowait(t_o + q * 32, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                  tmem_st32(t_o + q * 32, o);
+                }
+                tmem_wait_st();
+              }
+              if (move) m = tile_m;
+              l *= f;
+            }
+            if (__any_sync(0xffffffffu, far())) {
+              const float sub = m > -INFINITY ? m : 0.0f;
+#pragma unroll 1
+              for (int q = 0; q < 4; ++q) {
+                tmem_ld32_nowait(t_s + q * 32, s[0]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) s[0][i] = __float_as_uint(__uint_as_float(s[0][i]) - sub);
+                tmem_st32(t_s + q * 32, s[0]);
+              }
+              tmem_wait_st();
+              c_off = 0.0f;
+            }
+          }
+          const float sub = m > -INFINITY ? m * c_off : 0.0f;
           uint64_t l2[2] = {0ull, 0ull};   // two fp32 sums each
           const uint64_t c2 = f32x2(c, c), sub2 = f32x2(-sub, -sub);
           float mx[2] = {-INFINITY, -INFINITY};
@@ -1412,7 +1439,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int i = 0; i < 16; ++i) {
               const uint32_t s0 = s[q & 1][2 * i], s1 = s[q & 1][2 * i + 1];
               mx[i & 1] = max3(mx[i & 1], __uint_as_float(s0), __uint_as_float(s1));
-              const uint64_t x = mul2(add2(u32x2(s0, s1), sub2), c2);
+              const uint64_t x = fma2(u32x2(s0, s1), c2, sub2);
               const float p0 = ex2(__uint_as_float(static_cast<uint32_t>(x))), p1 = ex2(__uint_as_float(static_cast<uint32_t>(x >> 32)));
               l2[i & 1] = add2(l2[i & 1], f32x2(p0, p1));
               p[q][i] = pack2<T>(p0, p1);
@@ -1421,7 +1448,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const uint64_t t2 = add2(l2[0], l2[1]);
           tile_l = __uint_as_float(static_cast<uint32_t>(t2)) + __uint_as_float(static_cast<uint32_t>(t2 >> 32));
           tile_m = fmaxf(mx[0], mx[1]);
-        } while (move_m());
+          settle = c_off > 0.0f && __any_sync(0xffffffffu, (tile_m - m) * c > kRescale);
+          if (!settle) break;
+        }
         l += tile_l;
         any = true;
 #pragma unroll
@@ -1445,11 +1474,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const volatile int* met = seg_bad + 2 * (n_seg & 1u);
       if (!ok || met[0] || met[1] || (!wk.prefix && wk.s.bad)) l = quiet_nan();
       const bool read = ok && any;   // warp-uniform
-      // l and O are sums of exp2(s c - m c): what the product loses when it is rounded for the join they take on
-      const float m_c = m * c;
-      const float fix = fabsf(m_c) < INFINITY ? ex2(fminf(fmaxf(fmaf(m, c, -m_c), -60.0f), 60.0f)) : 1.0f;
-      m = m_c;
-      l *= fix;
       if (alt && team == 1) {
         join_ml[r128] = make_float2(m, l);
         if (read) {
@@ -1459,21 +1483,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             tmem_ld32_nowait(t_o + q * 32, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) join[(q * 32 + i) * 128 + r128] = __uint_as_float(o[i]) * fix;
+            for (int i = 0; i < 32; ++i) join[(q * 32 + i) * 128 + r128] = __uint_as_float(o[i]);
           }
         }
       }
       if (alt) named_bar_sync(1, 256);
       if (!alt || team == 0) {
-        float f0 = fix, f1 = 0.0f;
+        float f0 = 1.0f, f1 = 0.0f;
         const bool both = alt && cnt > 1;
         if (both) {
           const float2 other = join_ml[r128];
           const float M = fmaxf(m, other.x), sub = M > -INFINITY ? M : 0.0f;
-          const float f = ex2(m - sub);
-          f0 = fix * f;
-          f1 = ex2(other.x - sub);
-          l = l * f + other.y * f1;
+          f0 = ex2((m - sub) * c);
+          f1 = ex2((other.x - sub) * c);
+          l = l * f0 + other.y * f1;
           m = M;
         }
         const bool starts = pc.starts, ends = pc.ends;
@@ -1497,10 +1520,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
           float x[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]) * f0;
+          for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]);
           if (both) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] += join[(q * 32 + i) * 128 + r128] * f1;
+            for (int i = 0; i < 32; ++i) x[i] = x[i] * f0 + join[(q * 32 + i) * 128 + r128] * f1;
           }
           if (on && direct) {
 #pragma unroll
@@ -1515,7 +1538,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         }
         if (on && direct) {
-          if (a.lse) a.lse[row] = isnan(l) ? l : l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+          if (a.lse) a.lse[row] = isnan(l) ? l : l > 0.0f ? (m * c + log2f(l)) * 0.6931471805599453f : -INFINITY;
         } else if (on) {
           *part.ml = make_float2(m, l);
         }
@@ -1713,9 +1736,9 @@ struct CombineWork {
 };
 
 // (M, L, O) of a row over some parts, joined with that over others.
-__device__ __forceinline__ void join_parts(float& M, float& L, float4 (&o)[4], float m2, float l2, const float4 (&o2)[4]) {
+__device__ __forceinline__ void join_parts(float c, float& M, float& L, float4 (&o)[4], float m2, float l2, const float4 (&o2)[4]) {
   const float M1 = fmaxf(M, m2), base = M1 > -INFINITY ? M1 : 0.0f;
-  const float f = ex2(M - base), g = ex2(m2 - base);
+  const float f = ex2((M - base) * c), g = ex2((m2 - base) * c);
   M = M1;
   L = L * f + l2 * g;   // a poisoned part is NaN whatever its weight
 #pragma unroll
@@ -1764,6 +1787,7 @@ __global__ void __launch_bounds__(DIMS * 2 * SPLIT) combine_kernel(const __grid_
   if (n_own == 1 && !w.share) n_own = 0;   // written where it was computed
   const int n = n_pre + n_own;
   if (__all_sync(0xffffffffu, n <= 0)) return;   // the same in all warps
+  const float c = score_scale(a);
   float M = -INFINITY, L = 0.0f;
   float4 o[4];
 #pragma unroll
@@ -1794,7 +1818,7 @@ __global__ void __launch_bounds__(DIMS * 2 * SPLIT) combine_kernel(const __grid_
       }
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) join_parts(M, L, o, ml[u].x, ml[u].y, x[u]);
+    for (int u = 0; u < kUnroll; ++u) join_parts(c, M, L, o, ml[u].x, ml[u].y, x[u]);
   }
   for (int other = n_rows; other < 32; other <<= 1) {   // lanes that took other parts of the row
     float4 o2[4];
@@ -1803,7 +1827,7 @@ __global__ void __launch_bounds__(DIMS * 2 * SPLIT) combine_kernel(const __grid_
     for (int q = 0; q < 4; ++q)
       o2[q] = make_float4(__shfl_xor_sync(0xffffffffu, o[q].x, other), __shfl_xor_sync(0xffffffffu, o[q].y, other),
                           __shfl_xor_sync(0xffffffffu, o[q].z, other), __shfl_xor_sync(0xffffffffu, o[q].w, other));
-    join_parts(M, L, o, m2, l2, o2);
+    join_parts(c, M, L, o, m2, l2, o2);
   }
   if constexpr (SPLIT > 1) {
 #pragma unroll
@@ -1827,7 +1851,7 @@ __global__ void __launch_bounds__(DIMS * 2 * SPLIT) combine_kernel(const __grid_
         float4 o2[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) o2[q] = make_float4(src[2 + 4 * q][x], src[3 + 4 * q][x], src[4 + 4 * q][x], src[5 + 4 * q][x]);
-        join_parts(M, L, o, src[0][x], src[1][x], o2);
+        join_parts(c, M, L, o, src[0][x], src[1][x], o2);
       }
       __syncthreads();
     }
@@ -1842,7 +1866,7 @@ __global__ void __launch_bounds__(DIMS * 2 * SPLIT) combine_kernel(const __grid_
     dst[q / 2] = make_uint4(pack2<T>(o[q].x * inv, o[q].y * inv), pack2<T>(o[q].z * inv, o[q].w * inv),
                             pack2<T>(o[q + 1].x * inv, o[q + 1].y * inv), pack2<T>(o[q + 1].z * inv, o[q + 1].w * inv));
   if (a.lse && warp == 0)
-    a.lse[static_cast<int64_t>(t) * a.H + h] = isnan(L) ? L : L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+    a.lse[static_cast<int64_t>(t) * a.H + h] = isnan(L) ? L : L > 0.0f ? (M * c + log2f(L)) * 0.6931471805599453f : -INFINITY;
 }
 
 // ---- host ------------------------------------------------------------------------------------

@@ -37,7 +37,7 @@ def test_tree_bits_of_full_words():
 
 @pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("big", [2.0 ** 11, 2.0 ** 12, 2.0 ** 13, 2.0 ** 14, 2.0 ** 15])
-@pytest.mark.parametrize("n", [20, 40])
+@pytest.mark.parametrize("n", [1, 6, 20, 40])
 def test_scores_of_any_size(n, big, dtype):
     """Scores whose fp32 neighbours lie far apart: two keys one step of the sum (8 at 2^26) from each other.  The larger
     one takes all the weight, and no probability overflows on the way."""
