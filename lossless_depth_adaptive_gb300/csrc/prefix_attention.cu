@@ -141,6 +141,22 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Probabilities go to the tensor cores in 16 bits, one number each: off by half a step, 2^-8 in bf16 and 2^-11 in fp16,
+// where a pair of numbers would be exact for twice the products with V and no room in TMEM for it.  In fp16 half a
+// step is 2^-11 of a number down to 2^-14 only.  So fp16 probabilities are exp2(c (s - m) + kUp), a factor that O and l
+// share, and m, otherwise the largest score so far, comes down to that of a key tile which stays kDrop and more below
+// it: the weights of a tile are rounded relative to the tile's own, not to one key's far above (with values near zero
+// there, what an attention sink is, the others' sum is the result).  kDeep bounds the way down, so that fp32 holds what
+// the far key's weight is then.  In rows_kernel that takes 42.0 us instead of 41.0 for 32 sequences of 32 heads behind
+// 4096 positions, in tile_kernel nothing that shows.
+template <typename T> constexpr bool kIsHalf = std::is_same<T, __half>::value;
+template <typename T> constexpr float kUp = kIsHalf<T> ? 7.0f : 0.0f;
+constexpr float kDrop = 10.0f, kDeep = 60.0f;
+// lse of a row: log of the sum that (m, l) stand for
+template <typename T>
+__device__ __forceinline__ float log_sum(float m, float l, float c) {
+  return isnan(l) ? l : l > 0.0f ? (m * c + (log2f(l) - kUp<T>)) * 0.6931471805599453f : -INFINITY;
+}
 // c of the scores; a zero scale zeroes them instead.
 __device__ __forceinline__ float score_scale(const PrefixAttnArgs& a) {
   return a.scale_log2 == 0.0f ? 1.0f : fabsf(a.scale_log2);
@@ -844,6 +860,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
     float* ssum = reinterpret_cast<float*>(smem + SM::oSum);
     const uint32_t sp = smem_u32(smem + SM::oP);
     const float c = score_scale(a), sign = a.scale_log2 > 0.0f ? 1.0f : a.scale_log2 < 0.0f ? -1.0f : 0.0f;
+    const float drop = kDrop / c, depth = kDeep / c;   // of scores
     uint32_t phase = 0, n_seg = 0;
     int st = 0;
     bool ok = true;
@@ -868,6 +885,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
       }
       float o[MT][NV][4];
       float m[MT][2], l[MT][2];
+      float low[MT][2], deep[MT][2];   // fp16: m comes down to a tile's maximum between these two
       int seen_by_all = 0x7fffffff;   // keys up to this one are seen by every row of this thread
 #pragma unroll
       for (int u = 0; u < MT; ++u) {
@@ -876,7 +894,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int r = u * 16 + gr + 8 * h;
-          m[u][h] = -INFINITY;
+          m[u][h] = low[u][h] = deep[u][h] = -INFINITY;
           l[u][h] = 0.0f;
           if (r < d.rows) seen_by_all = min(seen_by_all, rd[r].last);
         }
@@ -956,14 +974,22 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int r = u * 16 + gr + 8 * h;
-            float mx = m[u][h];
+            float mx = -INFINITY;
 #pragma unroll
             for (int k = 0; k < kRowsWarps; ++k) mx = fmaxf(mx, smax[k * SM::kRows + r]);
+            if constexpr (kIsHalf<T>) {
+              const float tile_m = mx;
+              if (!(mx > m[u][h] || (mx < low[u][h] && mx > deep[u][h]))) mx = m[u][h];
+              low[u][h] = mx - drop;
+              deep[u][h] = fmaxf(deep[u][h], tile_m - depth);
+            } else {
+              mx = fmaxf(mx, m[u][h]);
+            }
             const float base = mx > -INFINITY ? mx : 0.0f;
             const float f = ex2((m[u][h] - base) * c);
             m[u][h] = mx;
-            const float p0 = ex2((x[u][h][0] - base) * c), p1 = ex2((x[u][h][1] - base) * c);
-            const float p2 = ex2((x[u][h][2] - base) * c), p3 = ex2((x[u][h][3] - base) * c);
+            auto prob = [&](float s) { return ex2(fmaf(s - base, c, kUp<T>)); };
+            const float p0 = prob(x[u][h][0]), p1 = prob(x[u][h][1]), p2 = prob(x[u][h][2]), p3 = prob(x[u][h][3]);
             l[u][h] = l[u][h] * f + ((p0 + p1) + (p2 + p3));
 #pragma unroll
             for (int n = 0; n < NV; ++n) {
@@ -1038,8 +1064,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
             for (int n = 0; n < NV; ++n)
               *reinterpret_cast<uint32_t*>(dst + n * 8) = pack2<T>(o[u][n][2 * h] * inv, o[u][n][2 * h + 1] * inv);
             if (a.lse && warp == 0 && tq == 0)
-              a.lse[static_cast<int64_t>(t) * a.H + head] =
-                  isnan(L) ? L : L > 0.0f ? (m[u][h] * c + log2f(L)) * 0.6931471805599453f : -INFINITY;
+              a.lse[static_cast<int64_t>(t) * a.H + head] = log_sum<T>(m[u][h], L, c);
           } else {
             const PartRef p = whole ? joined_part<HD>(prefix ? w.pre_o : w.own_o, prefix ? w.pre_ml : w.own_ml, d.kvh, rows_all,
                                                       t * a.G + hg)
@@ -1071,7 +1096,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
 // and take alternate key tiles, and join at the segment's end.  Either way one team's softmax runs
 // while the tensor cores work for the other.
 // The running maximum of a row moves only when a score exceeds it by more than 2^8 (P then stays
-// within 2^8, which both 16-bit types hold), so O is rescaled rarely: a rescale reads and writes
+// within 2^8, in fp16 within 2^15), so O is rescaled rarely: a rescale reads and writes
 // all of it through registers between two MMAs.  c s - c m is one FMA with the rounded product c m, which is good
 // while that is off by far less than one; of rows with larger products (kFar) the scores in TMEM are replaced by
 // s - m first.  Difference and product apart for every score: 3.5 us more of 203 for 1752 prompt tokens behind
@@ -1079,6 +1104,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
 // ============================================================================================
 constexpr int kTileThreads = 384;   // two softmax teams; producer, an MMA issuer for each team, an idle warp
 constexpr float kRescale = 8.0f;
+constexpr float kMostSum = 1099511627776.0f;   // 2^40: m comes down to a tile's (fp16) while l is below this
 constexpr float kFar = 1048576.0f;   // 2^20, where fp32 neighbours are 2^-3 apart
 
 
@@ -1336,6 +1362,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         uint32_t s[2][32];
         float tile_l, tile_m = -INFINITY;   // sum and maximum of this tile
         float c_off = c;                    // 0 when the scores in TMEM are s - m
+        auto moves = [&] {
+          const float d = (tile_m - m) * c;
+          // at m = -inf too, unless tile_m is -inf as well
+          return d > kRescale || (kIsHalf<T> && d < -kDrop && d > -kDeep && l < kMostSum);
+        };
         auto far = [&] { return m > -INFINITY && fabsf(m) * c >= kFar; };
         // m and the scores have to be looked at before P: masked scores, or such a row
         bool settle = !__all_sync(0xffffffffu, whole && rv.last >= key0 + kTileKeys - 1 && !far());
@@ -1392,8 +1423,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         uint32_t p[4][16];
         for (;;) {
           if (settle) {
-            // the row's m moves to the tile's maximum where that is larger by more than kRescale (or the first)
-            const bool move = (tile_m - m) * c > kRescale;   // at m = -inf too, unless tile_m is -inf as well
+            // the row's m moves to the tile's maximum where that is larger by more than kRescale (or the first), and
+            // in fp16 where it is smaller by more than kDrop
+            const bool move = moves();
             if (__any_sync(0xffffffffu, move)) {
               // by the products that the probabilities are relative to, or by the exact difference where those are
               const float f = !move ? 1.0f : ex2(far() ? (m - tile_m) * c : __fmul_rn(m, c) - __fmul_rn(tile_m, c));
@@ -1426,7 +1458,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               c_off = 0.0f;
             }
           }
-          const float sub = m > -INFINITY ? m * c_off : 0.0f;
+          const float sub = (m > -INFINITY ? m * c_off : 0.0f) - kUp<T>;
           uint64_t l2[2] = {0ull, 0ull};   // two fp32 sums each
           const uint64_t c2 = f32x2(c, c), sub2 = f32x2(-sub, -sub);
           float mx[2] = {-INFINITY, -INFINITY};
@@ -1448,7 +1480,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const uint64_t t2 = add2(l2[0], l2[1]);
           tile_l = __uint_as_float(static_cast<uint32_t>(t2)) + __uint_as_float(static_cast<uint32_t>(t2 >> 32));
           tile_m = fmaxf(mx[0], mx[1]);
-          settle = c_off > 0.0f && __any_sync(0xffffffffu, (tile_m - m) * c > kRescale);
+          settle = c_off > 0.0f && __any_sync(0xffffffffu, moves());
           if (!settle) break;
         }
         l += tile_l;
@@ -1538,7 +1570,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         }
         if (on && direct) {
-          if (a.lse) a.lse[row] = isnan(l) ? l : l > 0.0f ? (m * c + log2f(l)) * 0.6931471805599453f : -INFINITY;
+          if (a.lse) a.lse[row] = log_sum<T>(m, l, c);
         } else if (on) {
           *part.ml = make_float2(m, l);
         }
@@ -1866,7 +1898,7 @@ __global__ void __launch_bounds__(DIMS * 2 * SPLIT) combine_kernel(const __grid_
     dst[q / 2] = make_uint4(pack2<T>(o[q].x * inv, o[q].y * inv), pack2<T>(o[q].z * inv, o[q].w * inv),
                             pack2<T>(o[q + 1].x * inv, o[q + 1].y * inv), pack2<T>(o[q + 1].z * inv, o[q + 1].w * inv));
   if (a.lse && warp == 0)
-    a.lse[static_cast<int64_t>(t) * a.H + h] = isnan(L) ? L : L > 0.0f ? (M * c + log2f(L)) * 0.6931471805599453f : -INFINITY;
+    a.lse[static_cast<int64_t>(t) * a.H + h] = log_sum<T>(M, L, c);
 }
 
 // ---- host ------------------------------------------------------------------------------------

@@ -5,8 +5,8 @@ import pytest
 import torch
 
 from gpu_util import require_gpu
-from paged_ref import HALF
-from test_gpu_paged import BF, FP, SHARED, run_case
+from paged_ref import HALF, attention, gather
+from test_gpu_paged import BF, FP, SHARED, compare, paged, run_case
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +66,70 @@ def test_scores_of_any_size(n, big, dtype):
         assert bool(((out.double() - want).abs() <= want.abs() * (2.01 * HALF[dtype]) + 10 * math.exp(-16.0)).all())
         top = (big * big + step) * abs(scale)
         assert bool(((lse.cpu().double() - top).abs() <= top * 2.0 ** -21).all())
+
+
+def below_a_peak(G, hd, dtype, n, batch, length, nats, at, prefix=0, sign=1.0):
+    """A key at each position of `at` whose score lies `nats` above all the others' and whose value is zero: the result
+    is what the others' weights, exp(-nats) and less each, add up to.  Sequences of the same pages and queries, so that
+    a thread block takes many tiles of one; with a prefix they end at different positions behind it."""
+    dexlib = require_gpu()
+    kvh, ps = 2, 64
+    gen = torch.Generator().manual_seed(int(nats) + n)
+    _, pages, table = paged(dexlib, kvh, hd, ps, [length], dtype)
+    pages[:, 0] *= 0.25
+    pages[:, 0, :, :, 0] = 0.0
+    pages[:, 1] = pages[:, 1].abs()
+    for p in at:
+        page, row = int(table[0, p // ps]), p % ps
+        pages[page, 0, :, row] = 0.0
+        pages[page, 0, :, row, 0] = sign * nats * hd ** 0.5 / 8.0
+        pages[page, 1, :, row] = 0.0
+    cache = dexlib.PagedCache(pages.cuda(), table.expand(batch, -1).contiguous().cuda())
+    q = torch.randn((n, kvh * G, hd), generator=gen) * 0.25
+    q[:, :, 0] = 8.0
+    q = q.to(dtype)
+    every = q.repeat(batch, 1, 1).cuda()
+    start = (torch.arange(batch + 1) * n).int()
+    lens = [length - (b % 3 if prefix else 0) for b in range(batch)]
+    lse = torch.zeros(every.shape[:2], device="cuda")
+    scale = sign * hd ** -0.5
+    out = cache.attention(every, start.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), n, prefix, lse=lse, scale=scale)
+    for size in sorted(set(lens)):
+        o, L, bo, bl = attention(pages, table, q, start[:2], [size], scale=scale)
+        if dtype == FP:
+            # A probability in fp16 is also off by half a step of its smallest numbers, 2^-25.  The kernels take them
+            # relative to a tile's largest score so that this one comes to 2^-3 or more, and to 2^7 or more where it
+            # raises the running maximum (the peak): a weight is off by 2^-22 of its tile's largest one, in the
+            # peak's tile by 2^-32 of the peak's.
+            k, v = gather(pages, table[0], size)
+            for h in range(kvh * G):
+                s = (q[:, h].double() @ k[:, h // G].T) * scale
+                w = torch.exp(s - L[:, h][:, None])
+                w[:, [p for p in at if p < size]] = 0.0
+                # twice the sum of the largest weight of every 64 keys bounds that of any tiles of 64 or 128
+                top = torch.stack([x.amax(-1) for x in w.split(64, dim=1)]).sum(0) * 2
+                bo[:, h] += (128 * v.abs().max() * (2.0 ** -22 * top + 2.0 ** -32 * len(at)))[:, None]
+        for b in [b for b in range(batch) if lens[b] == size]:
+            compare(out[b * n:(b + 1) * n], lse[b * n:(b + 1) * n], (o, L, bo, bl), torch.ones(n, dtype=torch.bool))
+
+
+@pytest.mark.parametrize("dtype,hd", [(FP, 128), (FP, 64), (BF, 128)])
+@pytest.mark.parametrize("nats", [8.0, 13.0, 17.0, 21.0])
+@pytest.mark.parametrize("n", [1, 6, 20, 70])
+def test_weights_far_below_a_peak(n, nats, dtype, hd):
+    """One key far above thousands of others: at the front, in the middle, near the end, several of them; single
+    tokens and a few (rows_kernel), longer runs that share a row tile and that fill two (tile_kernel)."""
+    for at in ([0], [1500], [2900], [0, 1000, 1501]):
+        below_a_peak(4, hd, dtype, n, 40, 2930 + n, nats, at)
+
+
+@pytest.mark.parametrize("G", [1, 4])
+@pytest.mark.parametrize("nats", [13.0, 17.0])
+def test_weights_below_a_peak_in_a_shared_prefix(G, nats):
+    """The same behind a prefix that is read once, by either kernel, with the peak in it and behind it."""
+    for at in ([0], [20000, 32775]):
+        below_a_peak(G, 64, FP, 1, 16, 32790, nats, at, prefix=32768)
+
+
+def test_weights_below_a_peak_negative_scale():
+    below_a_peak(4, 128, FP, 20, 40, 2000, 17.0, [700], sign=-1.0)
