@@ -5,6 +5,7 @@
 #include "../../include/dex.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "rope_angle.h"
 
 namespace dex {
 
@@ -48,7 +49,8 @@ __device__ __forceinline__ Vec8<T> load8(const T* p) {
 // 1 as a 64-bit fixed-point fraction, r times it modulo 2^64 is the fraction of a turn left after
 // whole turns, exactly -- an fp32 product r * frequency would be off by 2^-24 r radians (0.06 at
 // r = 10^6).  Its upper 32 bits as a signed number are half-turns in units of 2^-31.  theta^(-2j/HD)
-// is the product of the powers theta^(-2 2^b / HD) over the bits b of j, each a 64-bit fraction.
+// is the product of the powers theta^(-2 2^b / HD) over the bits b of j, each a 64-bit fraction: at position 2^31
+// the turn is off by at most 2^-27, and what is left of the error is that of fp32 (2^-21.4 of a row's value).
 template <typename CT, typename IT, int HD>
 __global__ void __launch_bounds__(32 * kAppendWarps, 8) paged_append_kernel(const __grid_constant__ AppendArgs a, int rows) {
   constexpr int kItems = HD / 16, kStep = 32 / kItems;   // items per head row, rows of one pass of the warp
@@ -239,10 +241,8 @@ extern "C" int dex_paged_append(const dex_paged_kv* kv, const dex_append_args* a
   d.rotate = a->rope_theta != 0.0f;
   d.rejected = rejected;
   if (d.rotate) {
-    // powers of 53 bits: at position 2^31 the angle is off by at most 2^-23 of a turn
-    d.turn = static_cast<uint64_t>(0.15915494309189535 * 18446744073709551616.0);   // 2^64 / 2 pi
-    double f = pow(static_cast<double>(a->rope_theta), -2.0 / kv->head_dim);
-    for (int b = 0; b < 6; ++b, f *= f) d.power[b] = f < 1.0 ? static_cast<uint64_t>(f * 18446744073709551616.0) : ~uint64_t(0);
+    d.turn = dex::kTurnPerRadian;
+    dex::rope_powers(a->rope_theta, kv->head_dim, d.power);
   }
   return dex::launch_paged_append(d, st) == cudaSuccess ? DEX_OK : DEX_ECUDA;
 }

@@ -1,4 +1,5 @@
 """GPU tests of the paged-cache operators at the edges of their masks, scores and angles."""
+import decimal
 import math
 
 import pytest
@@ -133,3 +134,34 @@ def test_weights_below_a_peak_in_a_shared_prefix(G, nats):
 
 def test_weights_below_a_peak_negative_scale():
     below_a_peak(4, 128, FP, 20, 40, 2000, 17.0, [700], sign=-1.0)
+
+
+def turn_of(theta, pos, hd):
+    """The angles pos * theta^(-2j/hd), j < hd/2, in radians modulo a turn, from 60 digits."""
+    with decimal.localcontext() as ctx:
+        ctx.prec = 60
+        pi = decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+        log = decimal.Decimal(theta).ln()
+        turns = [((decimal.Decimal(-2 * j) / hd * log).exp() * pos / (2 * pi)) for j in range(hd // 2)]
+        return [float((t - t.to_integral_value()) * 2 * pi) for t in turns]
+
+
+@pytest.mark.parametrize("theta", [1.0, 1.0001, 1.01, 1.1, 2.0, 10.0, 1e4, 5e5, 1e6, 3e38])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_far_rotations(hd, theta):
+    """Angles at the farthest positions: the pair (sin a, cos a) turned by a is (0, 1), and what is left of the zero
+    is the error of the angle."""
+    dexlib = require_gpu()
+    theta = torch.tensor(theta).item()   # as the call takes it, in 32 bits
+    rope = [0, 1, 17, 131072, 10 ** 8 + 7, 2 ** 30, 2 ** 31 - 1, 2 ** 31 - 12345, -1, -(2 ** 31)]
+    n = len(rope)
+    angle = torch.tensor([turn_of(theta, r, hd) for r in rope], dtype=torch.float64)
+    x = torch.cat((angle.sin(), angle.cos()), 1).float()[:, None].contiguous().cuda()
+    cache = dexlib.PagedCache(torch.zeros((1, 2, 1, 16, hd), dtype=FP, device="cuda"), torch.zeros((1, 1), dtype=torch.int32, device="cuda"))
+    seq, pos = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.arange(n, dtype=torch.int32, device="cuda")
+    cache.append(x, x, seq, pos, theta=theta, rope_pos=torch.tensor(rope, dtype=torch.int32, device="cuda"))
+    got = cache.pages[0, 0, 0, :n].cpu().double()
+    # The angle in fp32 half-turns is off by pi 2^-25, sin and cos by two units in the last place (2^-23 of 1), the products and
+    # inputs by half of one: 2^-21.4 together, and half a step of fp16 (2^-25 below 2^-14) for the result.
+    assert got[:, :hd // 2].abs().max().item() <= 2.0 ** -21 + 2.0 ** -25
+    assert (got[:, hd // 2:] - 1.0).abs().max().item() <= 2.0 ** -11 + 2.0 ** -21
