@@ -354,8 +354,9 @@ int dex_prefix_attention_workspace(const dex_paged_kv* kv, const dex_attention_a
  * second product in the cache's type.  Rows of out and lse that belong to no sequence are
  * left as they were; out must not overlap q.  Keys and values at positions below seq_len, and with
  * prefix_len > 0 below that, must be finite, seen by a query or not; what pages hold beyond is never
- * used.  The lengths must not change while the call runs.  A page id that is out of range is never followed: the rows that need
- * it become NaN and status gets DEX_ATTN_BAD_PAGE.  A sequence whose seq_len is negative or beyond the
+ * used.  The lengths must not change while the call runs.  A page id that is out of range is never followed: the rows that see
+ * a position on such a page, in the table it is read through, become NaN, all others are unaffected, and status gets
+ * DEX_ATTN_BAD_PAGE.  A sequence whose seq_len is negative or beyond the
  * table gets NaN rows, one whose queries exceed max_q or n_tokens is skipped, both with DEX_ATTN_BAD_RANGE.
  * workspace: device, 256-byte aligned, at least the bytes dex_prefix_attention_workspace gives
  * (DEX_ECAPACITY otherwise); calls that may overlap on the GPU need workspaces of their own.

@@ -408,6 +408,19 @@ __device__ __forceinline__ uint32_t seen_bits(const RowView& v, int lo, int hi, 
   return bits & range_bits(lo - at, hi - at);
 }
 
+// Whether a row sees one of the keys [lo, hi) whose page in the table has an id out of range.  Asked only where a
+// segment has met such a page: its keys and values are zeros there, so the rows that do not see it are right.
+__device__ __forceinline__ bool sees_bad_page(const PagedKv& kv, const int32_t* table, RowView v, int lo, int hi) {
+  for (int entry = lo >> kv.page_shift; (entry << kv.page_shift) < hi; ++entry) {
+    const int id = table[entry];
+    if (id >= 0 && id < kv.n_pages) continue;
+    const int begin = max(lo, entry << kv.page_shift), end = min(hi, (entry + 1) << kv.page_shift);
+    for (int at = begin; at < end; at += 32)
+      if (seen_bits(v, begin, end, at)) return true;
+  }
+  return false;
+}
+
 // Own units of every sequence, as running totals in cum[0 .. batch]; the block's threads together.
 // scratch: a word per warp.  token_seq (at most 64 tokens, or null) receives each token's sequence.
 // Returns the total number of units of the kernel.
@@ -623,7 +636,8 @@ struct PageLoader {
 struct alignas(16) SegDesc {
   int32_t rows, mt, lo, hi;
   int32_t key0, cnt, kvh, flags;            // key0: first tile's first position; flags: kSeg* bits
-  int32_t info, range, last_range, pad;     // entry of pre_info / own_info, the range, that of the last tile (first part only)
+  int32_t info, range, last_range, seq;     // entry of pre_info / own_info, the range, that of the last tile (first
+                                            // part only), the sequence (own segments)
 };
 constexpr int kSegPrefix = 1, kSegStarts = 2, kSegEnds = 4, kSegBad = 8, kSegLast = 16;
 struct alignas(16) RowDesc {
@@ -788,7 +802,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
                                (!wk.prefix && wk.s.bad ? kSegBad : 0) |
                                (!w.queue && range + gridDim.x >= sh.ctas && g1 - g - pc.units <= kRowsSegCost ? kSegLast : 0));
           d[2] = make_int4(wk.prefix ? wk.seg : wk.own_info_index(), range,
-                           pc.starts ? sh.owner(g - static_cast<uint32_t>(off) + wk.units() - 1) : 0, 0);
+                           pc.starts ? sh.owner(g - static_cast<uint32_t>(off) + wk.units() - 1) : 0, wk.prefix ? 0 : wk.b);
           mbar_arrive_expect_tx(&seg_full[slot], static_cast<uint32_t>(wk.rows * HD * 2));
         }
         __syncwarp();
@@ -899,7 +913,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
           if (r < d.rows) seen_by_all = min(seen_by_all, rd[r].last);
         }
       }
-      bool bad = d.flags & kSegBad;
+      bool bad = false;   // it has met a bad page
       for (int i = 0; i < d.cnt; ++i) {
         // ---- scores of this warp's 16 keys ----
         const int kst = st;
@@ -1030,6 +1044,18 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
         if (lane == 0) mbar_arrive(&empty[vst]);
       }
       // ---- the segment's result ----
+      uint32_t poison = !ok || (d.flags & kSegBad) ? 0xffffffffu : 0u;   // a bit for each of this thread's rows
+      if (bad) {
+        const int32_t* table = d.flags & kSegPrefix ? a.prefix_table : a.kv.table + static_cast<int64_t>(d.seq) * a.kv.table_stride;
+#pragma unroll 1
+        for (int i = 0; i < 2 * MT; ++i) {
+          const int r = (i >> 1) * 16 + gr + 8 * (i & 1);
+          if (r < d.rows && sees_bad_page(a.kv, table, RowView{rd[r].last, rd[r].first, rd[r].word, true}, max(d.lo, d.key0),
+                                          min(d.hi, d.key0 + d.cnt * kRowsTile)))
+            poison |= 1u << i;
+        }
+        __syncwarp();
+      }
 #pragma unroll
       for (int u = 0; u < MT; ++u) {
         if (u >= d.mt) break;
@@ -1037,7 +1063,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
         for (int h = 0; h < 2; ++h) {
           l[u][h] += __shfl_xor_sync(0xffffffffu, l[u][h], 1);
           l[u][h] += __shfl_xor_sync(0xffffffffu, l[u][h], 2);
-          if (bad || !ok) l[u][h] = quiet_nan();
+          if (poison >> (2 * u + h) & 1u) l[u][h] = quiet_nan();
           if (tq == 0) ssum[warp * SM::kRows + u * 16 + gr + 8 * h] = l[u][h];
         }
       }
@@ -1103,6 +1129,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
 // 8192 positions.
 // ============================================================================================
 constexpr int kTileThreads = 384;   // two softmax teams; producer, an MMA issuer for each team, an idle warp
+constexpr int kMetBadPage = 1, kMetTimeout = 2;   // what an issuer has met in a segment
 constexpr float kRescale = 8.0f;
 constexpr float kMostSum = 1099511627776.0f;   // 2^40: m comes down to a tile's (fp16) while l is below this
 constexpr float kFar = 1048576.0f;   // 2^20, where fp32 neighbours are 2^-3 apart
@@ -1227,7 +1254,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   volatile int* bad_stage = reinterpret_cast<volatile int*>(smem + SM::oMisc);
   uint32_t* scratch = reinterpret_cast<uint32_t*>(smem + SM::oMisc) + SM::kStages;
   uint32_t* tmem_slot = scratch + 12;
-  volatile int* seg_bad = reinterpret_cast<volatile int*>(tmem_slot + 1);   // [2 segments][2 teams] it met a bad page (before o_full)
+  volatile int* seg_met = reinterpret_cast<volatile int*>(tmem_slot + 1);   // [2 segments][2 teams] kMet* bits (before o_full)
   uint32_t* cum = reinterpret_cast<uint32_t*>(smem + SM::oRing);
   const PrefixAttnArgs& a = w.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1503,8 +1530,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
       if (r128 == 0 && any) free_stage(v_stage, alt);
-      const volatile int* met = seg_bad + 2 * (n_seg & 1u);
-      if (!ok || met[0] || met[1] || (!wk.prefix && wk.s.bad)) l = quiet_nan();
+      const volatile int* met = seg_met + 2 * (n_seg & 1u);
+      const int met_any = met[0] | met[1];
+      if (!ok || (met_any & kMetTimeout) || (!wk.prefix && wk.s.bad)) l = quiet_nan();
+      if (met_any & kMetBadPage) {
+        const int32_t* table = wk.prefix ? a.prefix_table : a.kv.table + static_cast<int64_t>(wk.b) * a.kv.table_stride;
+        const int at = (wk.k.t0 + tile) * kTileKeys;
+        if (on && sees_bad_page(a.kv, table, rv, max(wk.k.lo, at), min(wk.k.hi, at + cnt * kTileKeys))) l = quiet_nan();
+        __syncwarp();
+      }
       const bool read = ok && any;   // warp-uniform
       if (alt && team == 1) {
         join_ml[r128] = make_float2(m, l);
@@ -1732,7 +1766,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         // The teams read it after o_full.  The word was last that of the segment before the last one, which every
         // warp had read before it let o_full of the last one complete, and q_full came after that.
-        seg_bad[2 * (n_seg & 1u) + team] = bad || !ok;
+        seg_met[2 * (n_seg & 1u) + team] = (bad ? kMetBadPage : 0) | (ok ? 0 : kMetTimeout);
         umma_commit(o_full);
         mbar_arrive(o_full);
         g += pc.units;

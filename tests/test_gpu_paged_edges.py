@@ -7,7 +7,7 @@ import torch
 
 from gpu_util import require_gpu
 from paged_ref import HALF, attention, gather
-from test_gpu_paged import BF, FP, SHARED, compare, paged, run_case
+from test_gpu_paged import BF, FP, SHARED, compare, paged, queries, run_case
 
 pytestmark = pytest.mark.gpu
 
@@ -165,3 +165,64 @@ def test_far_rotations(hd, theta):
     # inputs by half of one: 2^-21.4 together, and half a step of fp16 (2^-25 below 2^-14) for the result.
     assert got[:, :hd // 2].abs().max().item() <= 2.0 ** -21 + 2.0 ** -25
     assert (got[:, hd // 2:] - 1.0).abs().max().item() <= 2.0 ** -11 + 2.0 ** -21
+
+
+def bad_page_case(H, kvh, hd, ps, dtype, lens, new, bad, prefix=0, tree=None):
+    """Pages of `bad` (sequence or None for all, table entry) out of range: the rows that see a position on one of them
+    are NaN, and all others as if nothing had happened."""
+    dexlib = require_gpu()
+    cache, pages, table = paged(dexlib, kvh, hd, ps, lens, dtype, prefix)
+    q, start = queries(H, hd, new, dtype)
+    ref = attention(pages, table, q.cpu(), start, lens, prefix, tree=tree)
+    broken = table.clone()
+    for b, entry in bad:
+        broken[slice(None) if b is None else b, entry] = -3
+    cache.table.copy_(broken)
+    hit = torch.zeros(len(q), dtype=torch.bool)
+    for b, (length, n) in enumerate(zip(lens, new)):
+        for i in range(n):
+            t = int(start[b]) + i
+            for p in range(max(0, length)):
+                first = length - n
+                sees = p <= first + i if tree is None else p < first or bool(int(tree[t]) >> (p - first) & 1)
+                if sees and int(broken[b, p // ps]) < 0:
+                    hit[t] = True
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lse = torch.zeros(q.shape[:2], device="cuda")
+    out = cache.attention(q, start.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), max(new), prefix, lse=lse,
+                          status=status, tree_mask=None if tree is None else tree.cuda())
+    assert int(status.item()) == dexlib.DEX_ATTN_BAD_PAGE
+    assert bool(hit.any())
+    assert bool(torch.isnan(out[hit]).all()) and bool(torch.isnan(lse[hit]).all())
+    compare(out, lse, ref, ~hit)
+
+
+@pytest.mark.parametrize("H,kvh,hd,dtype", [(8, 2, 64, FP), (16, 4, 128, BF)])
+@pytest.mark.parametrize("n", [6, 30, 90])
+def test_bad_page_behind_the_first_queries(H, kvh, hd, dtype, n):
+    """A run of queries, the later ones of which see a bad page: those before it do not."""
+    for ps, past in ((16, 100), (32, 3), (64, 250)):
+        lens, new = [past + n, 40, past + n + 7], [n, 1, n]
+        entry = (past + n // 2) // ps
+        bad_page_case(H, kvh, hd, ps, dtype, lens, new, [(0, entry)])
+        bad_page_case(H, kvh, hd, ps, dtype, lens, new, [(0, entry), (2, (past + n + 6) // ps), (1, 0)])
+
+
+@pytest.mark.parametrize("H,kvh,hd,ps,new,prefix", SHARED)
+def test_bad_page_of_a_shared_prefix(H, kvh, hd, ps, new, prefix):
+    """Sequences that end before the prefix's bad page keep their results."""
+    lens = [prefix + n for n in new]
+    entry = (prefix // 2) // ps
+    for b in (1, 3, len(new) - 1):
+        lens[b] = max(1, entry * ps - b % 3)
+    bad_page_case(H, kvh, hd, ps, BF, lens, new, [(None, entry)], prefix)
+
+
+@pytest.mark.parametrize("n", [7, 40])
+def test_bad_page_that_tree_words_leave_out(n):
+    """Nodes whose words select nothing on the bad page keep their results."""
+    g = torch.Generator().manual_seed(n)
+    past = [43, 0, 96]
+    words = [w | (1 << i) if i % 2 else 1 << i for _ in past for i, w in enumerate(torch.randint(0, 1 << (n // 2), (n,), generator=g).tolist())]
+    bad_page_case(8, 2, 64, 16, FP, [p + n for p in past], [n] * 3, [(0, (past[0] + n - 1) // 16), (2, (past[2] + 3) // 16)],
+                  tree=torch.tensor(words, dtype=torch.int64))
