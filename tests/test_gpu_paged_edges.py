@@ -5,6 +5,7 @@ import math
 import pytest
 import torch
 
+import test_gpu_paged
 from gpu_util import require_gpu
 from paged_ref import HALF, attention, gather
 from test_gpu_paged import BF, FP, SHARED, compare, paged, queries, run_case
@@ -226,3 +227,25 @@ def test_bad_page_that_tree_words_leave_out(n):
     words = [w | (1 << i) if i % 2 else 1 << i for _ in past for i, w in enumerate(torch.randint(0, 1 << (n // 2), (n,), generator=g).tolist())]
     bad_page_case(8, 2, 64, 16, FP, [p + n for p in past], [n] * 3, [(0, (past[0] + n - 1) // 16), (2, (past[2] + 3) // 16)],
                   tree=torch.tensor(words, dtype=torch.int64))
+
+
+def test_shared_steps_of_one_kernel_in_a_graph():
+    """The captured steps over a shared prefix where one kernel reads the prefix and the sequences' own positions:
+    few rows (32 of all sequences at most), and positions enough (912 tiles of 64 in all) that it is read once."""
+    batch, kvh, prefix = 7, 32, 330
+    assert batch * kvh * (prefix // 64) >= 912
+    test_gpu_paged.test_shared_steps_in_a_graph(batch, kvh, 1, 128, prefix)
+
+
+@pytest.mark.parametrize("batch,kvh,prefix,longest", [(32, 32, 450, 200), (16, 64, 260, 300), (31, 32, 1000, 130)])
+@pytest.mark.parametrize("dtype,hd", [(BF, 64), (FP, 128)])
+def test_two_ranges_per_block(batch, kvh, prefix, longest, dtype, hd):
+    """Work enough that every thread block of the kernel for few rows takes two ranges in turn, prefix and own
+    segments in one kernel: eight units (a segment's tiles of 64 and one more) for each of 304 blocks."""
+    g = torch.Generator().manual_seed(prefix)
+    tails = [int(t) for t in torch.randint(1, longest, (batch,), generator=g)]
+    tails[0], tails[-1] = 1, longest
+    tiles = lambda lo, hi: -(-hi // 64) - lo // 64
+    units = kvh * (tiles(0, prefix) + 1 + sum(tiles(prefix, prefix + t) + 1 for t in tails))
+    assert units >= 8 * 304 and batch * kvh * (prefix // 64) >= 912
+    run_case(kvh, kvh, hd, 32, dtype, [prefix + t for t in tails], [1] * batch, prefix)
