@@ -1230,7 +1230,7 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 
 // Loads of a segment's cnt tiles: K of the first `ahead` tiles, then V of tile j and K of tile
 // j + ahead in turn -- the order in which the MMAs take them.
-__device__ __forceinline__ int k_load(int j, int cnt, int ahead) { return j < ahead ? j : ahead + 2 * (j - ahead) + 1; }
+__device__ __forceinline__ int k_load(int j, int ahead) { return j < ahead ? j : ahead + 2 * (j - ahead) + 1; }
 __device__ __forceinline__ int v_load(int j, int cnt, int ahead) {   // index of V_j among the 2 cnt loads
   const int a = min(ahead, cnt);
   return a + j + min(j, cnt - a);
@@ -1371,7 +1371,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       bool any = false;   // this team had a tile
       // stages of K of its next tile and V of its last one (thread 0), at hand before they are to be freed: the
       // loads that wait for them are needed within a tile's time
-      uint64_t *k_stage = stage_of(k_load(alt ? team : 0, cnt, ahead)), *v_stage = nullptr;
+      uint64_t *k_stage = stage_of(k_load(alt ? team : 0, ahead)), *v_stage = nullptr;
       for (int j = alt ? team : 0; j < cnt; j += ahead == 2 ? 2 : 1) {
         if (ok && !pipe_wait(&s_full[team], n_s & 1u)) {
           timed_out();
@@ -1519,7 +1519,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[team]);
         v_stage = stage_of(v_load(j, cnt, ahead));
-        k_stage = stage_of(k_load(j + ahead, cnt, ahead));
+        k_stage = stage_of(k_load(j + ahead, ahead));
         ++n_s;
       }
       // ---------------- the segment's result ----------------

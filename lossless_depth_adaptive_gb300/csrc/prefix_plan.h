@@ -48,14 +48,18 @@ struct Plan {
 
 // Which kernel computes what.  Segments of at most 32 rows go to rows_kernel, unless tile_kernel runs for the prefix
 // and there are few of them: a launch less (14 sequences of 8 K/V heads behind 27032 positions 46.5 -> 41.7 us; for
-// 36 of 8 behind 938 it would be 22.0 -> 28.3).  With 16 rows as the limit, 8 x 8 segments of 32 prefix rows take
+// 36 of 8 behind 938 it would be 22.0 -> 28.3).  They are counted by the table's slots, used or not: 14 sequences in 64
+// slots 53.2 us, with own_tile 51.7; 16 in 128 slots behind 4096 25.6, with own_tile 27.5.  With 16 rows as the limit, 8 x 8 segments of 32 prefix rows take
 // 23.4 us instead of 14.9, 32 of 32 rows 48.9 instead of 41.8.
 // Sharing costs a join of two parts of every row and mostly a launch, and saves reading the prefix for each sequence.
 // So it is shared when more than one sequence can have queries (n_tokens > max_q) and reading it for all of
 // them would give every CTA of rows_kernel three key tiles: at 624 tiles in all (13 sequences of 4 heads behind 777
 // positions) it takes 13.2 us shared and 12.2 not, at 1188 (9 of 4 behind 2158) 10.4 and 12.6, at 2048 (8 of 8
 // behind 2048) 13.1 and 16.3.  A prefix below two tiles is not shared (73 positions, 202 sequences of 8 heads: 83 us
-// shared, 70 not), and a sequence whose own rows fill a 128-row tile gains nothing from sharing.
+// shared, 70 not).  A sequence whose own rows fill a 128-row tile gains nothing from sharing, and the longest run
+// decides for the batch: where its rows can fill one, nothing is shared.  That is right for batches of such runs and
+// costs batches with one of them what sharing would have saved for the others (63 single tokens of 32 / 8 heads and a
+// run of 31 behind 8192 positions 83 us, and a run of 32 294; the single tokens alone 49, the run 19).
 inline Plan make_plan(const PrefixAttnArgs& a) {
   Plan p = {};
   const int64_t own_rows = static_cast<int64_t>(a.max_q) * a.G, all_rows = static_cast<int64_t>(a.n_tokens) * a.G;
