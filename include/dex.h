@@ -336,7 +336,7 @@ typedef struct dex_attention_args {
   int32_t n_tokens, n_heads;
   int32_t max_q;               /* no sequence has more queries than this (<= 64 with tree_mask) */
   int32_t prefix_len;          /* >= 0 */
-  float scale;                 /* of the scores, usually 1 / sqrt(head_dim) */
+  float scale;                 /* of the scores, usually 1 / sqrt(head_dim); below 2^127 in size */
 } dex_attention_args;
 
 /* Bits a call ORs into *status (device int32, cleared by the caller). */

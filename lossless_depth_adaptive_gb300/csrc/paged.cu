@@ -280,8 +280,9 @@ extern "C" int dex_prefix_attention(const dex_paged_kv* kv, const dex_attention_
   dex::PrefixAttnArgs d = {};
   const int rc = attention_args(kv, a, &d);
   if (rc) return rc;
+  const float scale_log2 = a->scale * 1.4426950408889634f;
   if (!kv->pages || !kv->table || !aligned16(kv->pages) || !a->q_start || !a->seq_len || (a->tree_mask && a->max_q > 64) ||
-      !(a->scale > -INFINITY && a->scale < INFINITY))
+      !(scale_log2 > -INFINITY && scale_log2 < INFINITY))
     return DEX_EINVAL;
   if (a->n_tokens == 0) return DEX_OK;
   const int64_t row = static_cast<int64_t>(a->n_heads) * kv->head_dim;
@@ -300,7 +301,7 @@ extern "C" int dex_prefix_attention(const dex_paged_kv* kv, const dex_attention_
   d.seq_len = a->seq_len;
   d.prefix_table = a->prefix_table ? a->prefix_table : kv->table;
   d.tree = a->tree_mask;
-  d.scale_log2 = a->scale * 1.4426950408889634f;
+  d.scale_log2 = scale_log2;
   d.status = status;
   return dex::launch_prefix_attention(d, workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DEX_OK : DEX_ECUDA;
 }

@@ -86,6 +86,13 @@ def test_bad_attention_is_refused(bad):
                                              None) == EINVAL
 
 
+@pytest.mark.parametrize("scale", [2.4e38, -3.0e38])
+def test_scale_beyond_its_base_is_refused(scale):
+    """Finite, but not in the base that the kernels use (times log2 e): it would make every score infinite."""
+    assert dexlib.lib().dex_prefix_attention(C.byref(kv()), C.byref(attn_args(scale=scale)), 1 << 20, 1 << 40, None,
+                                             None) == EINVAL
+
+
 def test_workspace_size():
     """Given by sizes alone; too small or misaligned a workspace is refused."""
     L = dexlib.lib()
