@@ -301,9 +301,14 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     return;
   }
 
-  const Pair c = octaves_per_unit(temp);
-  auto weight = [&](float x) { return weight_of(x, top, c, sh.table); };
-  const float far = c.hi > 0.0f ? fmaxf(-128.0f / c.hi, -3.0e38f) : -3.0e38f;
+  // Hot rows (their weights are mostly one) are weighed exactly at once: rough weights have no room to scale logits, and below
+  // -3e38 they cannot tell -inf from a logit that counts.
+  const float down = temp >= kHot ? kHotScale : 1.0f;
+  const Pair c = octaves_per_unit(temp * down);
+  const float per_unit = c.hi * down;   // octaves
+  const bool rough = temp < kHot && c.hi < INFINITY;
+  auto weight = [&](float x) { return weight_of(x, top, c, sh.table, down); };
+  const float far = fmaxf(-128.0f / per_unit, -3.0e38f);
   auto near = [&](float x) { return weight_near(x, top, c, far); };
   auto near_units = [&](float x) { return in_units(near(x)); };
   // What a sum of such weights may be off by: of tokens down to `octaves` below the largest 2^-21 + octaves 2^-24 ln 2 of it (weight_near),
@@ -453,12 +458,12 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   // The nucleus of most rows is small.  Looked for here where a thread has many logits: 256 rows of 151936 fp32 at temperature
   // 0.5 177 us, by the histogram alone 265; where it has few, a row whose nucleus is not small loses more than that gains (8 rows of
   // 32000, 8 per thread: 24.2 us, by the histogram alone 18.9).
-  const bool few_p = top_k == 0 && top_p < 1.0f && c.hi < INFINITY && steps >= 16;
+  const bool few_p = top_k == 0 && top_p < 1.0f && rough && steps >= 16;
   const bool by_maxima = few_p || (top_k > 0 && top_k <= kMostK);
   if (by_maxima || (top_k == 0 && top_p >= 1.0f && least > 0)) {
     uint64_t row_mass = 0;   // few_p: of the whole row, roughly
     bool worth = true;
-    const float scale = 8.0f * c.hi;
+    const float scale = 8.0f * per_unit;
     int threshold;
     if (by_maxima) {
       const int b = most == top ? 0 : static_cast<int>(fminf(sub_rn(top, most) * scale, kMaxBins - 1.0f));
@@ -553,7 +558,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   static_assert(kBins == 1 << kFineBits, "digits");
   constexpr float kPerOctave = kBins * ((kBins - 1) / kZeroOctaves);
   auto fine = [&](float x) {   // (starts as weight_near does)
-    const float y = mul_rn(fmaxf(sub_rn(x, top), far), c.hi);
+    const float y = mul_rn(fmaxf(sub_rn(x, top), far), per_unit);
     return x == top ? 0 : static_cast<int>(fminf(mul_rn(y, -kPerOctave), kBins * kBins - 1.0f));
   };
   // Sums of measure by bins (bin_of: -1 for none) over the row; returns the total, and the bin in which the running sum plus `above`
@@ -616,25 +621,25 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     in_bin = sh.found[2];
     return target;
   };
-  // Moves the cut to where the measure of what stays, largest first, reaches target_of(its total).  rough: what is summed over the
+  // Moves the cut to where the measure of what stays, largest first, reaches target_of(its total).  rough_of: what is summed over the
   // row; unless that is exact too, false where it does not tell.
   float depth = kZeroOctaves;   // of the cut, in octaves
-  auto select = [&](auto rough, auto measure, auto target_of, bool exact) {
+  auto select = [&](auto rough_of, auto measure, auto target_of, bool exact) {
     uint64_t above = 0;
     int bin;
     auto of_cut = [&](float x, int id) { return in_cut(x, id) ? measure(x) : uint64_t(0); };
-    auto sum_of = [&](float x, int id) { return in_cut(x, id) ? rough(x) : uint64_t(0); };
+    auto sum_of = [&](float x, int id) { return in_cut(x, id) ? rough_of(x) : uint64_t(0); };
     const uint64_t target = histogram([&](float x) { return fine(x) >> kFineBits; }, sum_of, target_of, above, bin), sum = in_all;
     if (bin >= kBins - 1) return exact;   // among the zero weights, or not at all: nothing is cut
     int low = bin << kFineBits, high = low + kBins - 1;
     // logits between which these are, and not much more (a cheaper question than fine)
     float x_low, x_high;
     auto limits = [&] {
-      const float unit = 1.0f / (kPerOctave * c.hi), wide = 1e-6f * (fabsf(top) + high * unit);
+      const float unit = 1.0f / (kPerOctave * per_unit), wide = 1e-6f * (fabsf(top) + high * unit);
       x_low = unit < 1e30f ? top - (high + 2) * unit - wide : -INFINITY;
       x_high = unit < 1e30f ? top - (low - 2) * unit + wide : INFINITY;
     };
-    const uint64_t middle = rough(top - (bin + 0.5f) * kBins / (kPerOctave * c.hi));   // the weight of the bin's tokens, about
+    const uint64_t middle = rough_of(top - (bin + 0.5f) * kBins / (kPerOctave * per_unit));   // the weight of the bin's tokens, about
     depth = (high + 1) / kPerOctave;
     // (the target is at most as much off as the sum that it is a part of)
     if (!exact && middle < 2 * (2 * slack(above, depth) + slack(sum - above, kZeroOctaves))) return false;   // it would hardly tell
@@ -766,7 +771,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   const float cut_k = cut;
   const int last_k = last;
   // (also with few logits per thread: 8 rows of 32000 with top-p 18.9 us, weighed exactly at once 20.5)
-  if (c.hi < INFINITY && (top_p >= 1.0f || select(near_units, weight, nucleus, false)) && finish(near_units, false)) return;
+  if (rough && (top_p >= 1.0f || select(near_units, weight, nucleus, false)) && finish(near_units, false)) return;
   cut = cut_k;
   last = last_k;
   if (top_p < 1.0f) select(weight, weight, nucleus, true);

@@ -31,6 +31,13 @@ DEX_WEIGHT_FN float sub_rn(float x, float y) {
   return x - y;
 #endif
 }
+DEX_WEIGHT_FN float fma_rn(float x, float y, float z) {
+#ifdef __CUDA_ARCH__
+  return __fmaf_rn(x, y, z);
+#else
+  return fmaf(x, y, z);
+#endif
+}
 DEX_WEIGHT_FN int32_t float_bits(float x) {
 #ifdef __CUDA_ARCH__
   return __float_as_int(x);
@@ -65,7 +72,12 @@ DEX_WEIGHT_FN Pair pair_of(double x) {
   return p;
 }
 
-// log2(e) / temperature, to 2^-46 of it and more (temperature > 0; infinite where that is).
+// From here on temperatures and logits are scaled down before weight_of, as octaves_per_unit would lose its lower part below the
+// normal floats and the difference of two logits that matter could overflow.  (A power of two: no rounding but of what is far too
+// small to matter.)
+constexpr float kHot = 0x1p100f, kHotScale = 0x1p-40f;
+
+// log2(e) / temperature, to 2^-46 of it and more (0 < temperature < kHot; infinite where that is).
 DEX_WEIGHT_FN Pair octaves_per_unit(float temperature) {
   constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.92596299112661746e-8f;
   Pair c;
@@ -78,12 +90,13 @@ DEX_WEIGHT_FN Pair octaves_per_unit(float temperature) {
 // below 2^-22 of the largest by a float's own 22 bits, before that
 // differences, products and the exponential are pairs of floats (46 bits and more): y = (x - top) c = n + j/32 + f with
 // 2^(j/32) from a table of pairs (j from -16 to 16) and 2^f = 1 + t + t^2/2 + ..., t = f ln 2 below 2^-6.5, of which the
-// first two terms need their low parts.
-DEX_WEIGHT_FN uint64_t weight_of(float x, float top, Pair c, const Pair* table) {
+// first two terms need their low parts.  scale: a power of two that x and top are multiplied by.
+DEX_WEIGHT_FN uint64_t weight_of(float x, float top, Pair c, const Pair* table, float scale = 1.0f) {
   if (x == top) return uint64_t(1) << kWeightBits;   // also where c is infinite
-  const float d = sub_rn(x, top);
-  const float b = sub_rn(d, x);                      // the part of -top that is in d
-  const float dl = sub_rn(x, sub_rn(d, b)) - (top + b);
+  const float most = mul_rn(top, scale);
+  const float d = fma_rn(x, scale, -most);
+  const float b = fma_rn(-x, scale, d);               // the part of -most that is in d
+  const float dl = fma_rn(x, scale, -sub_rn(d, b)) - (most + b);
   const float y = mul_rn(d, c.hi);
   if (!(y >= -45.0f)) return 0;                      // also NaN: infinities
   const float yl = fmaf(d, c.hi, -y) + fmaf(d, c.lo, mul_rn(dl, c.hi));
