@@ -105,7 +105,7 @@ constexpr size_t kMostBytes = 227 * 1024;
 static_assert(kHead + (1 << 18) / kMaxCluster * 4 + 16 <= kMostBytes, "a slice of the longest row");
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant__ SampleArgs a, int slice) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a, int slice) {
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
