@@ -463,10 +463,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if (by_maxima || (top_k == 0 && top_p >= 1.0f && least > 0)) {
     uint64_t row_mass = 0;   // few_p: of the whole row, roughly
     bool worth = true;
-    const float scale = 8.0f * per_unit;
-    int threshold;
+    int threshold;   // (products with per_unit in an order in which none overflows before it is compared)
     if (by_maxima) {
-      const int b = most == top ? 0 : static_cast<int>(fminf(sub_rn(top, most) * scale, kMaxBins - 1.0f));
+      const int b = most == top ? 0 : static_cast<int>(fminf(mul_rn(sub_rn(top, most), per_unit) * 8.0f, kMaxBins - 1.0f));
       red_shared(&sh.maxima[b], 1u);
       if (few_p) {
         uint64_t before;
@@ -495,9 +494,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     } else {   // weights of min_p and more, and some others
       threshold = static_cast<int>(fminf(8.0f * (1.0f - log2f(fminf(min_p, 1.0f))), static_cast<float>(kZeroBin)));
     }
-    // as a logit, somewhat lower than it need be (an infinite scale: the largest alone; a zero one: all)
-    const float far = static_cast<float>(threshold) / scale;
-    const float from = scale > 0.0f ? top - far - (fabsf(top) + far) * 1e-6f : -INFINITY;
+    // as a logit, somewhat lower than it need be (where weights have no room: the largest alone; where all have: all)
+    const float far = static_cast<float>(threshold) * 0.125f / per_unit;
+    const float from = top - far - (fabsf(top) + far) * 1e-6f;
     bool few = worth && collect(!__any_sync(0xffffffffu, most >= from), [&](float x, int) { return x >= from; }, [&](float x, int) { return weight(x); });
     uint64_t end = 0, off = 0;   // few_p: the nucleus ends where the mass before a token reaches `end`, which may be that much off
     if (few && few_p) {
@@ -633,13 +632,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (bin >= kBins - 1) return exact;   // among the zero weights, or not at all: nothing is cut
     int low = bin << kFineBits, high = low + kBins - 1;
     // logits between which these are, and not much more (a cheaper question than fine)
+    auto down_by = [&](float steps) { return steps * (1.0f / kPerOctave) / per_unit; };   // (a single step may be too small for a float)
     float x_low, x_high;
     auto limits = [&] {
-      const float unit = 1.0f / (kPerOctave * per_unit), wide = 1e-6f * (fabsf(top) + high * unit);
-      x_low = unit < 1e30f ? top - (high + 2) * unit - wide : -INFINITY;
-      x_high = unit < 1e30f ? top - (low - 2) * unit + wide : INFINITY;
+      const float wide = 1e-6f * (fabsf(top) + down_by(high));
+      x_low = down_by(1.0f) < 1e30f ? top - down_by(high + 2) - wide : -INFINITY;
+      x_high = down_by(1.0f) < 1e30f ? top - down_by(low - 2) + wide : INFINITY;
     };
-    const uint64_t middle = rough_of(top - (bin + 0.5f) * kBins / (kPerOctave * per_unit));   // the weight of the bin's tokens, about
+    const uint64_t middle = rough_of(top - down_by((bin + 0.5f) * kBins));   // the weight of the bin's tokens, about
     depth = (high + 1) / kPerOctave;
     // (the target is at most as much off as the sum that it is a part of)
     if (!exact && middle < 2 * (2 * slack(above, depth) + slack(sum - above, kZeroOctaves))) return false;   // it would hardly tell

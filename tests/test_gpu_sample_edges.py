@@ -1,4 +1,5 @@
-"""GPU tests of sampling at its edges, against the 64-bit form: the highest temperatures that a float holds."""
+"""GPU tests of sampling at its edges, against the 64-bit form: temperatures from the smallest to the largest that a float
+holds."""
 import math
 
 import pytest
@@ -43,5 +44,16 @@ def test_sample_hot_and_wide(T, v):
     x = (torch.rand((12, v), generator=gen) * 2 - 1) * min(3.4e38, 12 * T)
     x[3, ::3] = -math.inf
     u = torch.rand(12, generator=gen)
+    for k, p, m in LIMITS:
+        sample_case(x, u, T, k, p, m)
+
+
+@pytest.mark.parametrize("T", [1.5e-38, 1e-37, 1e-35, 1e-31])
+@pytest.mark.parametrize("v", [301, 5003, 40000])
+def test_sample_cold_and_narrow(T, v):
+    """Logits that differ by some multiples of a temperature next to the smallest normal float."""
+    x, u = spread_logits(12, v, F32, v)
+    x = x * T                                # (subnormal in part)
+    x[5] -= x[5].max()                       # the largest is zero
     for k, p, m in LIMITS:
         sample_case(x, u, T, k, p, m)
