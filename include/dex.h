@@ -461,7 +461,8 @@ typedef struct dex_sample_args {
  *           the mass of what top_k left lies (the first one always),
  *   min_p   of these the ones with w_v >= min_p,
  * and the token is the lowest id up to which more than u of the mass that is left lies.  So rows that share u and
- * settings are coupled.  logprob: the log of the token's share of that mass, good to 2^-18.  Temperature 0: the largest logit (lowest
+ * settings are coupled.  logprob: the log of the token's share of that mass, good to 2^-19 and 2^-22 of its
+ * size.  Temperature 0: the largest logit (lowest
  * id), log-probability 0; one so small that log2(e) / temperature is no float (below 4.3e-39): only tokens of the largest logit have a
  * chance.  Weights are computed to 2^-43 of the largest and summed as integers, so the result does not
  * depend on any order; a token below 2^-44 of the largest has no chance.  In the arrays top_k <= 0 or >= vocab, top_p >= 1

@@ -234,15 +234,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     a.tokens[row] = id;
     if (a.logprob) a.logprob[row] = logprob;
   };
-  auto share_of = [&](uint64_t w, uint64_t all) {   // its log
-    const float af = static_cast<float>(all);
-    if (2 * w > all) return log1pf(-(static_cast<float>(all - w) / af));
-    // log(r (1 + e)) with what the rounded quotient r leaves
-    const float wf = static_cast<float>(w), q = wf / af;
-    const float wl = static_cast<float>(static_cast<int64_t>(w - static_cast<uint64_t>(wf))), al = static_cast<float>(static_cast<int64_t>(all - static_cast<uint64_t>(af)));
-    return logf(q) + (fmaf(-q, af, wf) + fmaf(-q, al, wl)) / wf;
-  };
-
   // ---- the largest logit; a row with NaN or +inf has no answer
   float most = -INFINITY;   // of the thread's
   bool bad = false;
@@ -308,6 +299,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const float per_unit = c.hi * down;   // octaves
   const bool rough = temp < kHot && c.hi < INFINITY;
   auto weight = [&](float x) { return weight_of(x, top, c, sh.table, down); };
+  // The log of the share that a token of weight w has of the mass.  What it is drawn by are whole units of 2^-43; the share of one that
+  // is not most of the mass goes by its logit.
+  auto share_of = [&](float x, uint64_t w, uint64_t mass) {
+    if (2 * w > mass) return log1pf(-(static_cast<float>(mass - w) / static_cast<float>(mass)));
+    return log_share(x == top ? Pair{0.0f, 0.0f} : octaves_of(x, top, c, down), mass);
+  };
   const float far = fmaxf(-128.0f / per_unit, -3.0e38f);
   auto near = [&](float x) { return weight_near(x, top, c, far); };
   auto near_units = [&](float x) { return in_units(near(x)); };
@@ -544,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         mass += t;
       }
       const uint64_t target = __umul64hi(part, mass) + 1;   // more than u of the mass
-      if (incl - w < target && incl >= target) answer(static_cast<int>(sh.flat[tid].id), share_of(w, mass));
+      if (incl - w < target && incl >= target) answer(static_cast<int>(sh.flat[tid].id), share_of(from_key(sh.flat[tid].key), w, mass));
       return;
     }
     if (!few_p) cut = from;   // what is lower has no chance
@@ -707,7 +704,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     cluster_sync();
     return true;
   };
-  // The token among what stays; false where rough weights do not tell.
+  // The token among what stays; false where rough weights do not tell.  Its log-probability may go by a mass of rough weights: off by
+  // each one's 2^-21 and by 2^-24 ln 2 per octave, of which the tokens of a row lie, by their shares, at most log2(vocab) <= 18
+  // below the largest (else their entropy would be more than that), so by 2^-19.6; a float's step at a log of -16 is 2^-19.
   auto finish = [&](auto units_of, bool exact) {
     auto enough = [&](float x, uint64_t w) {   // min-p
       if (least == 0) return w;
@@ -755,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       const float x = to_f32(xs[id - v0]) + 0.0f;
       const uint64_t w = stays(x, id), off = exact ? 0 : slack(mass, depth) + slack(before, depth);
       sure = exact || (before + off < target && before + w >= target + off);
-      if (sure && lane == 0) answer(id, share_of(weight(x), mass));
+      if (sure && lane == 0) answer(id, share_of(x, weight(x), mass));
     }
     if (exact) return true;
     const uint32_t unsure = __syncthreads_or(!sure);

@@ -86,20 +86,41 @@ DEX_WEIGHT_FN Pair octaves_per_unit(float temperature) {
   return c;
 }
 
+// (x - top) c, that is how many octaves x lies below top, as a pair: the difference, its rounding error and the products' ones.
+// scale: a power of two that x and top are multiplied by.  (x == top where c is infinite, and infinities: NaN)
+DEX_WEIGHT_FN Pair octaves_of(float x, float top, Pair c, float scale = 1.0f) {
+  const float most = mul_rn(top, scale);
+  const float d = fma_rn(x, scale, -most);
+  const float b = fma_rn(-x, scale, d);              // the part of -most that is in d
+  const float dl = fma_rn(x, scale, -sub_rn(d, b)) - (most + b);
+  Pair y;
+  y.hi = mul_rn(d, c.hi);
+  y.lo = fmaf(d, c.hi, -y.hi) + fmaf(d, c.lo, mul_rn(dl, c.hi));
+  return y;
+}
+
+constexpr float kLn2 = 0.693147182464599609375f, kLn2Low = -1.904654323148236e-9f;
+
+// The log of 2^y / (mass 2^-43), for what is at most half of it: ln 2 y and the log of the mass have one sign, so nothing cancels; 2^-22 of
+// the result with a log good to one unit in the last place.  (An integer weight would not do: at 20 nats below the largest it has some 15
+// bits left, at 29 one.)
+DEX_WEIGHT_FN float log_share(Pair y, uint64_t mass) {
+  const float m = static_cast<float>(mass), rest = static_cast<float>(static_cast<int64_t>(mass - static_cast<uint64_t>(m)));
+  const float t = mul_rn(y.hi, kLn2);
+  const float tl = fmaf(y.hi, kLn2, -t) + fmaf(y.hi, kLn2Low, mul_rn(y.lo, kLn2));
+  return sub_rn(t, logf(mul_rn(m, 0x1p-43f))) + (tl - rest / m);
+}
+
 // w = 2^((x - top) c), c = log2(e) / temperature, in units of 2^-43; 0 below half a unit.  To within two units:
 // below 2^-22 of the largest by a float's own 22 bits, before that
 // differences, products and the exponential are pairs of floats (46 bits and more): y = (x - top) c = n + j/32 + f with
 // 2^(j/32) from a table of pairs (j from -16 to 16) and 2^f = 1 + t + t^2/2 + ..., t = f ln 2 below 2^-6.5, of which the
-// first two terms need their low parts.  scale: a power of two that x and top are multiplied by.
+// first two terms need their low parts.
 DEX_WEIGHT_FN uint64_t weight_of(float x, float top, Pair c, const Pair* table, float scale = 1.0f) {
   if (x == top) return uint64_t(1) << kWeightBits;   // also where c is infinite
-  const float most = mul_rn(top, scale);
-  const float d = fma_rn(x, scale, -most);
-  const float b = fma_rn(-x, scale, d);               // the part of -most that is in d
-  const float dl = fma_rn(x, scale, -sub_rn(d, b)) - (most + b);
-  const float y = mul_rn(d, c.hi);
+  const Pair o = octaves_of(x, top, c, scale);
+  const float y = o.hi, yl = o.lo;
   if (!(y >= -45.0f)) return 0;                      // also NaN: infinities
-  const float yl = fmaf(d, c.hi, -y) + fmaf(d, c.lo, mul_rn(dl, c.hi));
   if (y < -22.0f) {
     const float w = mul_rn(exp2_fast(y), 8796093022208.0f);   // in units, below 2^21
     return static_cast<uint64_t>(static_cast<uint32_t>(fmaf(w, mul_rn(yl, 0.693147182f), w) + 0.5f));
@@ -108,7 +129,6 @@ DEX_WEIGHT_FN uint64_t weight_of(float x, float top, Pair c, const Pair* table, 
   const float r = sub_rn(y, n);                      // exact, at most 1/2
   const float j = rintf(mul_rn(r, 32.0f));
   const float f = fmaf(j, -0.03125f, r);             // exact
-  constexpr float kLn2 = 0.693147182464599609375f, kLn2Low = -1.904654323148236e-9f;
   const float th = mul_rn(f, kLn2);
   const float rest_t = fmaf(f, kLn2, -th) + fmaf(f, kLn2Low, mul_rn(yl, kLn2));
   const float t = th + rest_t;                       // f may be smaller than yl

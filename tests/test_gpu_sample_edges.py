@@ -1,10 +1,11 @@
-"""GPU tests of sampling at its edges, against the 64-bit form: temperatures from the smallest to the largest that a float
-holds."""
+"""GPU tests of sampling at its edges, against 64-bit forms: temperatures from the smallest to the largest that a float
+holds, log-probabilities of tokens far below the largest."""
 import math
 
 import pytest
 import torch
 
+from gpu_util import require_gpu
 from test_gpu_serving import BF, F32, FP, sample_case, spread_logits
 
 pytestmark = pytest.mark.gpu
@@ -57,3 +58,32 @@ def test_sample_cold_and_narrow(T, v):
     x[5] -= x[5].max()                       # the largest is zero
     for k, p, m in LIMITS:
         sample_case(x, u, T, k, p, m)
+
+
+@pytest.mark.parametrize("v,below", [(1 << 17, 22.7), (1 << 17, 25.1), (1 << 17, 27.3), (1 << 18, 28.4), (400, 18.5), (3000, 20.0)])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_sample_logprob_of_the_tail(v, below, dtype):
+    """One peak and a tail of tokens far below it, drawn by a u next to one.  Which of the tail it is hangs on weights of a few units of
+    2^-43; its log-probability does not: 2^-19 for the mass (rough weights are off by 2^-21 and 2^-24 ln 2 per octave, of which a
+    row's tokens have at most log2 v in the mean, and units by 2^-24) and 2^-22 of its size for log, product and rounding."""
+    dexlib = require_gpu()
+    gen = torch.Generator().manual_seed(v)
+    x = (torch.rand((6, v), generator=gen) * 0.5 - below - 0.25)
+    x[:, 0] = 0.0
+    x[2:4] += 7.0
+    x = x.to(dtype)
+    tail = (v - 1) * math.exp(-below)
+    u = torch.tensor([1.0 - 2.0 ** -24, 1.0 - min(0.3 * tail, 2.0 ** -18), 1.0 - 2.0 ** -24, 1.0 - 2.0 ** -23, 1.0 - 2.0 ** -24, 0.5])
+    tails = 0
+    for k, p, m in [(0, 1.0, 0.0), (v - 1, 1.0, 0.0), (0, 1.0, 1e-13), (200, 1.0, 0.0), (0, 1.0 - 2.0 ** -24, 0.0)]:
+        logprob = torch.empty(6, device="cuda")
+        got = dexlib.sample(x.cuda(), u.cuda(), top_k=k, top_p=p, min_p=m, logprob=logprob).cpu().long()
+        w = (x.double() - x.double().max(dim=1, keepdim=True).values).exp()
+        down = w.sort(dim=1, descending=True).values[:, :k or v]
+        ahead = down.cumsum(dim=1) - down
+        left = (down * ((ahead < p * down.sum(dim=1, keepdim=True)) | (p == 1.0))).sum(dim=1)
+        want = (w.gather(1, got[:, None])[:, 0] / left).log()
+        err = (logprob.cpu().double() - want).abs()
+        assert bool((err <= 2.0 ** -19 + 2.0 ** -22 * want.abs()).all()), (k, p, m, err.tolist())
+        tails += int((got > 0).sum())
+    assert tails >= 6
