@@ -308,12 +308,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const float far = fmaxf(-128.0f / per_unit, -3.0e38f);
   auto near = [&](float x) { return weight_near(x, top, c, far); };
   auto near_units = [&](float x) { return in_units(near(x)); };
-  // What a sum of such weights may be off by: of tokens down to `octaves` below the largest 2^-21 + octaves 2^-24 ln 2 of it (weight_near),
-  // and their rounding to units.
-  auto slack = [](uint64_t sum, float octaves) {
-    return static_cast<uint64_t>(static_cast<float>(sum) * (4.77e-7f + octaves * 4.2e-8f)) + (uint64_t(1) << 19);
-  };
-  auto rough_sum = [&] {   // of the thread's, four at a time as floats (2^-22 of it: slack counts twice that beside the octaves)
+  auto rough_sum = [&] {   // of the thread's, four at a time as floats
     uint64_t sum = 0;
     float some = 0.0f;
     int n = 0;
@@ -499,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (few && few_p) {
       const uint64_t held = block_sum(static_cast<uint32_t>(tid) < all ? sh.flat[tid].w : 0);
       end = nucleus(row_mass);
-      off = slack(held, (threshold + 2) * 0.125f) + slack(row_mass - min(row_mass, held), kZeroOctaves);
+      off = rough_slack(held, (threshold + 2) * 0.125f) + rough_slack(row_mass - min(row_mass, held), kZeroOctaves);
       few = held >= end + off;   // else it is not all here
     }
     if (few) {
@@ -639,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const uint64_t middle = rough_of(top - down_by((bin + 0.5f) * kBins));   // the weight of the bin's tokens, about
     depth = (high + 1) / kPerOctave;
     // (the target is at most as much off as the sum that it is a part of)
-    if (!exact && middle < 2 * (2 * slack(above, depth) + slack(sum - above, kZeroOctaves))) return false;   // it would hardly tell
+    if (!exact && middle < 2 * (2 * rough_slack(above, depth) + rough_slack(sum - above, kZeroOctaves))) return false;   // it would hardly tell
     if (in_bin > (kFlat / 2) * middle) {   // many tokens: the bin's own bins
 
       cluster_sync();   // the histogram before has been read
@@ -662,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       return f >= low && f <= high && in_cut(x, id);
     };
     if (collect(false, there, of_cut)) {
-      const uint64_t off = exact ? 0 : 2 * slack(above, depth) + slack(sum - above, kZeroOctaves);
+      const uint64_t off = exact ? 0 : 2 * rough_slack(above, depth) + rough_slack(sum - above, kZeroOctaves);
       for (uint32_t i = warp; i < own; i += kWarps) {
         const Candidate me = sh.flat[ahead + i];
         const uint64_t to = above + rank_of(me).before;
@@ -752,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     bool sure = id != -2;
     if (id >= 0) {
       const float x = to_f32(xs[id - v0]) + 0.0f;
-      const uint64_t w = stays(x, id), off = exact ? 0 : slack(mass, depth) + slack(before, depth);
+      const uint64_t w = stays(x, id), off = exact ? 0 : rough_slack(mass, depth) + rough_slack(before, depth);
       sure = exact || (before + off < target && before + w >= target + off);
       if (sure && lane == 0) answer(id, share_of(x, weight(x), mass));
     }

@@ -154,8 +154,9 @@ DEX_WEIGHT_FN uint64_t weight_of(float x, float top, Pair c, const Pair* table, 
   return static_cast<uint64_t>(full + ((int64_t(1) << down) >> 1)) >> down;
 }
 
-// The same as a float, roughly: off by at most 2^-21 + 2^-24 |y| ln 2 of itself (2^-22 the exponential, the rest what the
-// difference loses), 2^-18 for y above -45; below that it counts for nothing.  An eighth of the instructions.  c.hi has to be finite; far: -128 / c.hi.
+// The same as a float, roughly: off by at most 2^-22 (the exponential) + 2^-24 (the last sum) + 2^-24 |y| ln 2 (what the
+// difference loses) of itself, 2^-18 for y above -45; below that it counts for nothing.  An eighth of the instructions.  c.hi has to be
+// finite and temperatures below kHot; far: -128 / c.hi.
 DEX_WEIGHT_FN float weight_near(float x, float top, Pair c, float far) {
   const float d = fmaxf(sub_rn(x, top), far);
   const float y = mul_rn(d, c.hi);
@@ -169,6 +170,14 @@ DEX_WEIGHT_FN uint64_t in_units(float w) {
   const int32_t bits = float_bits(w), e = (bits >> 23) - (127 + 23 - kWeightBits);   // its last place is 2^e units
   const uint64_t m = static_cast<uint64_t>((bits & 0x7fffff) | 0x800000);
   return e >= 0 ? m << e : e > -24 ? m >> -e : 0;
+}
+
+// What a sum of such weights of tokens down to `octaves` below the largest may be off by, against the sum of weight_of: each by the
+// above, and by three roundings where four of them were added as floats first, 2^-21 and 2^-24 ln 2 per octave in all (with a
+// twentieth to spare for what is of second order); and of the up to 2^18 tokens each by the unit that rounding down loses, the two
+// that weight_of may be off by and the half below which it is nothing.
+DEX_WEIGHT_FN uint64_t rough_slack(uint64_t sum, float octaves) {
+  return static_cast<uint64_t>(static_cast<float>(sum) * (5.0e-7f + octaves * 4.2e-8f)) + (uint64_t(1) << 20);
 }
 
 }  // namespace dex
