@@ -209,7 +209,9 @@ struct LastBlock {
 // query block alone from shared memory (both operands take all of its 128 bytes per clock).  Beside them there is room for
 // one block's scores of either half: the halves take turns, one computes while the MMAs run for the other.  Blocks are as long
 // as that allows, because a block's handovers between the warps take about 1000 cycles however long it is.
-template <typename T, int HD, bool kTensorKeys>
+// kRagged: the rows of a whole block may be no multiple of 16.  Columns behind the last row are zeros times a key, which is no number where
+// the key is infinite, so they are cleared.  (In the loop of the long blocks that would take 2 % of a call over whole prompts.)
+template <typename T, int HD, bool kTensorKeys, bool kRagged>
 __global__ void __launch_bounds__(kThreads, 1)
     mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ MassWork w) {
   constexpr uint32_t kKeyBytes = kHalf * HD * 2;
@@ -402,18 +404,27 @@ __global__ void __launch_bounds__(kThreads, 1)
               acc1 = add2(acc1, f32x2(ex2(__uint_as_float(static_cast<uint32_t>(y))), ex2(__uint_as_float(static_cast<uint32_t>(y >> 32)))));
             }
           };
+          auto clear = [&](uint32_t* v, int n, int c0) {
+            if (!kRagged || c0 + n <= rows) return;
+#pragma unroll
+            for (int i = 0; i < n; ++i) v[i] = c0 + i < rows ? v[i] : 0u;
+          };
           int c0 = from;
           for (; c0 + 16 < to; c0 += 32) {
             uint32_t v[32];
             tmem_ld32_nowait(t_s + c0, v);
             tmem_wait_ld32(v);
-            if (c0 + 32 >= to) release();
+            if (c0 + 32 >= to) {
+              release();
+              clear(v, 32, c0);
+            }
             add(v, 32, c0);
           }
           if (c0 < to) {
             uint32_t v[16];
             tmem_ld16_wait(t_s + c0, v);
             release();
+            clear(v, 16, c0);
             add(v, 16, c0);
           }
           if (from >= to) release();
@@ -688,7 +699,7 @@ namespace {
 
 template <typename T, int HD>
 cudaError_t launch_hd(const MassArgs& a, cudaStream_t st, int dev, int n_sm) {
-  static std::atomic<uint64_t> done[2];
+  static std::atomic<uint64_t> done[3];
   MassWork w = {};
   w.a = a;
   w.by_g = FastDiv(static_cast<uint32_t>(a.G));
@@ -717,7 +728,8 @@ cudaError_t launch_hd(const MassArgs& a, cudaStream_t st, int dev, int n_sm) {
     const cudaError_t e = set_smem(kernel, kSmem, done, dev);
     return e != cudaSuccess ? e : launch(kernel, grid, kThreads, kSmem, st, true, tm_k, tm_q, w);
   };
-  return single ? run(mass_kernel<T, HD, false>, done[0]) : run(mass_kernel<T, HD, true>, done[1]);
+  if (single) return run(mass_kernel<T, HD, false, true>, done[0]);
+  return w.tokens_per_block * a.G % 16 ? run(mass_kernel<T, HD, true, true>, done[1]) : run(mass_kernel<T, HD, true, false>, done[2]);
 }
 
 }  // namespace
