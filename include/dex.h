@@ -405,7 +405,7 @@ int dex_attention_mass(const dex_paged_kv* kv, const dex_mass_args* a, int32_t* 
  * the lowest positions; -0 equals 0; NaN comes last), in their order.  A sequence of at most keep keeps all. */
 typedef struct dex_evict_args {
   const float* mass;           /* device, as dex_attention_mass writes it */
-  float* mass_out;             /* device, or NULL; may be mass itself (then with the same stride) */
+  float* mass_out;             /* device, or NULL; may be mass itself (then with the same stride), else must not overlap it */
   int64_t mass_stride;         /* at least table_width * page_size */
   int64_t mass_out_stride;     /* the same */
   const int32_t* seq_len;      /* device [batch] */

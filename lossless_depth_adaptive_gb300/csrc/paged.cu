@@ -352,7 +352,9 @@ extern "C" int dex_paged_evict(const dex_paged_kv* kv, const dex_evict_args* a, 
       a->mass_stride < cap || a->mass_stride >= (int64_t(1) << 39))
     return DEX_EINVAL;
   if (!kv->pages || !kv->table || !aligned16(kv->pages) || !a->mass || !a->seq_len || !a->new_len || !a->kept ||
-      a->new_len == a->seq_len || (reinterpret_cast<uintptr_t>(a->mass) & 3) || (reinterpret_cast<uintptr_t>(a->mass_out) & 3))
+      (reinterpret_cast<uintptr_t>(a->new_len) < reinterpret_cast<uintptr_t>(a->seq_len + kv->batch) &&
+       reinterpret_cast<uintptr_t>(a->seq_len) < reinterpret_cast<uintptr_t>(a->new_len + kv->batch)) ||
+      (reinterpret_cast<uintptr_t>(a->mass) & 3) || (reinterpret_cast<uintptr_t>(a->mass_out) & 3))
     return DEX_EINVAL;
   if (a->mass_out && (a->mass_out_stride < cap || a->mass_out_stride >= (int64_t(1) << 39) ||
                       (a->mass_out == a->mass && a->mass_out_stride != a->mass_stride)))
