@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+from operator import index
 from typing import Dict, List, Optional, Sequence
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -621,8 +622,6 @@ class PagedCache:
         """
         i32, batch = self._i32, self.kv.batch
         n, heads = q.shape[0], q.shape[1]
-        if not (0 <= first < 2 ** 31 and 0 < window < 2 ** 31):
-            raise DexError(DEX_EINVAL, "first or window out of range")
         if q.dtype != self._dtype:
             raise DexError(DEX_EINVAL, "q must have the cache's type")
         if not (lse.dtype == self._torch.float32 and lse.is_contiguous() and lse.shape == q.shape[:2]):
@@ -630,10 +629,15 @@ class PagedCache:
         if mass is None:
             mass = self._torch.zeros((batch, self.kv_heads, self.kv.table_width * self.kv.page_size),
                                      dtype=self._torch.float32, device=self.device)
-        a = dex_mass_args(q.data_ptr(), lse.data_ptr(), mass.data_ptr(), self._rows("q", q, None, n),
-                          self._masses("mass", mass), self._vector("q_start", q_start, batch + 1, i32),
-                          self._vector("seq_len", seq_len, batch, i32), n, heads, window, first, int(accumulate),
-                          self.head_dim ** -0.5 if scale is None else scale)
+        try:
+            if not (0 <= first < 2 ** 31 and 0 < window < 2 ** 31):
+                raise DexError(DEX_EINVAL, "first or window out of range")
+            a = dex_mass_args(q.data_ptr(), lse.data_ptr(), mass.data_ptr(), self._rows("q", q, None, n),
+                              self._masses("mass", mass), self._vector("q_start", q_start, batch + 1, i32),
+                              self._vector("seq_len", seq_len, batch, i32), n, heads, window, first, int(accumulate),
+                              self.head_dim ** -0.5 if scale is None else scale)
+        except TypeError as e:
+            raise DexError(DEX_EINVAL, f"window and first must be whole numbers, scale a number: {e}") from None
         status_ptr = None if status is None else self._vector("status", status, 1, i32)
         for t in (q, lse, mass, q_start, seq_len, status):
             if t is not None and t.get_device() != self._dev:
@@ -654,8 +658,11 @@ class PagedCache:
         New tokens are appended at new_len, rotated (rope_pos) by their position in the text.
         """
         i32, batch = self._i32, self.kv.batch
-        if not (0 < keep < 2 ** 31 and 0 <= recent < 2 ** 31 and 0 <= first < 2 ** 31):
-            raise DexError(DEX_EINVAL, "keep, recent or first out of range")
+        try:
+            if not (0 < index(keep) < 2 ** 31 and 0 <= index(recent) < 2 ** 31 and 0 <= index(first) < 2 ** 31):
+                raise DexError(DEX_EINVAL, "keep, recent or first out of range")
+        except TypeError as e:
+            raise DexError(DEX_EINVAL, f"keep, recent and first must be whole numbers: {e}") from None
         if mass_out is None:
             mass_out = mass
         if new_len is None:
@@ -713,8 +720,11 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, exclude=No
         if isinstance(value, torch.Tensor):
             setattr(a, name, vector(name, value, torch.int32 if name == "top_k" else torch.float32))
         else:
-            _need(name != "top_k" or 0 <= value < 2 ** 31, "top_k out of range")
-            setattr(a, name + "_all", value)
+            try:
+                _need(name != "top_k" or 0 <= value < 2 ** 31, "top_k out of range")
+                setattr(a, name + "_all", value)
+            except TypeError as e:
+                raise DexError(DEX_EINVAL, f"{name} must be a {'whole ' if name == 'top_k' else ''}number or a tensor: {e}") from None
     if exclude is not None:
         _need(exclude.dim() == 2 and exclude.dtype == torch.int32 and exclude.shape[0] == n and
               (exclude.stride(1) == 1 or exclude.shape[1] <= 1), "exclude must be int32 [rows, n], contiguous rows")
