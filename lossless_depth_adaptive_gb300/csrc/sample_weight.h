@@ -173,11 +173,11 @@ DEX_WEIGHT_FN uint64_t in_units(float w) {
 }
 
 // What a sum of such weights of tokens down to `octaves` below the largest may be off by, against the sum of weight_of: each by the
-// above, and by three roundings where four of them were added as floats first, 2^-21 and 2^-24 ln 2 per octave in all (with a
-// twentieth to spare for what is of second order); and of the up to 2^18 tokens each by the unit that rounding down loses, the two
+// above, and by three roundings where four of them were added as floats first, 2^-21 and 2^-24 ln 2 per octave in all (and some
+// 2^-30 for what is of second order); and of the up to 2^18 tokens each by the unit that rounding down loses, the two
 // that weight_of may be off by and the half below which it is nothing.
 DEX_WEIGHT_FN uint64_t rough_slack(uint64_t sum, float octaves) {
-  return static_cast<uint64_t>(static_cast<float>(sum) * (5.0e-7f + octaves * 4.2e-8f)) + (uint64_t(1) << 20);
+  return static_cast<uint64_t>(static_cast<float>(sum) * (4.78e-7f + octaves * 4.2e-8f)) + (uint64_t(1) << 20);
 }
 
 }  // namespace dex
