@@ -431,13 +431,14 @@ namespace {
 template <int HD>
 cudaError_t launch(const EvictArgs& a, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  int dev = 0;
+  int dev = 0, n_sm = 0;
   cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   // Blocks of a cluster: as many as two per SM allow, each with 2048 positions or more of a full table or a round of rows.
   const int64_t chains = static_cast<int64_t>(a.kv.batch) * a.kv.KVH, positions = static_cast<int64_t>(a.kv.table_width) << a.kv.page_shift;
   unsigned n_cta = 1;
-  while (n_cta < kMaxCluster && chains * n_cta * 2 <= 304 && (positions >= int64_t(4096) * n_cta || a.keep > kWarps * kWarpRows * static_cast<int>(n_cta)))
+  while (n_cta < kMaxCluster && chains * n_cta * 2 <= 2 * n_sm && (positions >= int64_t(4096) * n_cta || a.keep > kWarps * kWarpRows * static_cast<int>(n_cta)))
     n_cta *= 2;
   const int64_t share = (positions + n_cta * kThreads - 1) / (n_cta * kThreads) * kThreads;
   const int cached = static_cast<int>(share < kMove / 4 ? kMove / 4 : share < kCached ? share : kCached);

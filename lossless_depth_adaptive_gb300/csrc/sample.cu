@@ -447,9 +447,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   int last = a.vocab;
 
   // ---- few tokens that matter: the first block finishes the row
-  // The nucleus of most rows is small.  Looked for here where a thread has many logits: 256 rows of 151936 fp32 at temperature
-  // 0.5 177 us, by the histogram alone 265; where it has few, a row whose nucleus is not small loses more than that gains (8 rows of
-  // 32000, 8 per thread: 24.2 us, by the histogram alone 18.9).
+  // The nucleus of most rows is small.  Looked for here where a thread has 16 logits and more.  In us, so and by the histogram alone, at
+  // temperature 0.5, where nuclei are small in most rows, and at 1, where they are not: 256 rows of 151936 fp32 171 and 254, 441 and 463; 256 of 50257 74
+  // and 104, 154 and 153; 8 rows of 65536 (16 per thread) 13 and 22, 50 and 46; 64 rows of 151936 bf16 64 and 55, 170 and 161.  With fewer logits per
+  // thread most is gained and lost: 8 rows of 50257 (13) 13 and 21, 44 and 41; 8 of 32000 (8) 12.5 and 18.9, 26 and 21.
   const bool few_p = top_k == 0 && top_p < 1.0f && rough && steps >= 16;
   const bool by_maxima = few_p || (top_k > 0 && top_k <= kMostK);
   if (by_maxima || (top_k == 0 && top_p >= 1.0f && least > 0)) {
@@ -774,18 +775,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
 template <typename T>
 cudaError_t launch(const SampleArgs& a, cudaStream_t st) {
-  // Blocks of a row.  Few rows: eight, for the latency (8 rows of 32000 fp32 16.7 us; four 24, two 34).  Where eight would not all
-  // be resident at two blocks per SM, four, if two of those fit an SM (64 rows of 151936 bf16: four 16.8 us, eight 25.5; 256
-  // rows fp32, one such block per SM: 289, eight 227).  A block per row that reads it anew for every pass, mostly from L2, is no
-  // better: 256 rows with top-k 111 us instead of 97, with top-p 420 instead of 267.
+  static std::atomic<uint64_t> done{0};   // devices where the kernel may have the shared memory of the longest row
+  int dev = 0, n_sm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  // Blocks of a row.  Few rows: eight, for the latency (8 rows of 32000 fp32 with top-p 19 us, with four 25.5; 8 rows of 151936, flat, 73 and
+  // 116).  Where eight would not all be resident at two blocks per SM, four, if two of those fit an SM (64 rows of 151936 bf16 with top-k 16.9 us, with
+  // eight 26; 256 rows of 32000 fp32 with top-p 61 and 146).  Else eight: with four there is one block per SM (256 rows of 151936 fp32, temperature
+  // alone 161 us, with four 204; settings of their own 190 and 229; top-k 50 93 and 90).
   const auto bytes_of = [&](int n) { return kHead + static_cast<size_t>((a.vocab + n * kThreads - 1) / (n * kThreads) * kThreads) * sizeof(T) + 16; };
-  const unsigned n_cta = a.n_rows > 38 && bytes_of(4) <= 112 * 1024 ? 4 : 8;
+  const unsigned n_cta = a.n_rows * 8 > 2 * n_sm && bytes_of(4) <= 112 * 1024 ? 4 : 8;
   const int slice = (a.vocab + static_cast<int>(n_cta) * kThreads - 1) / (static_cast<int>(n_cta) * kThreads) * kThreads;
   const size_t bytes = kHead + static_cast<size_t>(slice) * sizeof(T) + 16;
-  static std::atomic<uint64_t> done{0};   // devices where the kernel may have the shared memory of the longest row
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
   if (dev >= 64 || !(done.load(std::memory_order_relaxed) >> dev & 1)) {
     e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMostBytes));
     if (e != cudaSuccess) return e;
