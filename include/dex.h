@@ -464,8 +464,9 @@ typedef struct dex_sample_args {
  * settings are coupled.  logprob: the log of the token's share of that mass, good to 2^-19 and 2^-22 of its
  * size.  Temperature 0: the largest logit (lowest
  * id), log-probability 0; one so small that log2(e) / temperature is no float (below 4.3e-39): only tokens of the largest logit have a
- * chance.  Weights are computed to 2^-43 of the largest and summed as integers, so the result does not
- * depend on any order; a token below 2^-44 of the largest has no chance.  In the arrays top_k <= 0 or >= vocab, top_p >= 1
+ * chance.  Weights are integers in units of 2^-43 of the largest, each good to two, and their sums exact, so the result does not
+ * depend on any order; the border between two tokens is off by at most 2 vocab units.  A token below 2^-44 of the largest counts for nothing: it
+ * has no chance, at u = 0 either, and adds nothing to the mass that top_p is a part of.  In the arrays top_k <= 0 or >= vocab, top_p >= 1
  * and min_p <= 0 limit nothing, top_p <= 0 leaves the largest, min_p > 1 counts as 1, u is clamped to [0, 1).
  * A row that has no token to choose (NaN or +inf among its logits that are not excluded, all -inf or excluded, a setting or u that is NaN, a
  * negative or infinite temperature) gets token -1 and logprob NaN.  Runs on the current device; stream-ordered, no allocation, no workspace,

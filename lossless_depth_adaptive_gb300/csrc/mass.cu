@@ -10,10 +10,16 @@
 // lengths alone.  An item's masses are written once, and every key is read once.
 //
 // What bounds it.  Few query rows: HBM and the way to the first tile (one token each of 64 sequences of up to 2560 positions, 32
-// heads x 128: 102 us, 5.0 TB/s; the loads alone 87; 32 queries of four prompts of up to 32768 positions, 32 / 8 heads: 51 us, the loads
-// alone 39; one token each of 8 sequences of 2100: 12.9 us, 5 of them before the first scores).  Whole prompts: the handovers
-// between the warps for each query block beside the MMAs and the exponentials, which take 1536 cycles each per 192 rows and 256
-// keys (three of 3500-7000 tokens, 32 / 8 heads: 380 us, tensor pipe 52 % active).
+// heads x 128: 102 us, 5.0 TB/s, the loads alone 87; added to masses that are there 125; 32 queries of four prompts of up to 32768 positions, 32 / 8
+// heads: 51 us, the loads alone 39, some 4300 cycles per item, of which its summing warps take 1800 for the way to the next item and the join; one
+// token each of 8 sequences of 2100: 13.1 us, 5 of them before the first scores).  Whole prompts: the chain of a half's
+// columns, read up to the release of their buffer (half of a block's time), its next MMAs and the handovers, beside the MMAs and the
+// exponentials of both halves, which take 1536 cycles each per 192 rows and 256
+// keys (three of 3500-7000 tokens, 32 / 8 heads: 379 us at 1.95 GHz, 2900 cycles for each of the fullest CTA's 255 blocks, the mean CTA has 232;
+// tensor pipe 52 % active).
+//
+// Scores and lse meet in base 2 in fp32, and the exponential is the approximate one: a weight is off by some 2^-22 of |score| + |lse| + 2, which
+// is what fp32 inputs of that size say about it; a wider form would cost the loops that bound the call.
 #include <math.h>
 
 #include "../../include/dex.h"

@@ -3,7 +3,9 @@
 //
 // One cluster of blocks per row, each with a slice of the row in shared memory; logits are read once.  Weights
 // are 43-bit fractions of the largest (weight_of), so masses are exact integer sums: no order of summation,
-// number of blocks or atomic changes a token, and a border between two tokens is off by some 2^-43 of the mass.
+// number of blocks or atomic changes a token.  Each is off by up to two units of 2^-43, and one below half a unit is nothing, so the border
+// between two tokens of a row of V is off by at most 2 V units (2^-24 of the largest weight for the longest row; some sqrt(V) where
+// errors fall both ways).
 //
 // No limit sorts the row.  What top-k or top-p cuts off begins at one token, the last that stays in the order of
 // descending logits (equal ones: ascending ids), and everything else is a comparison with it.  It is found among candidates: few
@@ -19,10 +21,11 @@
 // counted, ten at a time, and then the ids.
 //
 // What bounds it.  Few rows: latency, some 25 steps of 500-3000 cycles (cluster barriers 700, a histogram's sums over the
-// cluster 4000): 8 rows of 32000 fp32, top-p 18.9 us; 15 rows of 128256 fp16, min-p 13.0; 64 rows of 151936 bf16, top-k
-// 50 and top-p 16.9.  Many rows: the issue of instructions between barriers (two blocks per SM; 49 % of the issue slots, HBM
-// 11 %): 256 rows of 151936 fp32 greedy 56 us, top-k 50 99, temperature alone 162, top-p at temperature 0.5 177, where most
-// rows are so flat that it takes exact weights 445; settings of their own 177.
+// cluster 4000), many of them code that runs once or twice: 8 rows of 32000 fp32, top-p 19.2 us (31 where a row takes exact weights, one call
+// of 27); 15 rows of 128256 fp16, min-p 13.1; 64 rows of 151936 bf16, top-k
+// 50 and top-p 16.8.  Many rows: the issue of instructions between barriers (two blocks per SM; 49 % of the issue slots, HBM
+// 11 %): 256 rows of 151936 fp32 greedy 45 us, top-k 50 93, temperature alone 162, top-p at temperature 0.5 170, where most
+// rows are so flat that it takes exact weights 440; settings of their own 178.
 #include <math.h>
 
 #include <atomic>
@@ -637,8 +640,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     // (the target is at most as much off as the sum that it is a part of)
     if (!exact && middle < 2 * (2 * rough_slack(above, depth) + rough_slack(sum - above, kZeroOctaves))) return false;   // it would hardly tell
     if (in_bin > (kFlat / 2) * middle) {   // many tokens: the bin's own bins
-
-      cluster_sync();   // the histogram before has been read
+      cluster_sync();   // (the histogram's own barriers would do)
       limits();
       histogram(
           [&](float x) {
@@ -677,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     uint32_t prefix = 0, mask = 0;
     for (int pass = 0; pass < 4; ++pass) {
       const int at = pass < 3 ? 22 - 10 * pass : 0, ones = pass < 3 ? 1023 : 3;
-      cluster_sync();   // the histogram before has been read
+      cluster_sync();   // (as above)
       int digit;
       histogram(
           [&](float x) {
@@ -765,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   }
   const float cut_k = cut;
   const int last_k = last;
-  // (also with few logits per thread: 8 rows of 32000 with top-p 18.9 us, weighed exactly at once 20.5)
+  // (also with few logits per thread: 8 rows of 32000 with top-p 19 us, weighed exactly at once 20.5 when this came in)
   if (rough && (top_p >= 1.0f || select(near_units, weight, nucleus, false)) && finish(near_units, false)) return;
   cut = cut_k;
   last = last_k;
