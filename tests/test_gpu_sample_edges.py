@@ -87,3 +87,16 @@ def test_sample_logprob_of_the_tail(v, below, dtype):
         assert bool((err <= 2.0 ** -19 + 2.0 ** -22 * want.abs()).all()), (k, p, m, err.tolist())
         tails += int((got > 0).sum())
     assert tails >= 6
+
+
+@pytest.mark.parametrize("T", [4e-39, 1e-41, 1.4e-45])
+@pytest.mark.parametrize("v,ties", [(301, 1), (5003, 40), (40000, 700)])
+def test_sample_coldest(T, v, ties):
+    """Where log2(e) / temperature is no float only tokens of the largest logit have a chance, and share it."""
+    x, u = spread_logits(12, v, F32, v)
+    for r in range(0, 12, 2):
+        x[r, torch.randperm(min(v, 2 * ties), generator=torch.Generator().manual_seed(r))[:ties]] = 30.0 if r < 6 else 0.0
+    x[6:, :] -= x[6:].max(dim=1, keepdim=True).values
+    for k, p, m in LIMITS:
+        got = sample_case(x, u, T, k, p, m)
+        assert bool((x.gather(1, got[:, None].long())[:, 0] == x.max(dim=1).values).all())
